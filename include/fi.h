@@ -253,6 +253,97 @@ FI_API const char* fi_last_error(void);
 FI_API fi_status fi_generate_noalloc(const fi_config* cfg, const void* h, int32_t n, const void* x0,
                                      const float* eps, float eps_scale, float* y_out, void* stream);
 
+/* ------------------------------------------------------------------ operators
+ * The layers that stand between the mixers of a hybrid stack, as calls of their
+ * own: linear attention (a mixer whose state has a fixed size) for prompts and
+ * for single tokens, and the linear layer. They need no context. Each runs
+ * asynchronously on `stream` (NULL = legacy default stream) on the current
+ * device, which must be the device of that stream and of every pointer; keeps
+ * no memory between calls; may be called from several threads and on several
+ * streams at once; and may be captured into a CUDA graph. Inputs are in
+ * cfg->dtype (FI_F32 or FI_BF16), sums and states in 32 bits. */
+
+/* Linear attention with one decay per head, for sequence b, head h:
+ *     S_t = g_h S_{t-1} + k_t v_t^T          (S: key_dim x value_dim, 32 bits)
+ *     o_t = R(scale * q_t^T S_t)             g_h = exp(log_decay[h])
+ * with R as above. Strides are in elements, between positions, sequences and
+ * heads ([0], [1], [2]); the innermost dimension is contiguous. q, k and v may
+ * be views (of one fused projection, say) and may have a stride of 0 (a
+ * position, sequence or head shared by all); o's elements must be distinct. */
+typedef struct {
+  int32_t heads;       /* H >= 1 */
+  int32_t key_dim;     /* 1..256 */
+  int32_t value_dim;   /* 1..256 */
+  int32_t batch;       /* B >= 1 */
+  int32_t dtype;       /* fi_dtype of q, k, v and o */
+  float scale;         /* finite */
+  int64_t q_stride[3]; /* position, sequence, head; >= 0 */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t o_stride[3];
+  int32_t reserved[4]; /* must be 0 */
+} fi_linattn_config;
+
+/* Device bytes of scratch that fi_linattn_prefill needs for n positions (may be
+ * 0). Depends on the sizes, strides, pointer alignment and the current device only.
+ * Errors: FI_E_INVALID, FI_E_CUDA. */
+FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t* bytes);
+
+/* A prompt of n positions (chunked form: matrix products inside chunks of
+ * positions, the state carried between them).
+ * log_decay: device [H] fp32, natural logarithms; values above 0 are taken as 0
+ *            (no decay), -infinity keeps nothing of the past.
+ * lengths:   NULL, or device [B] int32: sequence b has lengths[b] positions
+ *            (clamped to [0, n]); q, k and v behind them are not used, whatever
+ *            they hold, and o is left as it was there.
+ * state_in:  NULL (zeros) or device fp32 [B][H][key_dim][value_dim], the state
+ *            before position 0. state_out: NULL or the same, receives the state
+ *            after each sequence's last position (the state before, for an
+ *            empty sequence). The two may be the same buffer.
+ * workspace: device, 256-byte aligned, at least fi_linattn_workspace bytes; NULL
+ *            when that is 0. Calls that may overlap in time, replays of
+ *            captured graphs among them, need a workspace each.
+ * A q, k or v that is not finite at a used position makes outputs of its
+ * sequence and head non-finite from that position on, and may do so up to 127
+ * positions before it. n = 0 copies the state; n <= 2^30.
+ * Errors: FI_E_INVALID (NULL, sizes, strides, alignment, workspace too small),
+ * FI_E_CUDA. */
+FI_API fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
+                                    const float* log_decay, const int32_t* lengths, const float* state_in,
+                                    float* state_out, void* o, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* One position of every sequence (recurrent form): reads and updates
+ * state [B][H][key_dim][value_dim] (device, fp32) and writes o. q, k, v and o
+ * hold one position: stride [0] of each is not used.
+ * Errors: as fi_linattn_prefill. */
+FI_API fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const void* k, const void* v,
+                                 const float* log_decay, float* state, void* o, void* stream);
+
+typedef enum { FI_ACT_NONE = 0, FI_ACT_GELU = 1, FI_ACT_SILU = 2, FI_ACT_RELU = 3, FI_ACT_TANH = 4 } fi_act;
+
+/* y = R(act(x W^T + bias) + residual) over n rows, one rounding at the end.
+ * GELU is the exact form u Phi(u), as in fi_set_mlp_block. fp32 products are
+ * formed from operands split into three bf16 parts (24 bits). */
+typedef struct {
+  int32_t in_features;  /* 1..2^20 */
+  int32_t out_features; /* 1..2^20 */
+  int32_t dtype;        /* fi_dtype of x, w, bias, residual and y */
+  int32_t act;          /* fi_act */
+  int64_t ldx;          /* elements between rows of x [n][in]: >= in_features, or 0 (one row for all) */
+  int64_t ldw;          /* of w [out][in]: >= in_features */
+  int64_t ldr;          /* of residual [n][out]: >= out_features, or 0 (one row for all) */
+  int64_t ldy;          /* of y [n][out]: >= out_features */
+  int32_t reserved[4];  /* must be 0 */
+} fi_linear_config;
+
+/* bias: NULL or device [out]. residual: NULL or device [n][out]; it may be y
+ * itself (with ldr == ldy); y must not overlap x, w, bias or other rows of
+ * residual. n = 0 does nothing.
+ * Errors: FI_E_INVALID (NULL, sizes, leading dimensions, alignment, y == x),
+ * FI_E_CUDA. */
+FI_API fi_status fi_linear(const fi_linear_config* cfg, int32_t n, const void* x, const void* w, const void* bias,
+                           const void* residual, void* y, void* stream);
+
 /* Test hook: the number of barrier checks after which a device-side wait in
  * later fi_generate calls gives up (negative restores the default, about a
  * second of waiting). 0 makes every wait that is not already satisfied give up

@@ -5,7 +5,7 @@ this package only binds it. The binding (module `fi`) loads the library on first
 and raises if it has not been built: there is no fallback path.
 """
 _EXPORTS = ("Context", "FiError", "debug_fft", "status_str", "FI_F32", "FI_BF16", "KERNEL_CLASSES",
-            "EXPORTED", "LIB_PATH")
+            "EXPORTED", "LIB_PATH", "linattn_prefill", "linattn_step", "linear")
 
 
 def __getattr__(name):

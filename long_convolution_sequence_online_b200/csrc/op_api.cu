@@ -1,0 +1,172 @@
+// C-ABI of the context-free operators (declared in include/fi.h): argument
+// checks and launches.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "op_internal.cuh"
+
+using namespace fi;
+
+namespace {
+
+fi_status fail(fi_status s, const std::string& msg) {
+  set_last_error(msg);
+  return s;
+}
+fi_status invalid(const std::string& msg) { return fail(FI_E_INVALID, msg); }
+fi_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
+  return fail(FI_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Grids index sequences x heads in one dimension.
+constexpr int64_t kMaxRows = 65535;
+constexpr int32_t kMaxPositions = 1 << 30;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+// cfg -> s. `positions`: the number of positions the strides [0] step over (1:
+// not used).
+fi_status check_linattn(const fi_linattn_config* c, int64_t positions, LaShape* s) {
+  if (!c) return invalid("cfg is NULL");
+  if (c->heads < 1) return invalid("heads must be >= 1");
+  if (c->batch < 1) return invalid("batch must be >= 1");
+  if (c->key_dim < 1 || c->key_dim > 256) return invalid("key_dim must be in [1, 256]");
+  if (c->value_dim < 1 || c->value_dim > 256) return invalid("value_dim must be in [1, 256]");
+  if ((int64_t)c->heads * c->batch > kMaxRows) return invalid("batch x heads must be <= " + std::to_string(kMaxRows));
+  if (c->dtype != FI_F32 && c->dtype != FI_BF16) return invalid("dtype must be FI_F32 or FI_BF16");
+  if (!std::isfinite(c->scale)) return invalid("scale must be finite");
+  for (int r : c->reserved)
+    if (r != 0) return invalid("reserved fields must be 0");
+  for (int i = 0; i < 3; ++i)
+    for (int64_t v : {c->q_stride[i], c->k_stride[i], c->v_stride[i], c->o_stride[i]})
+      if (v < 0 || v > kMaxStride) return invalid("strides must be in [0, 2^40]");
+  // o's elements are distinct when, from the smallest stride up, each stride
+  // passes over the whole extent below it
+  struct Dim { int64_t stride, count; } d[3] = {{c->o_stride[0], positions}, {c->o_stride[1], c->batch}, {c->o_stride[2], c->heads}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = c->value_dim;
+  for (const Dim& x : d) {
+    if (x.count <= 1) continue;
+    if (x.stride < extent) return invalid("o_stride: rows of o overlap");
+    extent = x.stride * (x.count - 1) + extent;
+  }
+  *s = LaShape{};
+  s->H = c->heads;
+  s->dk = c->key_dim;
+  s->dv = c->value_dim;
+  s->B = c->batch;
+  s->bf16 = c->dtype == FI_BF16;
+  s->scale = c->scale;
+  for (int i = 0; i < 3; ++i) {
+    s->qs[i] = c->q_stride[i];
+    s->ks[i] = c->k_stride[i];
+    s->vs[i] = c->v_stride[i];
+    s->os[i] = c->o_stride[i];
+  }
+  return FI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t* bytes) {
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = 0;
+  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^30]");
+  LaShape s;
+  const fi_status r = check_linattn(cfg, n, &s);
+  if (r != FI_OK) return r;
+  if (n == 0) return FI_OK;
+  s.n = n;
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  *bytes = la_workspace_bytes(s, la_plan(s, sms));
+  return FI_OK;
+}
+
+fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
+                             const float* log_decay, const int32_t* lengths, const float* state_in, float* state_out,
+                             void* o, void* workspace, uint64_t workspace_bytes, void* stream) {
+  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^30]");
+  LaShape s;
+  const fi_status r = check_linattn(cfg, n, &s);
+  if (r != FI_OK) return r;
+  if (!log_decay || (n > 0 && (!q || !k || !v || !o))) return invalid("NULL argument");
+  const size_t esz = s.bf16 ? 2 : 4;
+  if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(log_decay, 4) ||
+      !aligned(lengths, 4) || !aligned(state_in, 4) || !aligned(state_out, 4))
+    return invalid("a pointer is not aligned to its element size");
+  s.n = n;
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const LaPlan p = la_plan(s, sms);
+  const size_t need = n > 0 ? la_workspace_bytes(s, p) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return invalid("workspace: " + std::to_string(need) + " bytes, 256-byte aligned, are needed");
+  const LaPtrs a{q, k, v, log_decay, lengths, state_in, state_out, o, need ? (float*)workspace : nullptr};
+  e = launch_linattn_prefill(s, p, a, (cudaStream_t)stream);
+  return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention prefill launch");
+}
+
+fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const void* k, const void* v,
+                          const float* log_decay, float* state, void* o, void* stream) {
+  LaShape s;
+  const fi_status r = check_linattn(cfg, 1, &s);
+  if (r != FI_OK) return r;
+  if (!q || !k || !v || !log_decay || !state || !o) return invalid("NULL argument");
+  const size_t esz = s.bf16 ? 2 : 4;
+  if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(log_decay, 4) ||
+      !aligned(state, 4))
+    return invalid("a pointer is not aligned to its element size");
+  s.n = 1;
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  e = launch_linattn_step(s, q, k, v, log_decay, state, o, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention step launch");
+}
+
+fi_status fi_linear(const fi_linear_config* c, int32_t n, const void* x, const void* w, const void* bias,
+                    const void* residual, void* y, void* stream) {
+  if (!c) return invalid("cfg is NULL");
+  if (n < 0) return invalid("n < 0");
+  if (c->in_features < 1 || c->in_features > (1 << 20)) return invalid("in_features must be in [1, 2^20]");
+  if (c->out_features < 1 || c->out_features > (1 << 20)) return invalid("out_features must be in [1, 2^20]");
+  if (c->dtype != FI_F32 && c->dtype != FI_BF16) return invalid("dtype must be FI_F32 or FI_BF16");
+  if (c->act < FI_ACT_NONE || c->act > FI_ACT_TANH) return invalid("act must be an fi_act");
+  for (int r : c->reserved)
+    if (r != 0) return invalid("reserved fields must be 0");
+  for (int64_t v : {c->ldx, c->ldw, c->ldr, c->ldy})
+    if (v < 0 || v > kMaxStride) return invalid("leading dimensions must be in [0, 2^40]");
+  if (c->ldx != 0 && c->ldx < c->in_features) return invalid("ldx must be >= in_features, or 0");
+  if (c->ldw < c->in_features) return invalid("ldw must be >= in_features");
+  if (c->ldy < c->out_features) return invalid("ldy must be >= out_features");
+  if (residual && c->ldr != 0 && c->ldr < c->out_features) return invalid("ldr must be >= out_features, or 0");
+  if (n == 0) return FI_OK;
+  if (!x || !w || !y) return invalid("NULL argument");
+  const size_t esz = c->dtype == FI_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || !aligned(w, esz) || !aligned(y, esz) || !aligned(bias, esz) || !aligned(residual, esz))
+    return invalid("a pointer is not aligned to its element size");
+  if (y == x || y == w || y == bias) return invalid("y must not be an input");
+  if (y == residual && c->ldr != c->ldy && n > 1) return invalid("residual may be y only with ldr == ldy");
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const LinShape s{n, c->in_features, c->out_features, c->dtype == FI_BF16, c->act, c->ldx, c->ldw, c->ldr, c->ldy};
+  e = launch_linear(s, x, w, bias, residual, y, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear layer launch");
+}
+
+}  // extern "C"

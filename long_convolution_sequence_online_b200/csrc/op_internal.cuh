@@ -1,0 +1,93 @@
+// Declarations of the context-free operators (linear attention, linear layer):
+// launchers in k_linattn.cu and k_linear.cu, argument checks and entry points
+// in op_api.cu.
+#pragma once
+
+#include "fi_internal.cuh"
+
+namespace fi {
+
+// ---------------------------------------------------------------- linear attention
+// Sizes and strides as in fi_linattn_config (strides in elements: position,
+// sequence, head), widened for address arithmetic.
+struct LaShape {
+  int H, dk, dv, B, n;
+  int bf16;
+  float scale;
+  int64_t qs[3], ks[3], vs[3], os[3];
+};
+
+// A prompt is cut into G segments of seg positions (a multiple of the chunk)
+// that run at the same time: a first launch forms every segment's own
+// contribution to the state, a second one adds up those before a segment and
+// computes its outputs. G = 1: one launch, no scratch.
+struct LaPlan {
+  int G, seg;
+};
+LaPlan la_plan(const LaShape& s, int num_sms);
+// Scratch of a plan: slot 0 of (sequence, head) holds the state before the
+// prompt, slot g the contribution of segment g - 1.
+inline size_t la_workspace_bytes(const LaShape& s, const LaPlan& p) {
+  return p.G > 1 ? (size_t)s.B * s.H * p.G * s.dk * s.dv * sizeof(float) : 0;
+}
+
+struct LaPtrs {
+  const void *q, *k, *v;
+  const float* log_decay;
+  const int32_t* lengths;   // NULL: all n
+  const float* state_in;    // NULL: zeros
+  float* state_out;         // NULL: not written
+  void* o;
+  float* ws;
+};
+cudaError_t launch_linattn_prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st);
+cudaError_t launch_linattn_step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay,
+                                float* state, void* o, int num_sms, cudaStream_t st);
+
+// The decay's exponent base 2 per position; log_decay above 0 counts as 0, and
+// -infinity becomes a finite value whose powers underflow to 0 (a lag of 0
+// still gives 1). NaN stays NaN.
+__device__ __forceinline__ float la_log2_decay(float log_decay) {
+  const float l = log_decay < -1e30f ? -1e30f : (log_decay > 0.f ? 0.f : log_decay);
+  return (float)((double)l * 1.4426950408889634);
+}
+// g^lag, lag >= 0.
+__device__ __forceinline__ float la_pow(float log2_decay, int lag) { return exp2f(log2_decay * (float)lag); }
+
+__device__ __forceinline__ int la_length(const int32_t* lengths, int b, int n) {
+  if (!lengths) return n;
+  const int l = __ldg(lengths + b);
+  return l < 0 ? 0 : (l > n ? n : l);
+}
+
+// ---------------------------------------------------------------- linear layer
+struct LinShape {
+  int n, K, N;      // rows, in_features, out_features
+  int bf16, act;
+  int64_t ldx, ldw, ldr, ldy;
+};
+cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
+                          void* y, int num_sms, cudaStream_t st);
+
+template <int ACT>
+__device__ __forceinline__ float linear_act(float u) {
+  if constexpr (ACT == FI_ACT_GELU) return 0.5f * u * (1.0f + erff(u * 0.70710678118654752f));
+  if constexpr (ACT == FI_ACT_SILU) return u / (1.0f + expf(-u));
+  if constexpr (ACT == FI_ACT_RELU) return u > 0.f || u != u ? u : 0.f;
+  if constexpr (ACT == FI_ACT_TANH) return tanhf(u);
+  return u;
+}
+
+// One value of a bf16 or fp32 array, and one rounded into it.
+template <typename T>
+__device__ __forceinline__ float op_load(const T* p) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
+  else return *p;
+}
+template <typename T>
+__device__ __forceinline__ void op_store(T* p, float v) {
+  if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(v);
+  else *p = v;
+}
+
+}  // namespace fi
