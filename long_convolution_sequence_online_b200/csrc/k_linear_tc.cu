@@ -1,0 +1,522 @@
+// Linear layer y = R(act(x W^T + bias) + residual) on the 5th-generation tensor
+// cores (tcgen05, accumulators in tensor memory).
+//
+// A persistent CTA per SM walks over output tiles of 128 rows x BN columns. The
+// contraction runs in blocks of 64: x and W tiles as K-major operands of
+// 128-byte rows in shared memory with the 128-byte swizzle, a ring of stages
+// between the producer and the one thread that issues the MMAs. Accumulators
+// are double buffered in tensor memory, so eight epilogue warps apply bias,
+// activation and residual to one tile while the next is multiplied.
+//
+// bf16 operands whose rows start at 16-byte boundaries come by TMA. Others, and
+// fp32 ones, are read by eight loader warps, which write the same layout:
+// fp32 values as three bf16 parts each, v = v0 + v1 + v2 (8 + 8 + 8 bits), and
+// the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 (the rest is below
+// 2^-24). The fp32 sums of many such products would pick up the tensor core's
+// rounding at every step, so each block of 64 gets an accumulator of its own
+// (smallest products first) and the epilogue warps add the blocks in registers.
+#include <mutex>
+
+#include "op_internal.cuh"
+#include "tc.cuh"
+
+namespace fi {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kEpiWarps = 8, kLoadWarps = 8;
+
+__device__ int g_linear_error;   // a bounded wait gave up since the last check
+
+// Stage of the ring: PARTS x (x tile 128 x 128 bytes, W tile BN x 128 bytes).
+template <int BN, int PARTS>
+constexpr int stage_bytes() { return PARTS * (kBM + BN) * 128; }
+template <int BN, int PARTS>
+constexpr int num_stages() { return PARTS == 3 ? 2 : (BN == 256 ? 4 : 6); }
+constexpr int kStagingLd = 33;
+constexpr int kStagingBytes = kEpiWarps * 32 * kStagingLd * 4;
+template <int BN, int PARTS>
+constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kStagingBytes; }
+
+struct LinTiles {
+  int mt, nt, group;   // row tiles, column tiles, row tiles per group
+  int64_t tiles;
+};
+
+// Tile order: groups of `group` row tiles, down the group's rows, then the next
+// column, so that the tiles at work together share rows and columns in L2.
+__device__ __forceinline__ void tile_at(const LinTiles& g, int64_t t, int& m, int& n) {
+  const int64_t per = (int64_t)g.group * g.nt;
+  const int gi = (int)(t / per);
+  const int r = (int)(t - gi * per);
+  const int rows = min(g.group, g.mt - gi * g.group);
+  n = r / rows;
+  m = gi * g.group + r - n * rows;
+}
+
+// act(acc + bias) + residual of 32 columns of a row per lane, to y. Vector form:
+// the lane stores its row's columns; otherwise through shared memory, so that
+// a warp's stores run along the columns.
+template <typename T, int ACT>
+__device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], const T* bias, const T* residual, T* y,
+                                            int64_t row0, int c0, bool vec, float* stg, int lane) {
+  if (c0 >= s.N) return;
+  if (bias) {
+    if (vec && c0 + 32 <= s.N) {
+      constexpr int E = 16 / sizeof(T);
+#pragma unroll
+      for (int u = 0; u < 32 / E; ++u) {
+        const uint4 b = __ldg(reinterpret_cast<const uint4*>(bias + c0) + u);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 2) {
+            v[u * 8 + 2 * e] += lo_f(w[e]);
+            v[u * 8 + 2 * e + 1] += hi_f(w[e]);
+          } else {
+            v[u * 4 + e] += __uint_as_float(w[e]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (c0 + e < s.N) v[e] += op_load(bias + c0 + e);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = linear_act<ACT>(v[e]);
+  if (vec && c0 + 32 <= s.N) {
+    const int64_t row = row0 + lane;
+    if (row >= s.n) return;
+    constexpr int E = 16 / sizeof(T);
+    T* yp = y + row * s.ldy + c0;
+    if (residual) {
+      const T* rp = residual + row * s.ldr + c0;
+#pragma unroll
+      for (int u = 0; u < 32 / E; ++u) {
+        const uint4 b = *(reinterpret_cast<const uint4*>(rp) + u);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 2) {
+            v[u * 8 + 2 * e] += lo_f(w[e]);
+            v[u * 8 + 2 * e + 1] += hi_f(w[e]);
+          } else {
+            v[u * 4 + e] += __uint_as_float(w[e]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 32 / E; ++u) {
+      uint4 o;
+      if constexpr (sizeof(T) == 2)
+        o = make_uint4(pack2(v[u * 8], v[u * 8 + 1]), pack2(v[u * 8 + 2], v[u * 8 + 3]),
+                       pack2(v[u * 8 + 4], v[u * 8 + 5]), pack2(v[u * 8 + 6], v[u * 8 + 7]));
+      else
+        o = make_uint4(__float_as_uint(v[u * 4]), __float_as_uint(v[u * 4 + 1]), __float_as_uint(v[u * 4 + 2]),
+                       __float_as_uint(v[u * 4 + 3]));
+      *(reinterpret_cast<uint4*>(yp) + u) = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) stg[lane * kStagingLd + e] = v[e];
+  __syncwarp();
+  const int c = c0 + lane;
+  if (c < s.N) {
+    const int rows = (int)min((int64_t)32, s.n - row0);
+    T* yp = y + row0 * s.ldy + c;
+    const T* rp = residual + row0 * s.ldr + c;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float w[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        w[r] = residual && r0 + r < rows ? op_load(rp + (int64_t)(r0 + r) * s.ldr) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r0 + r < rows) op_store(yp + (int64_t)(r0 + r) * s.ldy, stg[(r0 + r) * kStagingLd + lane] + w[r]);
+    }
+  }
+  __syncwarp();
+}
+
+// Loader warps: 8 consecutive elements (one 16-byte unit of a swizzled row) of
+// row `row` from column k; zeros outside.
+template <typename T>
+__device__ __forceinline__ void load8(const T* base, int64_t ld, int64_t row, int64_t rows, int k, int K, bool vec,
+                                      uint32_t (&raw)[4 * sizeof(T) / 2]) {
+  constexpr int W = 4 * sizeof(T) / 2;   // 32-bit words of 8 elements
+#pragma unroll
+  for (int i = 0; i < W; ++i) raw[i] = 0;
+  if (row >= rows || k >= K) return;
+  const T* p = base + row * ld + k;
+  if (vec && k + 8 <= K) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+    }
+    return;
+  }
+  const int m = min(8, K - k);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < m) {
+      if constexpr (sizeof(T) == 2)
+        raw[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) << (16 * (e & 1));
+      else
+        raw[e] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + e));
+    }
+}
+
+// BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32). TMA: operands by TMA.
+// Warps 0-7: epilogue (tensor-memory lanes 32 (w % 4) .. + 31, column half w / 4);
+// warp 8: MMA issuer; then one TMA warp or eight loader warps.
+template <int BN, int PARTS, bool TMA, typename T, int ACT>
+__global__ void __launch_bounds__(32 * (kEpiWarps + 1 + (TMA ? 1 : kLoadWarps)), 1)
+k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+            const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const T* residual, T* y,
+            int vec_load, int vec_store, int wait_limit) {
+  constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
+  constexpr int XB = kBM * 128, WB = BN * 128;
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ uint64_t full_bar[ST], empty_bar[ST], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  unsigned char* ring = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
+  float* staging = reinterpret_cast<float*>(ring + (size_t)ST * SB);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &abort_s;
+  if (warp == 0) tmem_alloc(&tmem_s, 2 * BN);
+  if (tid == 32) {
+    for (int i = 0; i < ST; ++i) {
+      bar_init(&full_bar[i], TMA ? 1 : kLoadWarps);
+      bar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&acc_full[i], 1);
+      bar_init(&acc_empty[i], kEpiWarps);
+    }
+    abort_s = 0;
+    bar_init_fence();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_s;
+  const int nk = (s.K + kBK - 1) / kBK;
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    atomicExch(&g_linear_error, 1);
+  };
+
+  if (warp < kEpiWarps) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = warp >> 2;
+    constexpr int CW = BN / 2;                     // columns of this warp
+    float* stg = staging + warp * 32 * kStagingLd;
+    uint32_t unit = 0;                             // accumulators drained
+    bool alive = true;
+    for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+      int m, n;
+      tile_at(g, t, m, n);
+      const int64_t row0 = (int64_t)m * kBM + 32 * q;
+      const int col0 = n * BN + half * CW;
+      const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + half * CW;
+      if constexpr (PARTS == 1) {
+        alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
+        if (!alive) break;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < CW; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(at + (unit & 1) * BN + c, r);
+          ld_wait();
+          if (c + 32 >= CW) {                      // all columns read: the MMA may overwrite them
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&acc_empty[unit & 1]);
+          }
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+          if (row0 < s.n) store_chunk<T, ACT>(s, v, bias, residual, y, row0, col0 + c, vec_store, stg, lane);
+        }
+        ++unit;
+      } else {
+        float acc[CW];
+#pragma unroll
+        for (int e = 0; e < CW; ++e) acc[e] = 0.f;
+        for (int kb = 0; kb < nk; ++kb, ++unit) {
+          alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
+          if (!alive) break;
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < CW; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(at + (unit & 1) * BN + c, r);
+            ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(r[e]);
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&acc_empty[unit & 1]);
+        }
+        if (!alive) break;
+#pragma unroll
+        for (int c = 0; c < CW; c += 32) {
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = acc[c + e];
+          if (row0 < s.n) store_chunk<T, ACT>(s, v, bias, residual, y, row0, col0 + c, vec_store, stg, lane);
+        }
+      }
+    }
+    if (!alive && lane == 0) give_up();
+  } else if (warp == kEpiWarps) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc(kBM, BN);
+      uint32_t kbs = 0, unit = 0;
+      bool alive = true;
+      for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+        for (int kb = 0; kb < nk; ++kb, ++kbs) {
+          const int st = kbs % ST;
+          if (PARTS > 1 || kb == 0) {
+            if (unit >= 2 && !bar_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag)) {
+              alive = false;
+              break;
+            }
+          }
+          if (!bar_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag)) {
+            alive = false;
+            break;
+          }
+          fence_after();
+          const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + PARTS * XB;
+          const uint32_t d = tmem + (unit & 1) * BN;
+          if constexpr (PARTS == 1) {
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) mma(d, desc_k(xa + 32 * k), desc_k(wa + 32 * k), id, kb > 0 || k > 0);
+          } else {
+            constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
+#pragma unroll
+            for (int p = 0; p < 6; ++p)
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)
+                mma(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
+          }
+          commit(&empty_bar[st]);
+          if (PARTS > 1 || kb == nk - 1) {
+            commit(&acc_full[unit & 1]);
+            ++unit;
+          }
+        }
+      }
+      if (!alive) give_up();
+      // shared and tensor memory are released only once the last MMAs are done
+      if (kbs > 0) bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDefaultWaitLimit);
+    }
+    __syncwarp();
+  } else if constexpr (TMA) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch(&xmap);
+      tma_prefetch(&wmap);
+      uint32_t kbs = 0;
+      bool alive = true;
+      for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+        int m, n;
+        tile_at(g, t, m, n);
+        for (int kb = 0; kb < nk; ++kb, ++kbs) {
+          const int st = kbs % ST;
+          if (kbs >= ST && !bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag)) {
+            alive = false;
+            break;
+          }
+          unsigned char* dst = ring + (size_t)st * SB;
+          bar_expect(&full_bar[st], SB);
+          tma_2d(dst, &xmap, &full_bar[st], kb * kBK, m * kBM);
+          tma_2d(dst + XB, &wmap, &full_bar[st], kb * kBK, n * BN);
+        }
+      }
+      if (!alive) give_up();
+      // no copy of this CTA may still be in flight when it ends
+      for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&full_bar[i % ST], (i / ST) & 1, kDefaultWaitLimit);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ loader warps
+    constexpr int W = 4 * sizeof(T) / 2, UX = kBM / 32, UW = BN / 32;
+    const int lt = tid - 32 * (kEpiWarps + 1);     // 0..255
+    const int unit8 = lt & 7, r0 = lt >> 3;        // 16-byte unit of a row, first row
+    uint32_t kbs = 0;
+    bool alive = true;
+    for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+      int m, n;
+      tile_at(g, t, m, n);
+      for (int kb = 0; kb < nk; ++kb, ++kbs) {
+        const int st = kbs % ST, k = kb * kBK + 8 * unit8;
+        uint32_t raw[UX + UW][W];
+#pragma unroll
+        for (int u = 0; u < UX; ++u)
+          load8<T>(x, s.ldx, (int64_t)m * kBM + r0 + 32 * u, s.n, k, s.K, vec_load & 1, raw[u]);
+#pragma unroll
+        for (int u = 0; u < UW; ++u)
+          load8<T>(w, s.ldw, (int64_t)n * BN + r0 + 32 * u, s.N, k, s.K, vec_load & 2, raw[UX + u]);
+        alive = __all_sync(0xffffffffu,
+                           kbs < ST || bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag));
+        if (!alive) break;
+        unsigned char* dst = ring + (size_t)st * SB;
+#pragma unroll
+        for (int u = 0; u < UX + UW; ++u) {
+          const int r = r0 + 32 * (u < UX ? u : u - UX);
+          unsigned char* tile = dst + (u < UX ? 0 : PARTS * XB);
+          constexpr int xb = XB, wb = WB;
+          const int step = u < UX ? xb : wb;       // to the next part's tile
+          const uint32_t off = (uint32_t)r * 128 + ((unit8 ^ (r & 7)) << 4);
+          if constexpr (PARTS == 1) {
+            *reinterpret_cast<uint4*>(tile + off) = make_uint4(raw[u][0], raw[u][1], raw[u][2], raw[u][3]);
+          } else {
+            uint32_t p[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              split3(__uint_as_float(raw[u][2 * e]), __uint_as_float(raw[u][2 * e + 1]), p[0][e], p[1][e], p[2][e]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              *reinterpret_cast<uint4*>(tile + i * step + off) = make_uint4(p[i][0], p[i][1], p[i][2], p[i][3]);
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&full_bar[st]);
+      }
+    }
+    if (!alive && lane == 0) give_up();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) tmem_free(tmem, 2 * BN);
+}
+
+// The dynamic shared-memory cap is one value per kernel for the whole process:
+// raised when a call needs more, never lowered.
+template <class Kern>
+cudaError_t raise_cap(Kern kernel, size_t smem) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  cudaFuncAttributes fa{};
+  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e != cudaSuccess || (size_t)fa.maxDynamicSharedSizeBytes >= smem) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+struct LinCall {
+  const LinShape& s;
+  const void *x, *w, *bias, *residual;
+  void* y;
+  int num_sms;
+  cudaStream_t st;
+};
+
+bool aligned16(const void* p, int64_t ld, int64_t rows, size_t esz) {
+  return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (ld * (int64_t)esz) % 16 == 0);
+}
+
+bool map_rows(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t strides[1] = {rows > 1 ? (uint64_t)ld * 2 : (uint64_t)((cols + 7) / 8 * 16)};
+  const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)box_rows};
+  return encode_map(map, p, 2, dims, strides, box);
+}
+
+template <int BN, int PARTS, bool TMA, typename T, int ACT>
+cudaError_t run(const LinCall& c) {
+  const LinShape& s = c.s;
+  auto kern = k_linear_tc<BN, PARTS, TMA, T, ACT>;
+  constexpr size_t smem = smem_bytes<BN, PARTS>();
+  cudaError_t e = raise_cap(kern, smem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap xmap{}, wmap{};
+  if (TMA && (!map_rows(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !map_rows(&wmap, c.w, s.N, s.K, s.ldw, BN)))
+    return cudaErrorInvalidValue;
+  LinTiles g{};
+  g.mt = (int)(((int64_t)s.n + kBM - 1) / kBM);
+  g.nt = (s.N + BN - 1) / BN;
+  g.group = g.mt < 16 ? g.mt : 16;
+  g.tiles = (int64_t)g.mt * g.nt;
+  const int vec_load = (aligned16(c.x, s.ldx, s.n, sizeof(T)) ? 1 : 0) | (aligned16(c.w, s.ldw, s.N, sizeof(T)) ? 2 : 0);
+  const int vec_store = aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
+                        (!c.residual || aligned16(c.residual, s.ldr, s.n, sizeof(T)));
+  const int grid = (int)(g.tiles < c.num_sms ? g.tiles : c.num_sms);
+  constexpr int threads = 32 * (kEpiWarps + 1 + (TMA ? 1 : kLoadWarps));
+  kern<<<grid, threads, smem, c.st>>>(s, g, xmap, wmap, (const T*)c.x, (const T*)c.w, (const T*)c.bias,
+                                      (const T*)c.residual, (T*)c.y, vec_load, vec_store, kDefaultWaitLimit);
+  return cudaGetLastError();
+}
+
+template <int BN, int PARTS, bool TMA, typename T>
+cudaError_t run_act(const LinCall& c) {
+  switch (c.s.act) {
+    case FI_ACT_NONE: return run<BN, PARTS, TMA, T, FI_ACT_NONE>(c);
+    case FI_ACT_GELU: return run<BN, PARTS, TMA, T, FI_ACT_GELU>(c);
+    case FI_ACT_SILU: return run<BN, PARTS, TMA, T, FI_ACT_SILU>(c);
+    case FI_ACT_RELU: return run<BN, PARTS, TMA, T, FI_ACT_RELU>(c);
+    case FI_ACT_TANH: return run<BN, PARTS, TMA, T, FI_ACT_TANH>(c);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+bool encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+  using Fn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                          const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                          CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Fn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (Fn)p;
+  }();
+  if (!fn) return false;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
+                          void* y, int num_sms, cudaStream_t st) {
+  const LinCall c{s, x, w, bias, residual, y, num_sms, st};
+  if (!s.bf16) return run_act<128, 3, false, float>(c);
+  // a row stride of 0 (one row of x for all) is no tensor-map stride
+  if (!aligned16(x, s.ldx, s.n, 2) || !aligned16(w, s.ldw, s.N, 2) || (s.ldx == 0 && s.n > 1))
+    return run_act<128, 1, false, __nv_bfloat16>(c);
+  const int64_t mt = ((int64_t)s.n + kBM - 1) / kBM;
+  if (mt * ((s.N + 255) / 256) >= num_sms) return run_act<256, 1, true, __nv_bfloat16>(c);
+  return run_act<128, 1, true, __nv_bfloat16>(c);
+}
+
+cudaError_t linear_take_error(cudaStream_t st, int* flag) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_linear_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && *flag) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_linear_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
+  return e;
+}
+
+}  // namespace fi
