@@ -1,15 +1,19 @@
 // Linear layer y = R(act(x W^T + bias) + residual) on the 5th-generation tensor
 // cores (tcgen05, accumulators in tensor memory).
 //
-// A persistent CTA per SM walks over output tiles of 128 rows x BN columns. The
-// contraction runs in blocks of 64: x and W tiles as K-major operands of
+// A persistent CTA (or pair of CTAs on neighbouring SMs) per SM walks over output
+// tiles of 128 (256) rows x BN columns. The contraction runs in blocks of 64: x and W tiles as K-major operands of
 // 128-byte rows in shared memory with the 128-byte swizzle, a ring of stages
 // between the producer and the one thread that issues the MMAs. Accumulators
 // are double buffered in tensor memory, so eight epilogue warps apply bias,
 // activation and residual to one tile while the next is multiplied.
 //
-// bf16 operands whose rows start at 16-byte boundaries come by TMA. Others, and
-// fp32 ones, are read by eight loader warps, which write the same layout:
+// bf16 operands whose rows start at 16-byte boundaries come by TMA into pairs of
+// CTAs that share each MMA (cta_group::2): each CTA holds its 128 rows of x and
+// half of the W tile, which halves the W traffic from L2. A lone CTA per tile of
+// 128 x 256 reads 96 bytes per clock and SM at the full MMA rate, more than L2
+// delivers: 496 us at n = 16384, 2048 -> 8192, against PAIR_US for pairs.
+// Other operands, and fp32 ones, are read by eight loader warps, which write the same layout:
 // fp32 values as three bf16 parts each, v = v0 + v1 + v2 (8 + 8 + 8 bits), and
 // the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 (the rest is below
 // 2^-24). The fp32 sums of many such products would pick up the tensor core's
@@ -31,27 +35,30 @@ constexpr int kEpiWarps = 8, kLoadWarps = 8;
 
 __device__ int g_linear_error;   // a bounded wait gave up since the last check
 
-// Stage of the ring: PARTS x (x tile 128 x 128 bytes, W tile BN x 128 bytes).
-template <int BN, int PARTS>
-constexpr int stage_bytes() { return PARTS * (kBM + BN) * 128; }
-template <int BN, int PARTS>
-constexpr int num_stages() { return PARTS == 3 ? 2 : (BN == 256 ? 4 : 6); }
+// Stage of the ring: `units` x (x tile 128 x 128 bytes, W tile BW x 128 bytes), BW
+// the W rows a CTA holds: BN, or half of them in a pair. The units are the parts
+// of fp32 values, or (pairs) two blocks of the contraction: a stage's waits and
+// signals take 350 to 450 cycles whatever its size, more than the 264 that the
+// MMAs of one block take at BN = 128.
+constexpr int kPairBlocks = 2;
+template <int BW, int UNITS>
+constexpr int stage_bytes() { return UNITS * (kBM + BW) * 128; }
+template <int BW, int UNITS>
+constexpr int num_stages() { return 196608 / stage_bytes<BW, UNITS>(); }
 constexpr int kStagingLd = 33;
 constexpr int kStagingBytes = kEpiWarps * 32 * kStagingLd * 4;
-template <int BN, int PARTS>
-constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kStagingBytes; }
+template <int BW, int UNITS>
+constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BW, UNITS>() * stage_bytes<BW, UNITS>() + kStagingBytes; }
 
 struct LinTiles {
   int mt, nt, group;   // row tiles, column tiles, row tiles per group
-  int64_t tiles;
+  int tiles;           // fewer than 2^31: y has at most 2^40 elements
 };
 
 // Tile order: groups of `group` row tiles, down the group's rows, then the next
 // column, so that the tiles at work together share rows and columns in L2.
-__device__ __forceinline__ void tile_at(const LinTiles& g, int64_t t, int& m, int& n) {
-  const int64_t per = (int64_t)g.group * g.nt;
-  const int gi = (int)(t / per);
-  const int r = (int)(t - gi * per);
+__device__ __forceinline__ void tile_at(const LinTiles& g, int t, int& m, int& n) {
+  const int per = g.group * g.nt, gi = t / per, r = t - gi * per;
   const int rows = min(g.group, g.mt - gi * g.group);
   n = r / rows;
   m = gi * g.group + r - n * rows;
@@ -88,7 +95,7 @@ __device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], c
     }
   }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = linear_act<ACT>(v[e]);
+  for (int e = 0; e < 32; ++e) v[e] = sizeof(T) == 2 ? linear_act_bf16<ACT>(v[e]) : linear_act<ACT>(v[e]);
   if (vec && c0 + 32 <= s.N) {
     const int64_t row = row0 + lane;
     if (row >= s.n) return;
@@ -174,16 +181,20 @@ __device__ __forceinline__ void load8(const T* base, int64_t ld, int64_t row, in
     }
 }
 
-// BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32). TMA: operands by TMA.
+// BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32). PAIR: operands by TMA, two
+// CTAs per tile of 256 rows.
 // Warps 0-7: epilogue (tensor-memory lanes 32 (w % 4) .. + 31, column half w / 4);
 // warp 8: MMA issuer; then one TMA warp or eight loader warps.
-template <int BN, int PARTS, bool TMA, typename T, int ACT>
-__global__ void __launch_bounds__(32 * (kEpiWarps + 1 + (TMA ? 1 : kLoadWarps)), 1)
+template <int BN, int PARTS, bool PAIR, typename T, int ACT>
+__global__ void __launch_bounds__(32 * (kEpiWarps + 1 + (PAIR ? 1 : kLoadWarps)), 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
             const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const T* residual, T* y,
             int vec_load, int vec_store, int wait_limit) {
-  constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
-  constexpr int XB = kBM * 128, WB = BN * 128;
+  constexpr int BW = PAIR ? BN / 2 : BN;           // W rows in this CTA's stages
+  constexpr int KS = PAIR ? kPairBlocks : 1, UNITS = PARTS * KS;
+  constexpr int ST = num_stages<BW, UNITS>(), SB = stage_bytes<BW, UNITS>();
+  constexpr int XB = kBM * 128, WB = BW * 128;
+  constexpr int TM = PAIR ? 2 * kBM : kBM;         // rows of a tile
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t full_bar[ST], empty_bar[ST], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_s;
@@ -192,24 +203,36 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   float* staging = reinterpret_cast<float*>(ring + (size_t)ST * SB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &abort_s;
-  if (warp == 0) tmem_alloc(&tmem_s, 2 * BN);
+  pdl_launch_dependents();
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+  if (warp == 0) {
+    if constexpr (PAIR) tmem_alloc2(&tmem_s, 2 * BN);
+    else tmem_alloc(&tmem_s, 2 * BN);
+  }
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
-      bar_init(&full_bar[i], TMA ? 1 : kLoadWarps);
+      bar_init(&full_bar[i], PAIR ? 1 : kLoadWarps);
       bar_init(&empty_bar[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&acc_full[i], 1);
-      bar_init(&acc_empty[i], kEpiWarps);
+      bar_init(&acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     abort_s = 0;
     bar_init_fence();
   }
   fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  else __syncthreads();
   fence_after();
+  pdl_wait_primary();                              // from here on inputs are read and y is written
   const uint32_t tmem = tmem_s;
-  const int nk = (s.K + kBK - 1) / kBK;
+  const int nk = (s.K + KS * kBK - 1) / (KS * kBK);   // stages per tile
+  auto acc_release = [&](uint32_t unit) {          // one warp has read the accumulator
+    if constexpr (PAIR) bar_arrive_leader(&acc_empty[unit & 1]);
+    else bar_arrive(&acc_empty[unit & 1]);
+  };
   auto give_up = [&]() {
     *abort_flag = 1;
     atomicExch(&g_linear_error, 1);
@@ -222,17 +245,17 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     float* stg = staging + warp * 32 * kStagingLd;
     uint32_t unit = 0;                             // accumulators drained
     bool alive = true;
-    for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+    for (int t = first; t < g.tiles && alive; t += stride) {
       int m, n;
       tile_at(g, t, m, n);
-      const int64_t row0 = (int64_t)m * kBM + 32 * q;
+      const int64_t row0 = (int64_t)m * TM + rank * kBM + 32 * q;
       const int col0 = n * BN + half * CW;
       const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + half * CW;
       if constexpr (PARTS == 1) {
         alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
         if (!alive) break;
         fence_after();
-#pragma unroll
+#pragma unroll 1                                   // straight-line code would be fetched once per launch
         for (int c = 0; c < CW; c += 32) {
           uint32_t r[32];
           tmem_ld32(at + (unit & 1) * BN + c, r);
@@ -240,7 +263,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
           if (c + 32 >= CW) {                      // all columns read: the MMA may overwrite them
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&acc_empty[unit & 1]);
+            if (lane == 0) acc_release(unit);
           }
           float v[32];
 #pragma unroll
@@ -266,7 +289,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
           }
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&acc_empty[unit & 1]);
+          if (lane == 0) acc_release(unit);
         }
         if (!alive) break;
 #pragma unroll
@@ -281,76 +304,86 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     if (!alive && lane == 0) give_up();
   } else if (warp == kEpiWarps) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc(kBM, BN);
+    if (rank == 0) {
+      constexpr uint32_t id = idesc(TM, BN);
+      const bool issuer = elect_one();
       uint32_t kbs = 0, unit = 0;
       bool alive = true;
-      for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+      for (int t = first; t < g.tiles && alive; t += stride) {
         for (int kb = 0; kb < nk; ++kb, ++kbs) {
           const int st = kbs % ST;
-          if (PARTS > 1 || kb == 0) {
-            if (unit >= 2 && !bar_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag)) {
-              alive = false;
-              break;
+          if (PARTS > 1 || kb == 0)
+            alive = unit < 2 || bar_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
+          alive = __all_sync(0xffffffffu, alive && bar_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag));
+          if (!alive) break;
+          fence_after();
+          const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + UNITS * XB;
+          const uint32_t d = tmem + (unit & 1) * BN;
+          const bool last = PARTS > 1 || kb == nk - 1;
+          if (issuer) {
+            if constexpr (PARTS == 1) {
+              const int steps = min(KS * kBK / 16, (s.K - kb * KS * kBK + 15) / 16);   // of 16
+#pragma unroll
+              for (int k = 0; k < KS * kBK / 16; ++k) {
+                if (k >= steps) break;
+                const uint32_t xo = (k / 4) * XB + (k % 4) * 32, wo = (k / 4) * WB + (k % 4) * 32;
+                if constexpr (PAIR) mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
+                else mma(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
+              }
+            } else {
+              constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
+#pragma unroll
+              for (int p = 0; p < 6; ++p)
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                  mma(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
+            }
+            if constexpr (PAIR) commit2(&empty_bar[st]);
+            else commit(&empty_bar[st]);
+            if (last) {
+              if constexpr (PAIR) commit2(&acc_full[unit & 1]);
+              else commit(&acc_full[unit & 1]);
             }
           }
-          if (!bar_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag)) {
-            alive = false;
-            break;
-          }
-          fence_after();
-          const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + PARTS * XB;
-          const uint32_t d = tmem + (unit & 1) * BN;
-          if constexpr (PARTS == 1) {
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) mma(d, desc_k(xa + 32 * k), desc_k(wa + 32 * k), id, kb > 0 || k > 0);
-          } else {
-            constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
-#pragma unroll
-            for (int p = 0; p < 6; ++p)
-#pragma unroll
-              for (int k = 0; k < kBK / 16; ++k)
-                mma(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
-          }
-          commit(&empty_bar[st]);
-          if (PARTS > 1 || kb == nk - 1) {
-            commit(&acc_full[unit & 1]);
-            ++unit;
-          }
+          __syncwarp();
+          if (last) ++unit;
         }
       }
-      if (!alive) give_up();
+      if (!alive && lane == 0) give_up();
       // shared and tensor memory are released only once the last MMAs are done
       if (kbs > 0) bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDefaultWaitLimit);
     }
     __syncwarp();
-  } else if constexpr (TMA) {
+  } else if constexpr (PAIR) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      tma_prefetch(&xmap);
-      tma_prefetch(&wmap);
-      uint32_t kbs = 0;
-      bool alive = true;
-      for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
-        int m, n;
-        tile_at(g, t, m, n);
-        for (int kb = 0; kb < nk; ++kb, ++kbs) {
-          const int st = kbs % ST;
-          if (kbs >= ST && !bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag)) {
-            alive = false;
-            break;
-          }
+    const bool issuer = elect_one();
+    uint32_t kbs = 0;
+    bool alive = true;
+    for (int t = first; t < g.tiles && alive; t += stride) {
+      int m, n;
+      tile_at(g, t, m, n);
+      for (int kb = 0; kb < nk; ++kb, ++kbs) {
+        const int st = kbs % ST, k = kb * KS * kBK;
+        alive = __all_sync(0xffffffffu,
+                           kbs < ST || bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag));
+        if (!alive) break;
+        if (issuer) {
           unsigned char* dst = ring + (size_t)st * SB;
-          bar_expect(&full_bar[st], SB);
-          tma_2d(dst, &xmap, &full_bar[st], kb * kBK, m * kBM);
-          tma_2d(dst + XB, &wmap, &full_bar[st], kb * kBK, n * BN);
+          const int blocks = min(KS, (s.K - k + kBK - 1) / kBK);
+          if (rank == 0) bar_expect(&full_bar[st], 2 * blocks * (XB + WB));   // both CTAs' tiles
+#pragma unroll
+          for (int u = 0; u < KS; ++u)
+            if (u < blocks) {
+              tma_2d_pair(dst + u * XB, &xmap, &full_bar[st], k + u * kBK, m * TM + rank * kBM);
+              tma_2d_pair(dst + UNITS * XB + u * WB, &wmap, &full_bar[st], k + u * kBK, n * BN + rank * BW);
+            }
         }
+        __syncwarp();
       }
-      if (!alive) give_up();
-      // no copy of this CTA may still be in flight when it ends
-      for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&full_bar[i % ST], (i / ST) & 1, kDefaultWaitLimit);
     }
-    __syncwarp();
+    if (!alive && lane == 0) give_up();
+    // no copy of this CTA may still be in flight when it ends: each stage's last use is done
+    for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDefaultWaitLimit);
   } else {
     // ------------------------------------------------------------ loader warps
     constexpr int W = 4 * sizeof(T) / 2, UX = kBM / 32, UW = BN / 32;
@@ -358,7 +391,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     const int unit8 = lt & 7, r0 = lt >> 3;        // 16-byte unit of a row, first row
     uint32_t kbs = 0;
     bool alive = true;
-    for (int64_t t = blockIdx.x; t < g.tiles && alive; t += gridDim.x) {
+    for (int t = first; t < g.tiles && alive; t += stride) {
       int m, n;
       tile_at(g, t, m, n);
       for (int kb = 0; kb < nk; ++kb, ++kbs) {
@@ -401,9 +434,13 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     if (!alive && lane == 0) give_up();
   }
   fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_relaxed();      // neither CTA ends while the other may still signal it
+  else __syncthreads();
   fence_after();
-  if (warp == 0) tmem_free(tmem, 2 * BN);
+  if (warp == 0) {
+    if constexpr (PAIR) tmem_free2(tmem, 2 * BN);
+    else tmem_free(tmem, 2 * BN);
+  }
 }
 
 // The dynamic shared-memory cap is one value per kernel for the whole process:
@@ -437,39 +474,55 @@ bool map_rows(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
   return encode_map(map, p, 2, dims, strides, box);
 }
 
-template <int BN, int PARTS, bool TMA, typename T, int ACT>
+template <int BN, int PARTS, bool PAIR, typename T, int ACT>
 cudaError_t run(const LinCall& c) {
   const LinShape& s = c.s;
-  auto kern = k_linear_tc<BN, PARTS, TMA, T, ACT>;
-  constexpr size_t smem = smem_bytes<BN, PARTS>();
+  auto kern = k_linear_tc<BN, PARTS, PAIR, T, ACT>;
+  constexpr int BW = PAIR ? BN / 2 : BN, TM = PAIR ? 2 * kBM : kBM;
+  constexpr size_t smem = smem_bytes<BW, PARTS * (PAIR ? kPairBlocks : 1)>();
   cudaError_t e = raise_cap(kern, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap{}, wmap{};
-  if (TMA && (!map_rows(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !map_rows(&wmap, c.w, s.N, s.K, s.ldw, BN)))
+  if (PAIR && (!map_rows(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !map_rows(&wmap, c.w, s.N, s.K, s.ldw, BW)))
     return cudaErrorInvalidValue;
   LinTiles g{};
-  g.mt = (int)(((int64_t)s.n + kBM - 1) / kBM);
+  g.mt = (int)(((int64_t)s.n + TM - 1) / TM);
   g.nt = (s.N + BN - 1) / BN;
-  g.group = g.mt < 16 ? g.mt : 16;
-  g.tiles = (int64_t)g.mt * g.nt;
+  g.group = g.mt < 2048 / TM ? g.mt : 2048 / TM;
+  g.tiles = g.mt * g.nt;
   const int vec_load = (aligned16(c.x, s.ldx, s.n, sizeof(T)) ? 1 : 0) | (aligned16(c.w, s.ldw, s.N, sizeof(T)) ? 2 : 0);
   const int vec_store = aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
                         (!c.residual || aligned16(c.residual, s.ldr, s.n, sizeof(T)));
-  const int grid = (int)(g.tiles < c.num_sms ? g.tiles : c.num_sms);
-  constexpr int threads = 32 * (kEpiWarps + 1 + (TMA ? 1 : kLoadWarps));
-  kern<<<grid, threads, smem, c.st>>>(s, g, xmap, wmap, (const T*)c.x, (const T*)c.w, (const T*)c.bias,
-                                      (const T*)c.residual, (T*)c.y, vec_load, vec_store, kDefaultWaitLimit);
-  return cudaGetLastError();
+  const int slots = PAIR ? c.num_sms / 2 : c.num_sms;
+  const int ctas = (g.tiles < slots ? g.tiles : slots) * (PAIR ? 2 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(32 * (kEpiWarps + 1 + (PAIR ? 1 : kLoadWarps)));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.st;
+  if (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.x, (const T*)c.w, (const T*)c.bias,
+                            (const T*)c.residual, (T*)c.y, vec_load, vec_store, (int)kDefaultWaitLimit);
 }
 
-template <int BN, int PARTS, bool TMA, typename T>
+template <int BN, int PARTS, bool PAIR, typename T>
 cudaError_t run_act(const LinCall& c) {
   switch (c.s.act) {
-    case FI_ACT_NONE: return run<BN, PARTS, TMA, T, FI_ACT_NONE>(c);
-    case FI_ACT_GELU: return run<BN, PARTS, TMA, T, FI_ACT_GELU>(c);
-    case FI_ACT_SILU: return run<BN, PARTS, TMA, T, FI_ACT_SILU>(c);
-    case FI_ACT_RELU: return run<BN, PARTS, TMA, T, FI_ACT_RELU>(c);
-    case FI_ACT_TANH: return run<BN, PARTS, TMA, T, FI_ACT_TANH>(c);
+    case FI_ACT_NONE: return run<BN, PARTS, PAIR, T, FI_ACT_NONE>(c);
+    case FI_ACT_GELU: return run<BN, PARTS, PAIR, T, FI_ACT_GELU>(c);
+    case FI_ACT_SILU: return run<BN, PARTS, PAIR, T, FI_ACT_SILU>(c);
+    case FI_ACT_RELU: return run<BN, PARTS, PAIR, T, FI_ACT_RELU>(c);
+    case FI_ACT_TANH: return run<BN, PARTS, PAIR, T, FI_ACT_TANH>(c);
   }
   return cudaErrorInvalidValue;
 }
@@ -503,8 +556,8 @@ cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const
   // a row stride of 0 (one row of x for all) is no tensor-map stride
   if (!aligned16(x, s.ldx, s.n, 2) || !aligned16(w, s.ldw, s.N, 2) || (s.ldx == 0 && s.n > 1))
     return run_act<128, 1, false, __nv_bfloat16>(c);
-  const int64_t mt = ((int64_t)s.n + kBM - 1) / kBM;
-  if (mt * ((s.N + 255) / 256) >= num_sms) return run_act<256, 1, true, __nv_bfloat16>(c);
+  const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM);
+  if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, true, __nv_bfloat16>(c);
   return run_act<128, 1, true, __nv_bfloat16>(c);
 }
 

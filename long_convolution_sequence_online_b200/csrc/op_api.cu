@@ -154,6 +154,7 @@ fi_status fi_linear(const fi_linear_config* c, int32_t n, const void* x, const v
   if (c->ldw < c->in_features) return invalid("ldw must be >= in_features");
   if (c->ldy < c->out_features) return invalid("ldy must be >= out_features");
   if (residual && c->ldr != 0 && c->ldr < c->out_features) return invalid("ldr must be >= out_features, or 0");
+  if ((int64_t)n * c->out_features > kMaxStride) return invalid("n x out_features must be <= 2^40");
   if (n == 0) return FI_OK;
   if (!x || !w || !y) return invalid("NULL argument");
   const size_t esz = c->dtype == FI_BF16 ? 2 : 4;

@@ -78,6 +78,47 @@ __device__ __forceinline__ float linear_act(float u) {
   return u;
 }
 
+// The same for results that are rounded to bf16: within 1e-6 of the value, in
+// fewer instructions (a tile's activations otherwise take as long as its
+// products). GELU: u Phi(u) from the tail Phi(-z) = exp(-z^2/2) t Q(t),
+// t = 1 / (1 + 0.265 z), z = |u|; Q is a least-maximum fit of degree 6 made for
+// this form (relative error 6.3e-7 for z up to 14, where the tail is 8e-45).
+// tanh: its series below 0.2, (1 - e) / (1 + e) with e = exp(-2 |u|) above.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int ACT>
+__device__ __forceinline__ float linear_act_bf16(float u) {
+  if constexpr (ACT == FI_ACT_GELU) {
+    const float z = fminf(fabsf(u), 14.f);
+    const float t = rcp_fast(fmaf(0.265f, z, 1.f));
+    float p = fmaf(-0.06778856f, t, 0.1952782f);
+    p = fmaf(p, t, -0.06636963f);
+    p = fmaf(p, t, 0.14249772f);
+    p = fmaf(p, t, 0.08294514f);
+    p = fmaf(p, t, 0.107837f);
+    p = fmaf(p, t, 0.10559982f);
+    const float tail = z * (p * t) * ex2_fast(z * z * -0.72134752f);
+    return u > 0.f ? u - tail : (u <= 0.f ? -tail : u);   // NaN stays
+  }
+  if constexpr (ACT == FI_ACT_SILU) return __fdividef(u, 1.0f + __expf(-u));
+  if constexpr (ACT == FI_ACT_TANH) {
+    const float z = fabsf(u), z2 = z * z;
+    const float e = ex2_fast(z * -2.8853900817779268f);
+    const float big = (1.f - e) * rcp_fast(1.f + e);
+    const float small = z * fmaf(z2, fmaf(z2, fmaf(z2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+    return copysignf(z < 0.2f ? small : big, u);
+  }
+  return linear_act<ACT>(u);
+}
+
 // One value of a bf16 or fp32 array, and one rounded into it.
 template <typename T>
 __device__ __forceinline__ float op_load(const T* p) {
