@@ -263,6 +263,12 @@ FI_API fi_status fi_generate_noalloc(const fi_config* cfg, const void* h, int32_
  * streams at once; and may be captured into a CUDA graph. Inputs are in
  * cfg->dtype (FI_F32 or FI_BF16), sums and states in 32 bits. */
 
+/* Wait until every call issued on `stream` has finished. Returns FI_E_TIMEOUT if
+ * a bounded device-side wait inside an operator's kernel gave up on the current
+ * device since the last check (the results of calls since then are not valid;
+ * the flag is cleared). The kernels' waits are all bounded. */
+FI_API fi_status fi_op_sync(void* stream);
+
 /* Linear attention with one decay per head, for sequence b, head h:
  *     S_t = g_h S_{t-1} + k_t v_t^T          (S: key_dim x value_dim, 32 bits)
  *     o_t = R(scale * q_t^T S_t)             g_h = exp(log_decay[h])

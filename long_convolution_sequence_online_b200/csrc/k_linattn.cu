@@ -325,7 +325,7 @@ cudaError_t step_vec(const LaShape& s, const void* q, const void* k, const void*
 }  // namespace
 
 // Enough segments that two CTAs per SM run, each of at least four chunks.
-LaPlan la_plan(const LaShape& s, int num_sms) {
+static LaPlan la_plan(const LaShape& s, int num_sms) {
   const int64_t per = (int64_t)s.B * s.H * ((s.dv + kSlice - 1) / kSlice);
   const int64_t chunks = ((int64_t)s.n + kC - 1) / kC;
   int64_t G = (2 * (int64_t)num_sms) / per;
@@ -336,7 +336,16 @@ LaPlan la_plan(const LaShape& s, int num_sms) {
   return LaPlan{(int)((chunks + c - 1) / c), (int)(c * kC)};
 }
 
-cudaError_t launch_linattn_prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
+size_t linattn_prefill_workspace(const LaShape& s, int num_sms) {
+  const size_t w = la_workspace_bytes(s, la_plan(s, num_sms));
+  if (!s.bf16 || s.dk > 128 || s.dv > 128) return w;
+  const size_t t = la_workspace_bytes(s, linattn_tc_plan(s, num_sms));
+  return w > t ? w : t;
+}
+
+cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sms, cudaStream_t st) {
+  if (linattn_tc_fits(s, a)) return launch_linattn_tc(s, linattn_tc_plan(s, num_sms), a, st);
+  const LaPlan p = la_plan(s, num_sms);
   return s.bf16 ? prefill_dk<__nv_bfloat16>(s, p, a, st) : prefill_dk<float>(s, p, a, st);
 }
 

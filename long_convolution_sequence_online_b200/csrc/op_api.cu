@@ -91,7 +91,7 @@ fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  *bytes = la_workspace_bytes(s, la_plan(s, sms));
+  *bytes = linattn_prefill_workspace(s, sms);
   return FI_OK;
 }
 
@@ -111,12 +111,11 @@ fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const LaPlan p = la_plan(s, sms);
-  const size_t need = n > 0 ? la_workspace_bytes(s, p) : 0;
+  const size_t need = n > 0 ? linattn_prefill_workspace(s, sms) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return invalid("workspace: " + std::to_string(need) + " bytes, 256-byte aligned, are needed");
   const LaPtrs a{q, k, v, log_decay, lengths, state_in, state_out, o, need ? (float*)workspace : nullptr};
-  e = launch_linattn_prefill(s, p, a, (cudaStream_t)stream);
+  e = launch_linattn_prefill(s, a, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention prefill launch");
 }
 
@@ -136,6 +135,14 @@ fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const voi
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   e = launch_linattn_step(s, q, k, v, log_decay, state, o, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention step launch");
+}
+
+fi_status fi_op_sync(void* stream) {
+  int a = 0, b = 0;
+  cudaError_t e = linear_take_error((cudaStream_t)stream, &a);
+  if (e == cudaSuccess) e = linattn_take_error((cudaStream_t)stream, &b);
+  if (e != cudaSuccess) return cuda_fail(e, "operator check");
+  return a || b ? fail(FI_E_TIMEOUT, "a bounded wait in an operator's kernel gave up") : FI_OK;
 }
 
 fi_status fi_linear(const fi_linear_config* c, int32_t n, const void* x, const void* w, const void* bias,

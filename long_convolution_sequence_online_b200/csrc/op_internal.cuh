@@ -24,7 +24,6 @@ struct LaShape {
 struct LaPlan {
   int G, seg;
 };
-LaPlan la_plan(const LaShape& s, int num_sms);
 // Scratch of a plan: slot 0 of (sequence, head) holds the state before the
 // prompt, slot g the contribution of segment g - 1.
 inline size_t la_workspace_bytes(const LaShape& s, const LaPlan& p) {
@@ -40,7 +39,17 @@ struct LaPtrs {
   void* o;
   float* ws;
 };
-cudaError_t launch_linattn_prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st);
+// Scratch of either kernel below, whichever the pointers' alignment allows.
+size_t linattn_prefill_workspace(const LaShape& s, int num_sms);
+cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sms, cudaStream_t st);
+// Tensor-core form (k_linattn_tc.cu): bf16, dimensions up to 128, tensors that a
+// tensor map can describe.
+bool linattn_tc_fits(const LaShape& s, const LaPtrs& a);
+LaPlan linattn_tc_plan(const LaShape& s, int num_sms);
+cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st);
+// Whether a bounded wait gave up in these kernels since the last check
+// (synchronises the stream; the flag is cleared).
+cudaError_t linattn_take_error(cudaStream_t st, int* flag);
 cudaError_t launch_linattn_step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay,
                                 float* state, void* o, int num_sms, cudaStream_t st);
 
@@ -68,6 +77,7 @@ struct LinShape {
 };
 cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
                           void* y, int num_sms, cudaStream_t st);
+cudaError_t linear_take_error(cudaStream_t st, int* flag);
 
 template <int ACT>
 __device__ __forceinline__ float linear_act(float u) {

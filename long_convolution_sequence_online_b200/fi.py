@@ -23,7 +23,7 @@ EXPORTED = ("fi_init", "fi_step", "fi_generate", "fi_generate_host", "fi_generat
             "fi_position", "fi_read_activations", "fi_set_stream", "fi_get_plan", "fi_profile",
             "fi_profile_read", "fi_destroy", "fi_status_str", "fi_last_error", "fi_debug_fft",
             "fi_generate_noalloc", "fi_debug_set_wait_limit", "fi_debug_chunk_schedule", "fi_prefill", "fi_profile_read_sides",
-            "fi_set_mlp_block", "fi_linattn_workspace", "fi_linattn_prefill", "fi_linattn_step", "fi_linear")
+            "fi_set_mlp_block", "fi_linattn_workspace", "fi_linattn_prefill", "fi_linattn_step", "fi_linear", "fi_op_sync")
 
 
 class FiError(RuntimeError):
@@ -86,6 +86,7 @@ def _load():
         "fi_linattn_workspace": [vp, i32, ctypes.POINTER(ctypes.c_uint64)],
         "fi_linattn_prefill": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
         "fi_linattn_step": [vp, vp, vp, vp, vp, vp, vp, vp],
+        "fi_op_sync": [vp],
         "fi_linear": [vp, i32, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
@@ -399,6 +400,11 @@ def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
         raise ValueError("residual must have y's shape and dtype")
     _check(lib.fi_linear(got[1], x.shape[0], x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
                          None if residual is None else residual.data_ptr(), y.data_ptr(), st), "fi_linear")
+
+
+def op_sync(stream=None):
+    """Waits for the stream; raises FiError (FI_E_TIMEOUT) if a bounded wait in an operator's kernel gave up."""
+    _check(lib.fi_op_sync(_stream(stream)), "fi_op_sync")
 
 
 def chunk_schedule(chunk: int, retimed: bool, coarse: bool = False):
