@@ -6,8 +6,6 @@
 //   o_i = scale [ sum_{j <= i} g^{i-j} (q_i . k_j) v_j + g^{i+1} q_i^T S ]
 //   S  <- g^C S + sum_j g^{C-1-j} k_j v_j^T.
 // Every power of g has an exponent >= 0, so nothing overflows whatever the decay.
-#include <mutex>
-
 #include "op_internal.cuh"
 
 namespace fi {
@@ -272,28 +270,16 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   }
 }
 
-// The dynamic shared-memory cap is one value per kernel for the whole process:
-// raised when a call needs more, never lowered.
-template <class Kern>
-cudaError_t raise_cap(Kern kernel, size_t smem) {
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  cudaFuncAttributes fa{};
-  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-  if (e != cudaSuccess || (size_t)fa.maxDynamicSharedSizeBytes >= smem) return e;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
 template <typename T, int DKP>
 cudaError_t prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
   cudaError_t e;
   const dim3 grid((unsigned)((s.dv + kSlice - 1) / kSlice), (unsigned)(s.B * s.H), (unsigned)p.G);
   if (p.G > 1) {
-    if ((e = raise_cap(k_linattn<T, DKP, false>, la_smem<DKP>())) != cudaSuccess) return e;
+    if ((e = allow_smem<k_linattn<T, DKP, false>>(la_smem<DKP>())) != cudaSuccess) return e;
     k_linattn<T, DKP, false><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = raise_cap(k_linattn<T, DKP, true>, la_smem<DKP>())) != cudaSuccess) return e;
+  if ((e = allow_smem<k_linattn<T, DKP, true>>(la_smem<DKP>())) != cudaSuccess) return e;
   k_linattn<T, DKP, true><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
   return cudaGetLastError();
 }

@@ -20,8 +20,6 @@
 // Warps: 0-3 scores -> P, then the outputs; 4-11 the state; 12-15 w V; 16 issues
 // the MMAs; 17 the TMA copies. Everything is handed over by mbarriers, so the
 // MMAs of one chunk, the copies of the next and the warps' arithmetic overlap.
-#include <mutex>
-
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -476,18 +474,6 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   if (warp == 0) tmem_free(tmem, 512);
 }
 
-// The dynamic shared-memory cap is one value per kernel for the whole process:
-// raised when a call needs more, never lowered.
-template <class Kern>
-cudaError_t raise_cap(Kern kernel, size_t smem) {
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  cudaFuncAttributes fa{};
-  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-  if (e != cudaSuccess || (size_t)fa.maxDynamicSharedSizeBytes >= smem) return e;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
 // Whether a tensor map can describe x: 16-byte aligned address and strides; a
 // stride of 0 is one shared element, which positions cannot be.
 bool mappable(const void* x, const int64_t (&st)[3], const LaShape& s) {
@@ -529,12 +515,12 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.G > 1) {
-    if ((e = raise_cap(k_linattn_tc<DK, DV, false>, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem<k_linattn_tc<DK, DV, false>>(smem)) != cudaSuccess) return e;
     if ((e = cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, false>, s, p, a, qm, km, vm, mul, (int)out16, (int)state16,
                                 (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
-  if ((e = raise_cap(k_linattn_tc<DK, DV, true>, smem)) != cudaSuccess) return e;
+  if ((e = allow_smem<k_linattn_tc<DK, DV, true>>(smem)) != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, true>, s, p, a, qm, km, vm, mul, (int)out16, (int)state16,
                             (int)kDefaultWaitLimit);
 }

@@ -19,8 +19,6 @@
 // 2^-24). The fp32 sums of many such products would pick up the tensor core's
 // rounding at every step, so each block of 64 gets an accumulator of its own
 // (smallest products first) and the epilogue warps add the blocks in registers.
-#include <mutex>
-
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -443,56 +441,25 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   }
 }
 
-// The dynamic shared-memory cap is one value per kernel for the whole process:
-// raised when a call needs more, never lowered.
-template <class Kern>
-cudaError_t raise_cap(Kern kernel, size_t smem) {
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  cudaFuncAttributes fa{};
-  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-  if (e != cudaSuccess || (size_t)fa.maxDynamicSharedSizeBytes >= smem) return e;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
-struct LinCall {
-  const LinShape& s;
-  const void *x, *w, *bias, *residual;
-  void* y;
-  int num_sms;
-  cudaStream_t st;
-};
-
-bool aligned16(const void* p, int64_t ld, int64_t rows, size_t esz) {
-  return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (ld * (int64_t)esz) % 16 == 0);
-}
-
-bool map_rows(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
-  const uint64_t strides[1] = {rows > 1 ? (uint64_t)ld * 2 : (uint64_t)((cols + 7) / 8 * 16)};
-  const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)box_rows};
-  return encode_map(map, p, 2, dims, strides, box);
-}
-
 template <int BN, int PARTS, bool PAIR, typename T, int ACT>
 cudaError_t run(const LinCall& c) {
   const LinShape& s = c.s;
-  auto kern = k_linear_tc<BN, PARTS, PAIR, T, ACT>;
+  constexpr auto kern = k_linear_tc<BN, PARTS, PAIR, T, ACT>;
   constexpr int BW = PAIR ? BN / 2 : BN, TM = PAIR ? 2 * kBM : kBM;
   constexpr size_t smem = smem_bytes<BW, PARTS * (PAIR ? kPairBlocks : 1)>();
-  cudaError_t e = raise_cap(kern, smem);
+  cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap{}, wmap{};
-  if (PAIR && (!map_rows(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !map_rows(&wmap, c.w, s.N, s.K, s.ldw, BW)))
+  if (PAIR && (!linear_map(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !linear_map(&wmap, c.w, s.N, s.K, s.ldw, BW)))
     return cudaErrorInvalidValue;
   LinTiles g{};
   g.mt = (int)(((int64_t)s.n + TM - 1) / TM);
   g.nt = (s.N + BN - 1) / BN;
   g.group = g.mt < 2048 / TM ? g.mt : 2048 / TM;
   g.tiles = g.mt * g.nt;
-  const int vec_load = (aligned16(c.x, s.ldx, s.n, sizeof(T)) ? 1 : 0) | (aligned16(c.w, s.ldw, s.N, sizeof(T)) ? 2 : 0);
-  const int vec_store = aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
-                        (!c.residual || aligned16(c.residual, s.ldr, s.n, sizeof(T)));
+  const int vec_load = (linear_aligned16(c.x, s.ldx, s.n, sizeof(T)) ? 1 : 0) | (linear_aligned16(c.w, s.ldw, s.N, sizeof(T)) ? 2 : 0);
+  const int vec_store = linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
+                        (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
   const int slots = PAIR ? c.num_sms / 2 : c.num_sms;
   const int ctas = (g.tiles < slots ? g.tiles : slots) * (PAIR ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
@@ -549,13 +516,22 @@ bool encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* di
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool linear_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t strides[1] = {rows > 1 ? (uint64_t)ld * 2 : (uint64_t)((cols + 7) / 8 * 16)};
+  const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)box_rows};
+  return encode_map(map, p, 2, dims, strides, box);
+}
+
 cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
                           void* y, int num_sms, cudaStream_t st) {
   const LinCall c{s, x, w, bias, residual, y, num_sms, st};
-  if (!s.bf16) return run_act<128, 3, false, float>(c);
   // a row stride of 0 (one row of x for all) is no tensor-map stride
-  if (!aligned16(x, s.ldx, s.n, 2) || !aligned16(w, s.ldw, s.N, 2) || (s.ldx == 0 && s.n > 1))
-    return run_act<128, 1, false, __nv_bfloat16>(c);
+  const bool tma = s.bf16 && linear_aligned16(x, s.ldx, s.n, 2) && linear_aligned16(w, s.ldw, s.N, 2) && (s.ldx != 0 || s.n == 1);
+  if (tma && s.n <= kFewRows) return launch_linear_few(c);
+  if (!tma && s.n <= kWarpRows) return launch_linear_rows(c);
+  if (!s.bf16) return run_act<128, 3, false, float>(c);
+  if (!tma) return run_act<128, 1, false, __nv_bfloat16>(c);
   const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM);
   if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, true, __nv_bfloat16>(c);
   return run_act<128, 1, true, __nv_bfloat16>(c);

@@ -21,9 +21,14 @@ fi_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 cudaError_t device_sms(int* sms) {
+  static std::atomic<int> known[64];       // by device; 0: not asked yet
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -138,11 +143,12 @@ fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const voi
 }
 
 fi_status fi_op_sync(void* stream) {
-  int a = 0, b = 0;
+  int a = 0, b = 0, d = 0;
   cudaError_t e = linear_take_error((cudaStream_t)stream, &a);
+  if (e == cudaSuccess) e = linear_few_take_error((cudaStream_t)stream, &d);
   if (e == cudaSuccess) e = linattn_take_error((cudaStream_t)stream, &b);
   if (e != cudaSuccess) return cuda_fail(e, "operator check");
-  return a || b ? fail(FI_E_TIMEOUT, "a bounded wait in an operator's kernel gave up") : FI_OK;
+  return a || b || d ? fail(FI_E_TIMEOUT, "a bounded wait in an operator's kernel gave up") : FI_OK;
 }
 
 fi_status fi_linear(const fi_linear_config* c, int32_t n, const void* x, const void* w, const void* bias,

@@ -3,9 +3,26 @@
 // in op_api.cu.
 #pragma once
 
+#include <atomic>
+
 #include "fi_internal.cuh"
 
 namespace fi {
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device (a kernel's
+// need is a constant of its instantiation).
+template <auto Kern>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};     // bit per device; devices beyond 63 set it on every call
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---------------------------------------------------------------- linear attention
 // Sizes and strides as in fi_linattn_config (strides in elements: position,
@@ -77,7 +94,26 @@ struct LinShape {
 };
 cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
                           void* y, int num_sms, cudaStream_t st);
+struct LinCall {
+  const LinShape& s;
+  const void *x, *w, *bias, *residual;
+  void* y;
+  int num_sms;
+  cudaStream_t st;
+};
+// Few rows (k_linear_few.cu): tensor cores with W's rows as the wide side (bf16,
+// operands by TMA, n <= kFewRows), or a warp per row of W (any operands).
+constexpr int kFewRows = 128, kWarpRows = 8;
+cudaError_t launch_linear_few(const LinCall& c);
+cudaError_t launch_linear_rows(const LinCall& c);
+// 16-byte aligned address and row stride.
+inline bool linear_aligned16(const void* p, int64_t ld, int64_t rows, size_t esz) {
+  return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (ld * (int64_t)esz) % 16 == 0);
+}
+// Whether a bounded wait gave up in these kernels since the last check
+// (synchronises the stream; the flag is cleared).
 cudaError_t linear_take_error(cudaStream_t st, int* flag);
+cudaError_t linear_few_take_error(cudaStream_t st, int* flag);
 
 template <int ACT>
 __device__ __forceinline__ float linear_act(float u) {

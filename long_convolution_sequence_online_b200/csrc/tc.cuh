@@ -214,5 +214,7 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t&
 // once per process.
 bool encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
+// Rows of a bf16 matrix in boxes of box_rows x 64.
+bool linear_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 
 }  // namespace fi

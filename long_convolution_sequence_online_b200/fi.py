@@ -261,71 +261,74 @@ def generate_noalloc(h, batch: int, n: int, x0, eps, y_out, dtype: str = "f32", 
 
 
 # -- operators (no context): linear attention and the linear layer
+#
+# What a call's tensors look like (shapes, strides, types, devices) is checked once
+# per combination and kept with the configuration it gives; the tensors' addresses
+# are not part of it.
 
 _DTYPE_CODE = {}          # torch dtype -> fi_dtype, filled on first use
-_configs: dict = {}       # operator configuration -> (ctypes struct, its address, scratch bytes), by sizes and strides
+_configs: dict = {}       # what the tensors look like -> (address of the configuration, scratch bytes, the configuration)
 
 
-def _dtype_code(dtype):
-    if not _DTYPE_CODE:
-        import torch
-        _DTYPE_CODE.update({torch.float32: FI_F32, torch.bfloat16: FI_BF16})
-    code = _DTYPE_CODE.get(dtype)
-    if code is None:
-        raise ValueError(f"expected float32 or bfloat16 tensors, got {dtype}")
-    return code
+def _look(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-def _keep(key, value):
+def _keep(key, cfg, need=0):
     if len(_configs) >= 4096:      # a program with ever new sizes does not grow without bound
         _configs.clear()
-    _configs[key] = value
-    return value
+    got = _configs[key] = (ctypes.addressof(cfg), need, cfg)
+    return got
 
 
-def _on_device(stream, dev, tensors):
-    """The stream for a call on CUDA device index `dev`, which must hold every tensor."""
+def _op_stream(stream, dev):
+    """The stream of a call whose tensors are on CUDA device `dev`, which must be the current one."""
     import torch
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError("expected CUDA tensors on one device")
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _heads_config(q, k, v, o, scale, n):
-    """fi_linattn_config of q, k [..][B][H][dk], v, o [..][B][H][dv] (n: positions, or None
-    for a step, whose tensors have no position dimension)."""
-    key = (q.shape, v.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, scale, n is None)
-    got = _configs.get(key)
-    if got is not None and k.shape == q.shape and o.shape == v.shape and k.dtype == v.dtype == o.dtype == q.dtype:
-        return got
-    want = 3 if n is None else 4
+def _check_tensors(tensors, dtype):
+    """One CUDA device, and one of the library's types for those of `tensors` that are not None; its code."""
+    import torch
+    if not _DTYPE_CODE:
+        _DTYPE_CODE.update({torch.float32: FI_F32, torch.bfloat16: FI_BF16})
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"expected float32 or bfloat16 tensors, got {dtype}")
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) != 1 or -1 in devices:
+        raise ValueError("expected CUDA tensors on one device")
+    return _DTYPE_CODE[dtype]
+
+
+def _linattn_config(key, q, k, v, log_decay, o, states, lengths, scale, n):
+    """Checks the tensors of a linear-attention call and keeps its configuration; n: positions, or
+    None for a step, whose tensors have no position dimension."""
+    import torch
+    code = _check_tensors((q, k, v, log_decay, o, lengths, *states), q.dtype)
+    lead, want = ("", 3) if n is None else ("[n]", 4)
     if q.dim() != want or k.shape != q.shape or o.shape != v.shape or v.dim() != want or v.shape[:-1] != q.shape[:-1]:
-        raise ValueError("expected q, k %s[B][H][key_dim] and v, o %s[B][H][value_dim]" % (("", "") if n is None else ("[n]", "[n]")))
+        raise ValueError(f"expected q, k {lead}[B][H][key_dim] and v, o {lead}[B][H][value_dim]")
     if not (k.dtype == v.dtype == o.dtype == q.dtype):
         raise ValueError("q, k, v and o must have one dtype")
     if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (q, k, v, o)):
         raise ValueError("the innermost dimension of q, k, v and o must be contiguous")
-    B, H, dk = (int(x) for x in q.shape[-3:])
-    cfg = LinattnConfig(H, dk, int(v.shape[-1]), B, _dtype_code(q.dtype), scale)
+    B, H, dk, dv = *(int(x) for x in q.shape[-3:]), int(v.shape[-1])
+    if log_decay.shape != (H,) or log_decay.dtype != torch.float32 or not log_decay.is_contiguous():
+        raise ValueError(f"log_decay must be a contiguous float32 tensor [{H}]")
+    if lengths is not None and (lengths.shape != (B,) or lengths.dtype != torch.int32 or not lengths.is_contiguous()):
+        raise ValueError(f"lengths must be a contiguous int32 tensor [{B}]")
+    for s in states:
+        if s is not None and (s.shape != (B, H, dk, dv) or s.dtype != torch.float32 or not s.is_contiguous()):
+            raise ValueError(f"a state must be a contiguous float32 tensor [{B}][{H}][{dk}][{dv}]")
+    cfg = LinattnConfig(H, dk, dv, B, code, scale)
     for name, t in (("q_stride", q), ("k_stride", k), ("v_stride", v), ("o_stride", o)):
-        st = t.stride()[:-1] if n is not None else (0, *t.stride()[:-1])
-        getattr(cfg, name)[:] = st
+        getattr(cfg, name)[:] = t.stride()[:-1] if n is not None else (0, *t.stride()[:-1])
     need = ctypes.c_uint64()
     if n is not None:
         _check(lib.fi_linattn_workspace(ctypes.addressof(cfg), n, ctypes.byref(need)), "fi_linattn_workspace")
-    return _keep(key, (cfg, ctypes.addressof(cfg), need.value))
-
-
-def _state_ptr(state, B, H, dk, dv, name):
-    import torch
-    if state is None:
-        return None
-    if state.shape != (B, H, dk, dv) or state.dtype != torch.float32 or not state.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor [{B}][{H}][{dk}][{dv}]")
-    return state.data_ptr()
+    return _keep(key, cfg, need.value)
 
 
 def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, lengths=None, scale: float = 1.0, stream=None):
@@ -336,70 +339,75 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
     strides with a contiguous innermost dimension; log_decay [H] float32;
     lengths [B] int32 or None; state_in, state_out [B][H][key_dim][value_dim]
     float32, contiguous, or None (they may be the same tensor)."""
-    import torch
-    n = q.shape[0]
-    dev = q.device.index
-    st = _on_device(stream, dev, (q, k, v, log_decay, o, state_in, state_out, lengths))
-    _, at, need = _heads_config(q, k, v, o, scale, n)
-    B, H, dk, dv = q.shape[1], q.shape[2], q.shape[3], v.shape[3]
-    if log_decay.shape != (H,) or log_decay.dtype != torch.float32 or not log_decay.is_contiguous():
-        raise ValueError(f"log_decay must be a contiguous float32 tensor [{H}]")
-    if lengths is not None and (lengths.shape != (B,) or lengths.dtype != torch.int32 or not lengths.is_contiguous()):
-        raise ValueError(f"lengths must be a contiguous int32 tensor [{B}]")
+    key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
+           o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), _look(log_decay), _look(state_in),
+           _look(state_out), _look(lengths), scale)
+    at, need, _ = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state_in, state_out), lengths, scale,
+                                                       int(q.shape[0]))
+    st = _op_stream(stream, key[12])
     ws = None
     if need:
+        import torch
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         if stream is not None:
             ws.record_stream(torch.cuda.ExternalStream(st, device=q.device) if st else torch.cuda.default_stream(q.device))
-    _check(lib.fi_linattn_prefill(at, n, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                  None if lengths is None else lengths.data_ptr(),
-                                  _state_ptr(state_in, B, H, dk, dv, "state_in"),
-                                  _state_ptr(state_out, B, H, dk, dv, "state_out"), o.data_ptr(),
-                                  None if ws is None else ws.data_ptr(), need, st), "fi_linattn_prefill")
+    s = lib.fi_linattn_prefill(at, q.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                               None if lengths is None else lengths.data_ptr(),
+                               None if state_in is None else state_in.data_ptr(),
+                               None if state_out is None else state_out.data_ptr(), o.data_ptr(),
+                               None if ws is None else ws.data_ptr(), need, st)
+    if s:
+        _check(s, "fi_linattn_prefill")
 
 
 def linattn_step(q, k, v, log_decay, state, o, scale: float = 1.0, stream=None):
     """One position of every sequence (fi_linattn_step): q, k [B][H][key_dim],
     v, o [B][H][value_dim], state [B][H][key_dim][value_dim] float32, updated in place."""
-    import torch
-    st = _on_device(stream, q.device.index, (q, k, v, log_decay, o, state))
-    _, at, _ = _heads_config(q, k, v, o, scale, None)
-    B, H, dk = q.shape
-    if log_decay.shape != (H,) or log_decay.dtype != torch.float32 or not log_decay.is_contiguous():
-        raise ValueError(f"log_decay must be a contiguous float32 tensor [{H}]")
-    _check(lib.fi_linattn_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                               _state_ptr(state, B, H, dk, v.shape[2], "state"), o.data_ptr(), st), "fi_linattn_step")
+    key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
+           o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), state.shape, state.stride(),
+           state.dtype, state.get_device(), log_decay.shape, log_decay.stride(), log_decay.dtype, log_decay.get_device(),
+           scale)
+    at = (_configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state,), None, scale, None))[0]
+    s = lib.fi_linattn_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
+                            o.data_ptr(), _op_stream(stream, key[12]))
+    if s:
+        _check(s, "fi_linattn_step")
+
+
+def _linear_config(key, x, w, y, bias, residual, act):
+    code = _check_tensors((x, w, y, bias, residual), x.dtype)
+    if x.dim() != 2 or w.dim() != 2 or y.dim() != 2 or x.shape[1] != w.shape[1] or tuple(y.shape) != (x.shape[0], w.shape[0]):
+        raise ValueError("expected x [n][in], w [out][in] and y [n][out]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    if any(t is not None and t.dtype != x.dtype for t in (w, y, bias, residual)):
+        raise ValueError("x, w, y, bias and residual must have one dtype")
+    if bias is not None and (tuple(bias.shape) != (w.shape[0],) or not bias.is_contiguous()):
+        raise ValueError("bias must be contiguous, [out]")
+    if residual is not None and residual.shape != y.shape:
+        raise ValueError("residual must have y's shape")
+    if any(t is not None and t.shape[-1] > 1 and t.stride(-1) != 1 for t in (x, w, y, residual)):
+        raise ValueError("the rows of x, w, y and residual must be contiguous")
+    nin, nout = int(x.shape[1]), int(w.shape[0])
+
+    def ld(t, cols):     # the stride of a single row says nothing
+        return int(t.stride(0)) if t.shape[0] > 1 else cols
+
+    return _keep(key, LinearConfig(nin, nout, code, ACTIVATIONS[act], ld(x, nin), ld(w, nin),
+                                   nout if residual is None else ld(residual, nout), ld(y, nout)))
 
 
 def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
     """y = act(x w^T + bias) + residual (fi_linear): x [n][in], w [out][in], y and
     residual [n][out], bias [out], all float32 or all bfloat16, rows of any stride
     with contiguous elements. act: none, gelu, silu, relu or tanh. residual may be y."""
-    st = _on_device(stream, x.device.index, (x, w, y, bias, residual))
-    key = (x.shape, w.shape, y.shape, x.stride(), w.stride(), y.stride(), residual is not None and residual.stride(),
-           x.dtype, act)
-    got = _configs.get(key)
-    if got is None:
-        if x.dim() != 2 or w.dim() != 2 or y.dim() != 2 or x.shape[1] != w.shape[1] or tuple(y.shape) != (x.shape[0], w.shape[0]):
-            raise ValueError("expected x [n][in], w [out][in] and y [n][out]")
-        if act not in ACTIVATIONS:
-            raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
-        if any(t is not None and t.shape[-1] > 1 and t.stride(-1) != 1 for t in (x, w, y, residual)):
-            raise ValueError("the rows of x, w, y and residual must be contiguous")
-        n, nin, nout = int(x.shape[0]), int(x.shape[1]), int(w.shape[0])
-        # the stride of a single row says nothing
-        ld = lambda t, cols: int(t.stride(0)) if t.shape[0] > 1 else max(cols, 1)   # noqa: E731
-        cfg = LinearConfig(nin, nout, _dtype_code(x.dtype), ACTIVATIONS[act], ld(x, nin), ld(w, nin),
-                           nout if residual is None else ld(residual, nout), ld(y, nout))
-        got = _keep(key, (cfg, ctypes.addressof(cfg), 0))
-    if w.dtype != x.dtype or y.dtype != x.dtype:
-        raise ValueError("x, w, y, bias and residual must have one dtype")
-    if bias is not None and (bias.dtype != x.dtype or bias.shape != (w.shape[0],) or not bias.is_contiguous()):
-        raise ValueError("bias must be contiguous, [out], of x's dtype")
-    if residual is not None and (residual.dtype != x.dtype or residual.shape != y.shape):
-        raise ValueError("residual must have y's shape and dtype")
-    _check(lib.fi_linear(got[1], x.shape[0], x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
-                         None if residual is None else residual.data_ptr(), y.data_ptr(), st), "fi_linear")
+    key = (x.shape, w.shape, y.shape, x.stride(), w.stride(), y.stride(), x.dtype, w.dtype, y.dtype, x.get_device(),
+           w.get_device(), y.get_device(), _look(bias), _look(residual), act)
+    at = (_configs.get(key) or _linear_config(key, x, w, y, bias, residual, act))[0]
+    s = lib.fi_linear(at, x.shape[0], x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                      None if residual is None else residual.data_ptr(), y.data_ptr(), _op_stream(stream, key[9]))
+    if s:
+        _check(s, "fi_linear")
 
 
 def op_sync(stream=None):
