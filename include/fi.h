@@ -259,7 +259,7 @@ FI_API fi_status fi_generate_noalloc(const fi_config* cfg, const void* h, int32_
  * for single tokens, and the linear layer. They need no context. Each runs
  * asynchronously on `stream` (NULL = legacy default stream) on the current
  * device, which must be the device of that stream and of every pointer; keeps
- * no memory between calls; may be called from several threads and on several
+ * no memory between calls (scratch, where a call needs some, is the caller's); may be called from several threads and on several
  * streams at once; and may be captured into a CUDA graph. Inputs are in
  * cfg->dtype (FI_F32 or FI_BF16), sums and states in 32 bits. */
 
@@ -342,13 +342,22 @@ typedef struct {
   int32_t reserved[4];  /* must be 0 */
 } fi_linear_config;
 
+/* Device bytes of scratch that fi_linear needs for n rows of these x and w (may be
+ * 0): copies of operands that the tensor cores cannot read as they stand, that is
+ * fp32 ones and bf16 ones whose address or row stride is no multiple of 16 bytes.
+ * Depends on the sizes, the strides and the addresses modulo 16 only.
+ * Errors: FI_E_INVALID. */
+FI_API fi_status fi_linear_workspace(const fi_linear_config* cfg, int32_t n, const void* x, const void* w, uint64_t* bytes);
+
 /* bias: NULL or device [out]. residual: NULL or device [n][out]; it may be y
  * itself (with ldr == ldy); y must not overlap x, w, bias or other rows of
- * residual. n = 0 does nothing.
- * Errors: FI_E_INVALID (NULL, sizes, leading dimensions, alignment, y == x),
- * FI_E_CUDA. */
+ * residual. workspace: device, 256-byte aligned, at least fi_linear_workspace
+ * bytes; NULL when that is 0. Calls that may overlap in time, replays of captured
+ * graphs among them, need a workspace each. n = 0 does nothing; n <= 2^29.
+ * Errors: FI_E_INVALID (NULL, sizes, leading dimensions, alignment, y == x,
+ * workspace too small), FI_E_CUDA. */
 FI_API fi_status fi_linear(const fi_linear_config* cfg, int32_t n, const void* x, const void* w, const void* bias,
-                           const void* residual, void* y, void* stream);
+                           const void* residual, void* y, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Test hook: the number of barrier checks after which a device-side wait in
  * later fi_generate calls gives up (negative restores the default, about a

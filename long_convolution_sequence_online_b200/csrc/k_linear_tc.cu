@@ -1,24 +1,27 @@
 // Linear layer y = R(act(x W^T + bias) + residual) on the 5th-generation tensor
 // cores (tcgen05, accumulators in tensor memory).
 //
-// A persistent CTA (or pair of CTAs on neighbouring SMs) per SM walks over output
-// tiles of 128 (256) rows x BN columns. The contraction runs in blocks of 64: x and W tiles as K-major operands of
-// 128-byte rows in shared memory with the 128-byte swizzle, a ring of stages
-// between the producer and the one thread that issues the MMAs. Accumulators
+// A persistent pair of CTAs on neighbouring SMs walks over output tiles of 256
+// rows x BN columns; each MMA works for both (cta_group::2): a CTA holds its 128
+// rows of x and half of the W tile, which halves the W traffic from L2 and shared
+// memory. The contraction runs in blocks of 64: x and W tiles as K-major operands
+// of 128-byte rows in shared memory with the 128-byte swizzle, a ring of stages
+// between the producers and the one thread that issues the MMAs. Accumulators
 // are double buffered in tensor memory, so eight epilogue warps apply bias,
 // activation and residual to one tile while the next is multiplied.
 //
-// bf16 operands whose rows start at 16-byte boundaries come by TMA into pairs of
-// CTAs that share each MMA (cta_group::2): each CTA holds its 128 rows of x and
-// half of the W tile, which halves the W traffic from L2. A lone CTA per tile of
-// 128 x 256 reads 96 bytes per clock and SM at the full MMA rate, more than L2
-// delivers: 496 us at n = 16384, 2048 -> 8192, against PAIR_US for pairs.
-// Other operands, and fp32 ones, are read by eight loader warps, which write the same layout:
-// fp32 values as three bf16 parts each, v = v0 + v1 + v2 (8 + 8 + 8 bits), and
-// the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 (the rest is below
-// 2^-24). The fp32 sums of many such products would pick up the tensor core's
-// rounding at every step, so each block of 64 gets an accumulator of its own
-// (smallest products first) and the epilogue warps add the blocks in registers.
+// Operands come by TMA, which wants bf16 rows that start at 16-byte boundaries.
+// Others are laid out so first, by a launch of their own into scratch (on chip,
+// loader warps that read and converted tiles for the MMAs took 3300 cycles per
+// block of 64 where the MMAs take 264 and, fp32, 1584: two warps per scheduler do
+// not hide their own instructions' latency).
+//
+// fp32 values are laid out as three bf16 parts each, v = v0 + v1 + v2 (8 + 8 + 8
+// bits), and the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 are added up (the
+// rest is below 2^-24). The tensor core does not round its sums to nearest: left
+// in one accumulator, such products at a contraction of 2048 were 1.4e-5 off in
+// the 2-norm, 1.3e-7 with each block of 64 in an accumulator of its own (smallest
+// products first) and the blocks added up in the epilogue warps' registers.
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -29,24 +32,26 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kEpiWarps = 8, kLoadWarps = 8;
+constexpr int kEpiWarps = 8;
+// Warps of a CTA: 0-7 epilogue, 8 the MMA issuer, 9 TMA.
+constexpr int kLinThreads = 32 * (kEpiWarps + 2);
 
 __device__ int g_linear_error;   // a bounded wait gave up since the last check
 
-// Stage of the ring: `units` x (x tile 128 x 128 bytes, W tile BW x 128 bytes), BW
-// the W rows a CTA holds: BN, or half of them in a pair. The units are the parts
-// of fp32 values, or (pairs) two blocks of the contraction: a stage's waits and
-// signals take 350 to 450 cycles whatever its size, more than the 264 that the
-// MMAs of one block take at BN = 128.
-constexpr int kPairBlocks = 2;
-template <int BW, int UNITS>
-constexpr int stage_bytes() { return UNITS * (kBM + BW) * 128; }
-template <int BW, int UNITS>
-constexpr int num_stages() { return 196608 / stage_bytes<BW, UNITS>(); }
-constexpr int kStagingLd = 33;
+// Stage of the ring: `units` x (x tile 128 x 128 bytes, half of a W tile BN / 2 x
+// 128 bytes). The units are the parts of fp32 values, or two blocks of the
+// contraction: a stage's waits and signals take 350 to 450 cycles whatever its
+// size, more than the 264 that the MMAs of one block take at BN = 128.
+template <int PARTS>
+constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
+template <int BN, int PARTS>
+constexpr int stage_bytes() { return PARTS * kStageBlocks<PARTS> * (kBM + BN / 2) * 128; }
+template <int BN, int PARTS>
+constexpr int num_stages() { return 196608 / stage_bytes<BN, PARTS>(); }
+constexpr int kStagingCols = 16, kStagingLd = kStagingCols + 1;
 constexpr int kStagingBytes = kEpiWarps * 32 * kStagingLd * 4;
-template <int BW, int UNITS>
-constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BW, UNITS>() * stage_bytes<BW, UNITS>() + kStagingBytes; }
+template <int BN, int PARTS>
+constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kStagingBytes; }
 
 struct LinTiles {
   int mt, nt, group;   // row tiles, column tiles, row tiles per group
@@ -130,69 +135,43 @@ __device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], c
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) stg[lane * kStagingLd + e] = v[e];
-  __syncwarp();
-  const int c = c0 + lane;
-  if (c < s.N) {
-    const int rows = (int)min((int64_t)32, s.n - row0);
-    T* yp = y + row0 * s.ldy + c;
-    const T* rp = residual + row0 * s.ldr + c;
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      float w[8];
+  for (int h = 0; h < 32; h += kStagingCols) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        w[r] = residual && r0 + r < rows ? op_load(rp + (int64_t)(r0 + r) * s.ldr) : 0.f;
+    for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[h + e];
+    __syncwarp();
+    const int cl = lane & 15, c = c0 + h + cl;      // a lane's column; rows lane / 16, + 2, ...
+    if (c < s.N) {
+      const int rows = (int)min((int64_t)32, s.n - row0);
+      T* yp = y + row0 * s.ldy + c;
+      const T* rp = residual + row0 * s.ldr + c;
+#pragma unroll 1
+      for (int r0 = lane >> 4; r0 < rows; r0 += 16) {
+        float w[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < rows) op_store(yp + (int64_t)(r0 + r) * s.ldy, stg[(r0 + r) * kStagingLd + lane] + w[r]);
+        for (int r = 0; r < 8; ++r)
+          w[r] = residual && r0 + 2 * r < rows ? op_load(rp + (int64_t)(r0 + 2 * r) * s.ldr) : 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r0 + 2 * r < rows) op_store(yp + (int64_t)(r0 + 2 * r) * s.ldy, stg[(r0 + 2 * r) * kStagingLd + cl] + w[r]);
+      }
     }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
-// Loader warps: 8 consecutive elements (one 16-byte unit of a swizzled row) of
-// row `row` from column k; zeros outside.
-template <typename T>
-__device__ __forceinline__ void load8(const T* base, int64_t ld, int64_t row, int64_t rows, int k, int K, bool vec,
-                                      uint32_t (&raw)[4 * sizeof(T) / 2]) {
-  constexpr int W = 4 * sizeof(T) / 2;   // 32-bit words of 8 elements
-#pragma unroll
-  for (int i = 0; i < W; ++i) raw[i] = 0;
-  if (row >= rows || k >= K) return;
-  const T* p = base + row * ld + k;
-  if (vec && k + 8 <= K) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
-    }
-    return;
-  }
-  const int m = min(8, K - k);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < m) {
-      if constexpr (sizeof(T) == 2)
-        raw[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) << (16 * (e & 1));
-      else
-        raw[e] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + e));
-    }
-}
-
-// BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32). PAIR: operands by TMA, two
-// CTAs per tile of 256 rows.
-// Warps 0-7: epilogue (tensor-memory lanes 32 (w % 4) .. + 31, column half w / 4);
-// warp 8: MMA issuer; then one TMA warp or eight loader warps.
-template <int BN, int PARTS, bool PAIR, typename T, int ACT>
-__global__ void __launch_bounds__(32 * (kEpiWarps + 1 + (PAIR ? 1 : kLoadWarps)), 1)
+// BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32; part p of a matrix is its rows
+// p n .. (p + 1) n). An epilogue warp drains tensor-memory lanes 32 (w % 4) .. + 31,
+// column half w / 4.
+template <int BN, int PARTS, typename T, int ACT>
+__global__ void __launch_bounds__(kLinThreads, 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-            const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const T* residual, T* y,
-            int vec_load, int vec_store, int wait_limit) {
-  constexpr int BW = PAIR ? BN / 2 : BN;           // W rows in this CTA's stages
-  constexpr int KS = PAIR ? kPairBlocks : 1, UNITS = PARTS * KS;
-  constexpr int ST = num_stages<BW, UNITS>(), SB = stage_bytes<BW, UNITS>();
+            const T* __restrict__ bias, const T* residual, T* y,
+            int vec_store, int wait_limit) {
+  constexpr int BW = BN / 2;                       // W rows in this CTA's stages
+  constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
+  constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
   constexpr int XB = kBM * 128, WB = BW * 128;
-  constexpr int TM = PAIR ? 2 * kBM : kBM;         // rows of a tile
+  constexpr int TM = 2 * kBM;                      // rows of a tile
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t full_bar[ST], empty_bar[ST], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_s;
@@ -202,35 +181,27 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &abort_s;
   pdl_launch_dependents();
-  const int rank = PAIR ? (int)cluster_rank() : 0;
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
-  if (warp == 0) {
-    if constexpr (PAIR) tmem_alloc2(&tmem_s, 2 * BN);
-    else tmem_alloc(&tmem_s, 2 * BN);
-  }
+  const int rank = (int)cluster_rank();
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  if (warp == 0) tmem_alloc2(&tmem_s, 2 * BN);
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
-      bar_init(&full_bar[i], PAIR ? 1 : kLoadWarps);
+      bar_init(&full_bar[i], 1);
       bar_init(&empty_bar[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&acc_full[i], 1);
-      bar_init(&acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
+      bar_init(&acc_empty[i], 2 * kEpiWarps);
     }
     abort_s = 0;
     bar_init_fence();
   }
   fence_before();
-  if constexpr (PAIR) cluster_sync();
-  else __syncthreads();
+  cluster_sync();
   fence_after();
   pdl_wait_primary();                              // from here on inputs are read and y is written
   const uint32_t tmem = tmem_s;
   const int nk = (s.K + KS * kBK - 1) / (KS * kBK);   // stages per tile
-  auto acc_release = [&](uint32_t unit) {          // one warp has read the accumulator
-    if constexpr (PAIR) bar_arrive_leader(&acc_empty[unit & 1]);
-    else bar_arrive(&acc_empty[unit & 1]);
-  };
   auto give_up = [&]() {
     *abort_flag = 1;
     atomicExch(&g_linear_error, 1);
@@ -261,7 +232,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
           if (c + 32 >= CW) {                      // all columns read: the MMA may overwrite them
             fence_before();
             __syncwarp();
-            if (lane == 0) acc_release(unit);
+            if (lane == 0) bar_arrive_leader(&acc_empty[unit & 1]);
           }
           float v[32];
 #pragma unroll
@@ -278,16 +249,16 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
           if (!alive) break;
           fence_after();
 #pragma unroll
-          for (int c = 0; c < CW; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(at + (unit & 1) * BN + c, r);
+          for (int c = 0; c < CW; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(at + (unit & 1) * BN + c, r);
             ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(r[e]);
+            for (int e = 0; e < 16; ++e) acc[c + e] += __uint_as_float(r[e]);
           }
           fence_before();
           __syncwarp();
-          if (lane == 0) acc_release(unit);
+          if (lane == 0) bar_arrive_leader(&acc_empty[unit & 1]);
         }
         if (!alive) break;
 #pragma unroll
@@ -325,8 +296,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
               for (int k = 0; k < KS * kBK / 16; ++k) {
                 if (k >= steps) break;
                 const uint32_t xo = (k / 4) * XB + (k % 4) * 32, wo = (k / 4) * WB + (k % 4) * 32;
-                if constexpr (PAIR) mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
-                else mma(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
+                mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
               }
             } else {
               constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
@@ -334,14 +304,10 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
               for (int p = 0; p < 6; ++p)
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                  mma(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
+                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
             }
-            if constexpr (PAIR) commit2(&empty_bar[st]);
-            else commit(&empty_bar[st]);
-            if (last) {
-              if constexpr (PAIR) commit2(&acc_full[unit & 1]);
-              else commit(&acc_full[unit & 1]);
-            }
+            commit2(&empty_bar[st]);
+            if (last) commit2(&acc_full[unit & 1]);
           }
           __syncwarp();
           if (last) ++unit;
@@ -352,7 +318,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       if (kbs > 0) bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDefaultWaitLimit);
     }
     __syncwarp();
-  } else if constexpr (PAIR) {
+  } else {
     // ------------------------------------------------------------ TMA producer
     const bool issuer = elect_one();
     uint32_t kbs = 0;
@@ -367,13 +333,14 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         if (!alive) break;
         if (issuer) {
           unsigned char* dst = ring + (size_t)st * SB;
-          const int blocks = min(KS, (s.K - k + kBK - 1) / kBK);
-          if (rank == 0) bar_expect(&full_bar[st], 2 * blocks * (XB + WB));   // both CTAs' tiles
+          const int units = PARTS == 1 ? min(KS, (s.K - k + kBK - 1) / kBK) : PARTS;
+          if (rank == 0) bar_expect(&full_bar[st], 2 * units * (XB + WB));   // both CTAs' tiles
 #pragma unroll
-          for (int u = 0; u < KS; ++u)
-            if (u < blocks) {
-              tma_2d_pair(dst + u * XB, &xmap, &full_bar[st], k + u * kBK, m * TM + rank * kBM);
-              tma_2d_pair(dst + UNITS * XB + u * WB, &wmap, &full_bar[st], k + u * kBK, n * BN + rank * BW);
+          for (int u = 0; u < UNITS; ++u)
+            if (u < units) {
+              const int ku = PARTS == 1 ? k + u * kBK : k;
+              tma_2d_pair(dst + u * XB, &xmap, &full_bar[st], ku, (PARTS == 1 ? 0 : u * s.n) + m * TM + rank * kBM);
+              tma_2d_pair(dst + UNITS * XB + u * WB, &wmap, &full_bar[st], ku, (PARTS == 1 ? 0 : u * s.N) + n * BN + rank * BW);
             }
         }
         __syncwarp();
@@ -382,119 +349,127 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     if (!alive && lane == 0) give_up();
     // no copy of this CTA may still be in flight when it ends: each stage's last use is done
     for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDefaultWaitLimit);
-  } else {
-    // ------------------------------------------------------------ loader warps
-    constexpr int W = 4 * sizeof(T) / 2, UX = kBM / 32, UW = BN / 32;
-    const int lt = tid - 32 * (kEpiWarps + 1);     // 0..255
-    const int unit8 = lt & 7, r0 = lt >> 3;        // 16-byte unit of a row, first row
-    uint32_t kbs = 0;
-    bool alive = true;
-    for (int t = first; t < g.tiles && alive; t += stride) {
-      int m, n;
-      tile_at(g, t, m, n);
-      for (int kb = 0; kb < nk; ++kb, ++kbs) {
-        const int st = kbs % ST, k = kb * kBK + 8 * unit8;
-        uint32_t raw[UX + UW][W];
-#pragma unroll
-        for (int u = 0; u < UX; ++u)
-          load8<T>(x, s.ldx, (int64_t)m * kBM + r0 + 32 * u, s.n, k, s.K, vec_load & 1, raw[u]);
-#pragma unroll
-        for (int u = 0; u < UW; ++u)
-          load8<T>(w, s.ldw, (int64_t)n * BN + r0 + 32 * u, s.N, k, s.K, vec_load & 2, raw[UX + u]);
-        alive = __all_sync(0xffffffffu,
-                           kbs < ST || bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag));
-        if (!alive) break;
-        unsigned char* dst = ring + (size_t)st * SB;
-#pragma unroll
-        for (int u = 0; u < UX + UW; ++u) {
-          const int r = r0 + 32 * (u < UX ? u : u - UX);
-          unsigned char* tile = dst + (u < UX ? 0 : PARTS * XB);
-          constexpr int xb = XB, wb = WB;
-          const int step = u < UX ? xb : wb;       // to the next part's tile
-          const uint32_t off = (uint32_t)r * 128 + ((unit8 ^ (r & 7)) << 4);
-          if constexpr (PARTS == 1) {
-            *reinterpret_cast<uint4*>(tile + off) = make_uint4(raw[u][0], raw[u][1], raw[u][2], raw[u][3]);
-          } else {
-            uint32_t p[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              split3(__uint_as_float(raw[u][2 * e]), __uint_as_float(raw[u][2 * e + 1]), p[0][e], p[1][e], p[2][e]);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              *reinterpret_cast<uint4*>(tile + i * step + off) = make_uint4(p[i][0], p[i][1], p[i][2], p[i][3]);
-          }
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&full_bar[st]);
-      }
-    }
-    if (!alive && lane == 0) give_up();
   }
   fence_before();
-  if constexpr (PAIR) cluster_sync_relaxed();      // neither CTA ends while the other may still signal it
-  else __syncthreads();
+  cluster_sync_relaxed();                          // neither CTA ends while the other may still signal it
   fence_after();
-  if (warp == 0) {
-    if constexpr (PAIR) tmem_free2(tmem, 2 * BN);
-    else tmem_free(tmem, 2 * BN);
+  if (warp == 0) tmem_free2(tmem, 2 * BN);
+}
+
+// An operand that TMA cannot take (fp32, or rows at no 16-byte boundary) as
+// `parts` bf16 matrices of rows of Kp = K rounded up to 8 elements, the rest zero:
+// 8 elements per thread, read once, written once.
+struct LinOperand {
+  const void* src;
+  __nv_bfloat16* dst;
+  int64_t rows, ld;
+  int vec;               // rows start at 16-byte boundaries
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand b, int K, int Kp, int64_t units_a, int64_t units) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int per = Kp / 8;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const bool first = u < units_a;
+    const LinOperand& o = first ? a : b;
+    const int64_t v = first ? u : u - units_a, row = v / per;
+    const int k = (int)(v - row * per) * 8;
+    const T* p = (const T*)o.src + row * o.ld + k;
+    __nv_bfloat16* d = o.dst + row * Kp + k;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) << (16 * (e & 1));
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float f[8];
+      if (o.vec && k + 8 <= K) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = k + e < K ? __ldg(p + e) : 0.f;
+      }
+      uint32_t q[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split3(f[2 * e], f[2 * e + 1], q[0][e], q[1][e], q[2][e]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint4*>(d + i * o.rows * Kp) = make_uint4(q[i][0], q[i][1], q[i][2], q[i][3]);
+    }
   }
 }
 
-template <int BN, int PARTS, bool PAIR, typename T, int ACT>
+template <int BN, int PARTS, typename T, int ACT>
 cudaError_t run(const LinCall& c) {
   const LinShape& s = c.s;
-  constexpr auto kern = k_linear_tc<BN, PARTS, PAIR, T, ACT>;
-  constexpr int BW = PAIR ? BN / 2 : BN, TM = PAIR ? 2 * kBM : kBM;
-  constexpr size_t smem = smem_bytes<BW, PARTS * (PAIR ? kPairBlocks : 1)>();
+  constexpr auto kern = k_linear_tc<BN, PARTS, T, ACT>;
+  constexpr int TM = 2 * kBM;
+  constexpr size_t smem = smem_bytes<BN, PARTS>();
   cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
-  CUtensorMap xmap{}, wmap{};
-  if (PAIR && (!linear_map(&xmap, c.x, s.n, s.K, s.ldx, kBM) || !linear_map(&wmap, c.w, s.N, s.K, s.ldw, BW)))
+  CUtensorMap xmap, wmap;
+  if (!linear_map(&xmap, c.x, (int64_t)PARTS * s.n, s.K, s.ldx, kBM) ||
+      !linear_map(&wmap, c.w, (int64_t)PARTS * s.N, s.K, s.ldw, BN / 2))
     return cudaErrorInvalidValue;
   LinTiles g{};
   g.mt = (int)(((int64_t)s.n + TM - 1) / TM);
   g.nt = (s.N + BN - 1) / BN;
-  g.group = g.mt < 2048 / TM ? g.mt : 2048 / TM;
+  g.group = g.mt < 8 ? g.mt : 8;
   g.tiles = g.mt * g.nt;
-  const int vec_load = (linear_aligned16(c.x, s.ldx, s.n, sizeof(T)) ? 1 : 0) | (linear_aligned16(c.w, s.ldw, s.N, sizeof(T)) ? 2 : 0);
   const int vec_store = linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
                         (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
-  const int slots = PAIR ? c.num_sms / 2 : c.num_sms;
-  const int ctas = (g.tiles < slots ? g.tiles : slots) * (PAIR ? 2 : 1);
-  cudaLaunchConfig_t cfg = {};
+  const int pairs = g.tiles < c.num_sms / 2 ? g.tiles : c.num_sms / 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(32 * (kEpiWarps + 1 + (PAIR ? 1 : kLoadWarps)));
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.st;
-  if (PAIR) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.x, (const T*)c.w, (const T*)c.bias,
-                            (const T*)c.residual, (T*)c.y, vec_load, vec_store, (int)kDefaultWaitLimit);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, vec_store,
+                            (int)kDefaultWaitLimit);
 }
 
-template <int BN, int PARTS, bool PAIR, typename T>
+template <int BN, int PARTS, typename T>
 cudaError_t run_act(const LinCall& c) {
   switch (c.s.act) {
-    case FI_ACT_NONE: return run<BN, PARTS, PAIR, T, FI_ACT_NONE>(c);
-    case FI_ACT_GELU: return run<BN, PARTS, PAIR, T, FI_ACT_GELU>(c);
-    case FI_ACT_SILU: return run<BN, PARTS, PAIR, T, FI_ACT_SILU>(c);
-    case FI_ACT_RELU: return run<BN, PARTS, PAIR, T, FI_ACT_RELU>(c);
-    case FI_ACT_TANH: return run<BN, PARTS, PAIR, T, FI_ACT_TANH>(c);
+    case FI_ACT_NONE: return run<BN, PARTS, T, FI_ACT_NONE>(c);
+    case FI_ACT_GELU: return run<BN, PARTS, T, FI_ACT_GELU>(c);
+    case FI_ACT_SILU: return run<BN, PARTS, T, FI_ACT_SILU>(c);
+    case FI_ACT_RELU: return run<BN, PARTS, T, FI_ACT_RELU>(c);
+    case FI_ACT_TANH: return run<BN, PARTS, T, FI_ACT_TANH>(c);
   }
   return cudaErrorInvalidValue;
 }
 
+// Which operands TMA takes as they are. A row stride of 0 (one row of x for all)
+// is no tensor-map stride.
+bool direct_x(const LinShape& s, const void* x) {
+  return s.bf16 && linear_aligned16(x, s.ldx, s.n, 2) && (s.ldx != 0 || s.n == 1);
+}
+bool direct_w(const LinShape& s, const void* w) { return s.bf16 && linear_aligned16(w, s.ldw, s.N, 2); }
+int padded(int K) { return (K + 7) / 8 * 8; }
+size_t operand_bytes(const LinShape& s, int64_t rows) {
+  return ((size_t)(s.bf16 ? 1 : 3) * rows * padded(s.K) * 2 + 255) / 256 * 256;
+}
+
 }  // namespace
+
+size_t linear_workspace(const LinShape& s, const void* x, const void* w) {
+  const bool dx = direct_x(s, x), dw = direct_w(s, w);
+  if ((dx && dw) || s.n <= kWarpRows) return 0;
+  return (dx ? 0 : operand_bytes(s, s.n)) + (dw ? 0 : operand_bytes(s, s.N));
+}
 
 bool encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box) {
@@ -523,18 +498,47 @@ bool linear_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int
   return encode_map(map, p, 2, dims, strides, box);
 }
 
-cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
-                          void* y, int num_sms, cudaStream_t st) {
-  const LinCall c{s, x, w, bias, residual, y, num_sms, st};
-  // a row stride of 0 (one row of x for all) is no tensor-map stride
-  const bool tma = s.bf16 && linear_aligned16(x, s.ldx, s.n, 2) && linear_aligned16(w, s.ldw, s.N, 2) && (s.ldx != 0 || s.n == 1);
-  if (tma && s.n <= kFewRows) return launch_linear_few(c);
-  if (!tma && s.n <= kWarpRows) return launch_linear_rows(c);
-  if (!s.bf16) return run_act<128, 3, false, float>(c);
-  if (!tma) return run_act<128, 1, false, __nv_bfloat16>(c);
+cudaError_t launch_linear(const LinShape& shape, const void* x, const void* w, const void* bias, const void* residual,
+                          void* y, void* workspace, int num_sms, cudaStream_t st) {
+  LinShape s = shape;
+  LinCall c{s, x, w, bias, residual, y, num_sms, st};
+  const bool dx = direct_x(s, x), dw = direct_w(s, w);
+  if (!dx || !dw) {
+    if (s.n <= kWarpRows) return launch_linear_rows(c);
+    const int Kp = padded(s.K);
+    LinOperand a{}, b{};
+    unsigned char* at = (unsigned char*)workspace;
+    if (!dx) {
+      a = LinOperand{x, (__nv_bfloat16*)at, s.n, s.ldx, linear_aligned16(x, s.ldx, s.n, s.bf16 ? 2 : 4)};
+      at += operand_bytes(s, s.n);
+      c.x = a.dst;
+      s.ldx = Kp;
+    }
+    if (!dw) {
+      b = LinOperand{w, (__nv_bfloat16*)at, s.N, s.ldw, linear_aligned16(w, s.ldw, s.N, s.bf16 ? 2 : 4)};
+      c.w = b.dst;
+      s.ldw = Kp;
+    }
+    const int64_t ua = a.rows * (Kp / 8), units = ua + b.rows * (Kp / 8);
+    const int64_t blocks = (units + 255) / 256, most = (int64_t)num_sms * 16;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = s.bf16 ? cudaLaunchKernelEx(&cfg, k_linear_layout<__nv_bfloat16>, a, b, s.K, Kp, ua, units)
+                                 : cudaLaunchKernelEx(&cfg, k_linear_layout<float>, a, b, s.K, Kp, ua, units);
+    if (e != cudaSuccess) return e;
+  }
+  if (!s.bf16) return run_act<128, 3, float>(c);
+  if (s.n <= kFewRows) return launch_linear_few(c);
   const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM);
-  if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, true, __nv_bfloat16>(c);
-  return run_act<128, 1, true, __nv_bfloat16>(c);
+  if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, __nv_bfloat16>(c);
+  return run_act<128, 1, __nv_bfloat16>(c);
 }
 
 cudaError_t linear_take_error(cudaStream_t st, int* flag) {

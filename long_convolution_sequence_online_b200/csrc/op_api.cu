@@ -37,6 +37,7 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 constexpr int64_t kMaxRows = 65535;
 constexpr int32_t kMaxPositions = 1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxLd = (int64_t)1 << 38;      // below a tensor map's 2^40 bytes
 
 // cfg -> s. `positions`: the number of positions the strides [0] step over (1:
 // not used).
@@ -77,6 +78,26 @@ fi_status check_linattn(const fi_linattn_config* c, int64_t positions, LaShape* 
     s->vs[i] = c->v_stride[i];
     s->os[i] = c->o_stride[i];
   }
+  return FI_OK;
+}
+
+fi_status check_linear(const fi_linear_config* c, int32_t n, bool residual, LinShape* s) {
+  if (!c) return invalid("cfg is NULL");
+  if (n < 0 || n > kMaxPositions / 2) return invalid("n must be in [0, 2^29]");
+  if (c->in_features < 1 || c->in_features > (1 << 20)) return invalid("in_features must be in [1, 2^20]");
+  if (c->out_features < 1 || c->out_features > (1 << 20)) return invalid("out_features must be in [1, 2^20]");
+  if (c->dtype != FI_F32 && c->dtype != FI_BF16) return invalid("dtype must be FI_F32 or FI_BF16");
+  if (c->act < FI_ACT_NONE || c->act > FI_ACT_TANH) return invalid("act must be an fi_act");
+  for (int r : c->reserved)
+    if (r != 0) return invalid("reserved fields must be 0");
+  for (int64_t v : {c->ldx, c->ldw, c->ldr, c->ldy})
+    if (v < 0 || v > kMaxLd) return invalid("leading dimensions must be in [0, 2^38]");
+  if (c->ldx != 0 && c->ldx < c->in_features) return invalid("ldx must be >= in_features, or 0");
+  if (c->ldw < c->in_features) return invalid("ldw must be >= in_features");
+  if (c->ldy < c->out_features) return invalid("ldy must be >= out_features");
+  if (residual && c->ldr != 0 && c->ldr < c->out_features) return invalid("ldr must be >= out_features, or 0");
+  if ((int64_t)n * c->out_features > (int64_t)1 << 40) return invalid("n x out_features must be <= 2^40");
+  *s = LinShape{n, c->in_features, c->out_features, c->dtype == FI_BF16, c->act, c->ldx, c->ldw, c->ldr, c->ldy};
   return FI_OK;
 }
 
@@ -151,35 +172,34 @@ fi_status fi_op_sync(void* stream) {
   return a || b || d ? fail(FI_E_TIMEOUT, "a bounded wait in an operator's kernel gave up") : FI_OK;
 }
 
-fi_status fi_linear(const fi_linear_config* c, int32_t n, const void* x, const void* w, const void* bias,
-                    const void* residual, void* y, void* stream) {
-  if (!c) return invalid("cfg is NULL");
-  if (n < 0) return invalid("n < 0");
-  if (c->in_features < 1 || c->in_features > (1 << 20)) return invalid("in_features must be in [1, 2^20]");
-  if (c->out_features < 1 || c->out_features > (1 << 20)) return invalid("out_features must be in [1, 2^20]");
-  if (c->dtype != FI_F32 && c->dtype != FI_BF16) return invalid("dtype must be FI_F32 or FI_BF16");
-  if (c->act < FI_ACT_NONE || c->act > FI_ACT_TANH) return invalid("act must be an fi_act");
-  for (int r : c->reserved)
-    if (r != 0) return invalid("reserved fields must be 0");
-  for (int64_t v : {c->ldx, c->ldw, c->ldr, c->ldy})
-    if (v < 0 || v > kMaxStride) return invalid("leading dimensions must be in [0, 2^40]");
-  if (c->ldx != 0 && c->ldx < c->in_features) return invalid("ldx must be >= in_features, or 0");
-  if (c->ldw < c->in_features) return invalid("ldw must be >= in_features");
-  if (c->ldy < c->out_features) return invalid("ldy must be >= out_features");
-  if (residual && c->ldr != 0 && c->ldr < c->out_features) return invalid("ldr must be >= out_features, or 0");
-  if ((int64_t)n * c->out_features > kMaxStride) return invalid("n x out_features must be <= 2^40");
-  if (n == 0) return FI_OK;
+fi_status fi_linear_workspace(const fi_linear_config* cfg, int32_t n, const void* x, const void* w, uint64_t* bytes) {
+  if (!bytes) return invalid("bytes is NULL");
+  *bytes = 0;
+  LinShape s;
+  const fi_status r = check_linear(cfg, n, false, &s);
+  if (r != FI_OK || n == 0) return r;
+  *bytes = linear_workspace(s, x, w);
+  return FI_OK;
+}
+
+fi_status fi_linear(const fi_linear_config* cfg, int32_t n, const void* x, const void* w, const void* bias,
+                    const void* residual, void* y, void* workspace, uint64_t workspace_bytes, void* stream) {
+  LinShape s;
+  const fi_status r = check_linear(cfg, n, residual != nullptr, &s);
+  if (r != FI_OK || n == 0) return r;
   if (!x || !w || !y) return invalid("NULL argument");
-  const size_t esz = c->dtype == FI_BF16 ? 2 : 4;
+  const size_t esz = s.bf16 ? 2 : 4;
   if (!aligned(x, esz) || !aligned(w, esz) || !aligned(y, esz) || !aligned(bias, esz) || !aligned(residual, esz))
     return invalid("a pointer is not aligned to its element size");
   if (y == x || y == w || y == bias) return invalid("y must not be an input");
-  if (y == residual && c->ldr != c->ldy && n > 1) return invalid("residual may be y only with ldr == ldy");
+  if (y == residual && s.ldr != s.ldy && n > 1) return invalid("residual may be y only with ldr == ldy");
+  const size_t need = linear_workspace(s, x, w);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return invalid("workspace: " + std::to_string(need) + " bytes, 256-byte aligned, are needed");
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const LinShape s{n, c->in_features, c->out_features, c->dtype == FI_BF16, c->act, c->ldx, c->ldw, c->ldr, c->ldy};
-  e = launch_linear(s, x, w, bias, residual, y, sms, (cudaStream_t)stream);
+  e = launch_linear(s, x, w, bias, residual, y, workspace, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear layer launch");
 }
 

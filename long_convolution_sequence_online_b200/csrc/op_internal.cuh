@@ -92,8 +92,10 @@ struct LinShape {
   int bf16, act;
   int64_t ldx, ldw, ldr, ldy;
 };
+// Scratch for operands that have to be laid out first (256-byte aligned).
+size_t linear_workspace(const LinShape& s, const void* x, const void* w);
 cudaError_t launch_linear(const LinShape& s, const void* x, const void* w, const void* bias, const void* residual,
-                          void* y, int num_sms, cudaStream_t st);
+                          void* y, void* workspace, int num_sms, cudaStream_t st);
 struct LinCall {
   const LinShape& s;
   const void *x, *w, *bias, *residual;

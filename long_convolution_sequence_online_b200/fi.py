@@ -23,7 +23,8 @@ EXPORTED = ("fi_init", "fi_step", "fi_generate", "fi_generate_host", "fi_generat
             "fi_position", "fi_read_activations", "fi_set_stream", "fi_get_plan", "fi_profile",
             "fi_profile_read", "fi_destroy", "fi_status_str", "fi_last_error", "fi_debug_fft",
             "fi_generate_noalloc", "fi_debug_set_wait_limit", "fi_debug_chunk_schedule", "fi_prefill", "fi_profile_read_sides",
-            "fi_set_mlp_block", "fi_linattn_workspace", "fi_linattn_prefill", "fi_linattn_step", "fi_linear", "fi_op_sync")
+            "fi_set_mlp_block", "fi_linattn_workspace", "fi_linattn_prefill", "fi_linattn_step", "fi_linear", "fi_linear_workspace",
+            "fi_op_sync")
 
 
 class FiError(RuntimeError):
@@ -87,7 +88,8 @@ def _load():
         "fi_linattn_prefill": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
         "fi_linattn_step": [vp, vp, vp, vp, vp, vp, vp, vp],
         "fi_op_sync": [vp],
-        "fi_linear": [vp, i32, vp, vp, vp, vp, vp, vp],
+        "fi_linear_workspace": [vp, i32, vp, vp, ctypes.POINTER(ctypes.c_uint64)],
+        "fi_linear": [vp, i32, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -263,8 +265,8 @@ def generate_noalloc(h, batch: int, n: int, x0, eps, y_out, dtype: str = "f32", 
 # -- operators (no context): linear attention and the linear layer
 #
 # What a call's tensors look like (shapes, strides, types, devices) is checked once
-# per combination and kept with the configuration it gives; the tensors' addresses
-# are not part of it.
+# per combination and kept with the configuration it gives; of the tensors' addresses
+# only the alignment is part of it, where scratch depends on it.
 
 _DTYPE_CODE = {}          # torch dtype -> fi_dtype, filled on first use
 _configs: dict = {}       # what the tensors look like -> (address of the configuration, scratch bytes, the configuration)
@@ -287,6 +289,15 @@ def _op_stream(stream, dev):
     if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _scratch(need, like, stream, st):
+    """Scratch of one call: the allocator hands its memory out again once the call's stream has passed it."""
+    import torch
+    ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(st, device=like.device) if st else torch.cuda.default_stream(like.device))
+    return ws
 
 
 def _check_tensors(tensors, dtype):
@@ -345,12 +356,7 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
     at, need, _ = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state_in, state_out), lengths, scale,
                                                        int(q.shape[0]))
     st = _op_stream(stream, key[12])
-    ws = None
-    if need:
-        import torch
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            ws.record_stream(torch.cuda.ExternalStream(st, device=q.device) if st else torch.cuda.default_stream(q.device))
+    ws = _scratch(need, q, stream, st) if need else None
     s = lib.fi_linattn_prefill(at, q.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                None if lengths is None else lengths.data_ptr(),
                                None if state_in is None else state_in.data_ptr(),
@@ -393,19 +399,27 @@ def _linear_config(key, x, w, y, bias, residual, act):
     def ld(t, cols):     # the stride of a single row says nothing
         return int(t.stride(0)) if t.shape[0] > 1 else cols
 
-    return _keep(key, LinearConfig(nin, nout, code, ACTIVATIONS[act], ld(x, nin), ld(w, nin),
-                                   nout if residual is None else ld(residual, nout), ld(y, nout)))
+    cfg = LinearConfig(nin, nout, code, ACTIVATIONS[act], ld(x, nin), ld(w, nin),
+                       nout if residual is None else ld(residual, nout), ld(y, nout))
+    need = ctypes.c_uint64()
+    _check(lib.fi_linear_workspace(ctypes.addressof(cfg), x.shape[0], x.data_ptr(), w.data_ptr(), ctypes.byref(need)),
+           "fi_linear_workspace")
+    return _keep(key, cfg, need.value)
 
 
 def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
     """y = act(x w^T + bias) + residual (fi_linear): x [n][in], w [out][in], y and
     residual [n][out], bias [out], all float32 or all bfloat16, rows of any stride
     with contiguous elements. act: none, gelu, silu, relu or tanh. residual may be y."""
+    px, pw = x.data_ptr(), w.data_ptr()
     key = (x.shape, w.shape, y.shape, x.stride(), w.stride(), y.stride(), x.dtype, w.dtype, y.dtype, x.get_device(),
-           w.get_device(), y.get_device(), _look(bias), _look(residual), act)
-    at = (_configs.get(key) or _linear_config(key, x, w, y, bias, residual, act))[0]
-    s = lib.fi_linear(at, x.shape[0], x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
-                      None if residual is None else residual.data_ptr(), y.data_ptr(), _op_stream(stream, key[9]))
+           w.get_device(), y.get_device(), _look(bias), _look(residual), act, px & 15, pw & 15)
+    at, need, _ = _configs.get(key) or _linear_config(key, x, w, y, bias, residual, act)
+    st = _op_stream(stream, key[9])
+    ws = _scratch(need, x, stream, st) if need else None
+    s = lib.fi_linear(at, x.shape[0], px, pw, None if bias is None else bias.data_ptr(),
+                      None if residual is None else residual.data_ptr(), y.data_ptr(),
+                      None if ws is None else ws.data_ptr(), need, st)
     if s:
         _check(s, "fi_linear")
 

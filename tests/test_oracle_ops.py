@@ -152,7 +152,7 @@ def test_linear_refuses_bad_configurations(kw, why):
     fi = _fi()
     cfg = _lin(fi, **kw)
     far = [ctypes.c_void_p(4096 * i) for i in range(1, 6)]
-    assert fi.lib.fi_linear(ctypes.addressof(cfg), 4, *far, None) == fi.FI_E_INVALID
+    assert fi.lib.fi_linear(ctypes.addressof(cfg), 4, *far, None, 0, None) == fi.FI_E_INVALID
     assert why in fi.lib.fi_last_error().decode()
 
 
@@ -162,22 +162,22 @@ def test_linear_refuses_nulls_alignment_and_aliases():
     cfg = _lin(fi)
     at = ctypes.addressof(cfg)
     x, w, b, r, y = (ctypes.c_void_p(1 << (12 + i)) for i in range(5))
-    assert L.fi_linear(None, 4, x, w, b, r, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, -1, x, w, b, r, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, 4, None, w, b, r, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, 4, x, None, b, r, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, 4, x, w, b, r, None, None) == fi.FI_E_INVALID
+    assert L.fi_linear(None, 4, x, w, b, r, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, -1, x, w, b, r, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 4, None, w, b, r, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 4, x, None, b, r, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 4, x, w, b, r, None, None, 0, None) == fi.FI_E_INVALID
     odd = ctypes.c_void_p(4098)
     for i in range(5):
         a = [x, w, b, r, y]
         a[i] = odd
-        assert L.fi_linear(at, 4, *a, None) == fi.FI_E_INVALID
+        assert L.fi_linear(at, 4, *a, None, 0, None) == fi.FI_E_INVALID
         assert "aligned" in L.fi_last_error().decode()
-    assert L.fi_linear(at, 4, y, w, b, r, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, 4, x, y, b, r, y, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 4, y, w, b, r, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 4, x, y, b, r, y, None, 0, None) == fi.FI_E_INVALID
     bad = _lin(fi, ldr=24)
-    assert L.fi_linear(ctypes.addressof(bad), 4, x, w, b, y, y, None) == fi.FI_E_INVALID
-    assert L.fi_linear(at, 0, x, w, b, r, y, None) == fi.FI_OK      # no rows: nothing to do
+    assert L.fi_linear(ctypes.addressof(bad), 4, x, w, b, y, y, None, 0, None) == fi.FI_E_INVALID
+    assert L.fi_linear(at, 0, x, w, b, r, y, None, 0, None) == fi.FI_OK      # no rows: nothing to do
 
 
 def test_binding_refuses_cpu_tensors():
