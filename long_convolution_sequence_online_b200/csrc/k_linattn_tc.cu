@@ -17,9 +17,15 @@
 // bf16 K are exact, and every chunk's KV is accumulated on its own (the tensor
 // core's sums are not rounded to nearest) and added to S in registers.
 //
-// Warps: 0-3 scores -> P, then the outputs; 4-11 the state; 12-15 w V; 16 issues
-// the MMAs; 17 the TMA copies. Everything is handed over by mbarriers, so the
-// MMAs of one chunk, the copies of the next and the warps' arithmetic overlap.
+// Sixteen worker warps do all arithmetic, each on a 32 x 32 (state, outputs: 32 x
+// DV / 4) block of every matrix, one phase after another; one warp issues the
+// MMAs, one the TMA copies. Per chunk c the workers form the first half of w V,
+// the outputs of chunk c - 1, the second half of w V, P, and the state; the MMAs
+// run in the order KV (first half), Q K^T, KV (second half), Q S, P V. Each phase
+// of the workers then overlaps MMAs that do not need it, and an arrival on
+// w_ready tells the issuer that everything before it in the workers' order is done
+// as well. (Warps with a role each - P and outputs 4, state 8, w V 4 - took 10400
+// cycles a chunk at 128 x 128: a role's few warps do not hide their latency.)
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -31,21 +37,21 @@ using namespace tc;
 
 constexpr int kCh = 128;                 // positions per chunk
 constexpr int kWHalf = 64;               // positions of w V in shared memory at a time
-constexpr int kSlots = 4;                // tiles of Q, K, V in flight
-constexpr int kOutWarps = 4, kStateWarps = 8, kScaleWarps = 4;
-constexpr int kMmaWarp = kOutWarps + kStateWarps + kScaleWarps, kTmaWarp = kMmaWarp + 1;
+constexpr int kWorkers = 16;
+constexpr int kMmaWarp = kWorkers, kTmaWarp = kMmaWarp + 1;
 constexpr int kLaTcThreads = 32 * (kTmaWarp + 1);
 
 __device__ int g_linattn_error;          // a bounded wait gave up since the last check
 
-// DK, DV: key and value dimensions padded to 64 or 128.
+// DK, DV: key and value dimensions padded to 64 or 128. V is always double
+// buffered (the next chunk's w V starts first), K and Q where there is room.
 template <int DK, int DV>
 struct LaSmem {
+  static constexpr int kSlotsKQ = DK == 128 && DV == 128 ? 1 : 2, kSlotsV = 2;
   static constexpr int kTileK = kCh * 2 * DK, kTileV = kCh * 2 * DV;
-  static constexpr int kSlot = kTileK > kTileV ? kTileK : kTileV;
   static constexpr int kPart = kWHalf * 2 * DV;
   static constexpr int kState = DK * 2 * DV;
-  static constexpr size_t bytes = 1024 + (size_t)kSlots * kSlot + 3 * kPart + kState;
+  static constexpr size_t bytes = 1024 + (size_t)2 * kSlotsKQ * kTileK + kSlotsV * kTileV + 3 * kPart + kState;
 };
 
 // Coordinates of a tensor map [dim][position][sequence][head]; a stride of 0
@@ -60,18 +66,23 @@ constexpr uint32_t kColP = 0, kColInter = 128, kColIntra = 256, kColKV = 384;
 template <int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
-             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, LaMul mul, int vec_out,
-             int vec_state, int wait_limit) {
+             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+             const __grid_constant__ CUtensorMap omap, LaMul mul, int tma_out, int vec_state, int wait_limit) {
   using L = LaSmem<DK, DV>;
-  constexpr int TILES = OUT ? 3 : 2;     // per chunk: K, (Q,) V
+  constexpr int NKQ = L::kSlotsKQ, NV = L::kSlotsV;
+  constexpr int CW = DV / 4;             // a worker's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t full[kSlots], empty[kSlots], qk_done, p_ready, o_done, o_free, w_ready, w_free, kv_done, s_ready, fixed, drained;
+  __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: not with outputs
+  __shared__ uint64_t w_ready, w_free, qk_done, kv_done, qs_done, p_ready, o_done, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
+  __shared__ float GD[63];               // GD[31 + i] = g^i, i = 0 .. 31 (masked below)
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
-  unsigned char* slots = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
-  unsigned char* wv = slots + kSlots * L::kSlot;
+  unsigned char* ks = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
+  unsigned char* qs = ks + NKQ * L::kTileK;
+  unsigned char* vs = qs + NKQ * L::kTileK;
+  unsigned char* wv = vs + NV * L::kTileV;
   unsigned char* sop = wv + 3 * L::kPart;
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -95,20 +106,24 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   if (warp == 0) tmem_alloc(&tmem_s, 512);
   if (tid >= 64 && tid < 64 + kCh + 1) G[tid - 64] = la_pow(ld2, tid - 64);
   if (tid >= 256 && tid < 288) GR[tid - 256] = la_pow(ld2, 31 - (tid - 256));
+  if (tid >= 288 && tid < 288 + 63) GD[tid - 288] = la_pow(ld2, max(0, tid - 288 - 31));
   if (tid == 32) {
-    for (int i = 0; i < kSlots; ++i) {
-      bar_init(&full[i], 1);
-      bar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&k_full[i], 1);
+      bar_init(&k_empty[i], 1);
+      bar_init(&q_full[i], 1);
+      bar_init(&q_empty[i], 1);
+      bar_init(&v_full[i], 1);
+      bar_init(&v_empty[i], 1);
     }
-    bar_init(&qk_done, 1);
-    bar_init(&p_ready, kOutWarps);
-    bar_init(&o_done, 1);
-    bar_init(&o_free, kOutWarps);
-    bar_init(&w_ready, kScaleWarps);
+    bar_init(&w_ready, kWorkers);
     bar_init(&w_free, 1);
+    bar_init(&qk_done, 1);
     bar_init(&kv_done, 1);
-    bar_init(&s_ready, kStateWarps);
-    bar_init(&fixed, kScaleWarps);
+    bar_init(&qs_done, 1);
+    bar_init(&p_ready, kWorkers);
+    bar_init(&o_done, 1);
+    bar_init(&o_staged, kWorkers);
     bar_init(&drained, 1);
     abort_s = 0;
     bar_init_fence();
@@ -119,7 +134,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   const uint32_t tmem = tmem_s;
   volatile int* abort_flag = &abort_s;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, wait_limit, abort_flag));
+    return warp_wait(bar, parity, wait_limit, abort_flag);
   };
   auto give_up = [&]() {
     if (lane == 0) {
@@ -127,104 +142,18 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       atomicExch(&g_linattn_error, 1);
     }
   };
-  auto tile_of = [&](int c, int which) { return c * TILES + which; };   // 0: K, 1: Q (OUT), last: V
-  auto tile_at = [&](int t) { return slots + (t % kSlots) * L::kSlot; };
+
   // The last chunk of a sequence shorter than the batch: what stands behind its
   // end (anything, NaN too) is cleared in the tiles before they are multiplied.
   const bool ragged = end == len && len < s.n && (end - t0) % kCh != 0;
 
-  if (warp < kOutWarps) {
-    // ------------------------------------------------------------ P and the outputs
-    if constexpr (OUT) {
-      const int i = 32 * warp + lane;              // row of the chunk
-      const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
-      bool alive = true;
-      for (int c = 0; c < nch && alive; ++c) {
-        const int m = min(kCh, (int)(end - t0) - c * kCh);
-        alive = wait(&qk_done, c & 1);
-        if (!alive) break;
-        fence_after();
-#pragma unroll 1
-        for (int blk = 0; blk < 4; ++blk) {
-          uint32_t out[16];
-          if (blk <= warp) {
-            uint32_t r[32];
-            tmem_ld32(at + kColP + 32 * blk, r);
-            ld_wait();
-            if (blk < warp) {
-              const float f = G[i - 32 * blk - 31];
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(&GR[e]);
-                out[e / 2] = pack2(__uint_as_float(r[e]) * (f * g4.x), __uint_as_float(r[e + 1]) * (f * g4.y));
-                out[e / 2 + 1] = pack2(__uint_as_float(r[e + 2]) * (f * g4.z), __uint_as_float(r[e + 3]) * (f * g4.w));
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                out[e / 2] = pack2(e <= lane ? __uint_as_float(r[e]) * G[(lane - e) & 31] : 0.f,
-                                   e + 1 <= lane ? __uint_as_float(r[e + 1]) * G[(lane - e - 1) & 31] : 0.f);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) out[e] = 0;
-          }
-          tmem_st16(at + kColP + 16 * blk, out);
-        }
-        st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&p_ready);
-        alive = wait(&o_done, c & 1);
-        if (!alive) break;
-        fence_after();
-        const float fi_ = s.scale * G[i + 1], fo = s.scale;
-        const int64_t t = t0 + (int64_t)c * kCh + i;
-        __nv_bfloat16* op = (__nv_bfloat16*)a.o + b * s.os[1] + h * s.os[2] + t * s.os[0];
-#pragma unroll 1
-        for (int d = 0; d < DV; d += 32) {
-          uint32_t r[32], q[32];
-          tmem_ld32(at + kColInter + d, r);
-          tmem_ld32(at + kColIntra + d, q);
-          ld_wait();
-          if (d + 32 >= DV) {
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&o_free);
-          }
-          if (i < m) {
-            if (vec_out) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (d + 8 * u < s.dv) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const int x = 8 * u + 2 * e;
-                    w[e] = pack2(fmaf(fi_, __uint_as_float(r[x]), fo * __uint_as_float(q[x])),
-                                 fmaf(fi_, __uint_as_float(r[x + 1]), fo * __uint_as_float(q[x + 1])));
-                  }
-                  *reinterpret_cast<uint4*>(op + d + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (d + e < s.dv)
-                  op[d + e] = __float2bfloat16_rn(fmaf(fi_, __uint_as_float(r[e]), fo * __uint_as_float(q[e])));
-            }
-          }
-        }
-      }
-      if (!alive) give_up();
-    }
-  } else if (warp < kOutWarps + kStateWarps) {
-    // ------------------------------------------------------------ the state
-    // Row 32 (warp % 4) + lane, columns [col0, + CW) of S in registers.
-    constexpr int CW = DV / 2;
-    const int quarter = warp & 3, half = (warp - kOutWarps) >> 2;
-    const int row = 32 * quarter + lane, col0 = half * CW;
-    const uint32_t at = tmem + ((uint32_t)(32 * quarter) << 16) + kColKV + col0;
-    float st[CW];
+  if (warp < kWorkers) {
+    // ------------------------------------------------------------ workers
+    const int quarter = warp & 3, grp = warp >> 2;
+    const int row = 32 * quarter + lane;           // of the chunk (P, outputs) and of the state (key dimension)
+    const int col0 = grp * CW;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    float st[CW];                                  // S, row `row`, columns col0 ..
 #pragma unroll
     for (int e = 0; e < CW; ++e) st[e] = 0.f;
     if constexpr (OUT) {
@@ -253,40 +182,172 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     }
     // S as the B operand of Q S: rows of 64 bf16 columns, 128-byte swizzle.
     auto publish = [&]() {
-      if constexpr (OUT) {
-        if (row < DK) {
+      if (OUT && row < DK) {
 #pragma unroll
-          for (int e = 0; e < CW; e += 8) {
-            const int col = col0 + e, unit = (col & 63) >> 3;
-            unsigned char* dst = sop + (col >> 6) * (DK * 128) + row * 128 + ((unit ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(st[e], st[e + 1]), pack2(st[e + 2], st[e + 3]),
-                                                        pack2(st[e + 4], st[e + 5]), pack2(st[e + 6], st[e + 7]));
-          }
+        for (int e = 0; e < CW; e += 8) {
+          const int col = col0 + e, unit = (col & 63) >> 3;
+          unsigned char* dst = sop + (col >> 6) * (DK * 128) + row * 128 + ((unit ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(st[e], st[e + 1]), pack2(st[e + 2], st[e + 3]),
+                                                      pack2(st[e + 4], st[e + 5]), pack2(st[e + 6], st[e + 7]));
         }
-        fence_async();
       }
+    };
+    // Half of w V as three parts, m positions of the chunk in use. The arrival also
+    // hands over S (published before) and releases the tensor memory read before.
+    auto scale = [&](const unsigned char* v, int half, int m) {
+      constexpr int UNITS = kWHalf * DV / 8 / (32 * kWorkers);   // 16-byte units per thread
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int e = tid + u * (32 * kWorkers);   // 64-column block, row, unit
+        const int blk = e / (kWHalf * 8), rem = e & (kWHalf * 8 - 1), r = half * kWHalf + (rem >> 3);
+        uint4 x = *reinterpret_cast<const uint4*>(v + blk * (kCh * 128) + half * (kWHalf * 128) + rem * 16);
+        const float w = r < m ? G[m - 1 - r] : 0.f;
+        if (r >= m) x = make_uint4(0, 0, 0, 0);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        uint32_t q0[4], q1[4], q2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(w * lo_f(xs[i]), w * hi_f(xs[i]), q0[i], q1[i], q2[i]);
+        unsigned char* dst = wv + blk * (kWHalf * 128) + rem * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+        *reinterpret_cast<uint4*>(dst + L::kPart) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+        *reinterpret_cast<uint4*>(dst + 2 * L::kPart) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+      }
+      fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(&s_ready);
+      if (lane == 0) bar_arrive(&w_ready);
+    };
+    // Outputs of chunk c: rows `row`, columns col0 .., 16 at a time (more would not
+    // fit the registers beside the state, and a spill goes to L2: shared memory
+    // leaves little L1). They go to V's tile, which is not read any more, and from
+    // there by TMA (a lane per row, stores from registers touch 32 lines each and
+    // took 2500 cycles a chunk); rows behind the end of a sequence, which a tile
+    // would overwrite, and an o that no tensor map describes, go directly.
+    auto outputs = [&](int c) {
+      if (!wait(&o_done, c & 1)) return false;
+      fence_after();
+      const int64_t t = t0 + (int64_t)c * kCh + row;
+      const float f_inter = s.scale * G[row + 1], f_intra = s.scale;
+      const bool tile = tma_out && !(ragged && c == nch - 1);
+      unsigned char* dst = vs + (c % NV) * L::kTileV + row * 128;
+      __nv_bfloat16* op = (__nv_bfloat16*)a.o + b * s.os[1] + h * s.os[2] + t * s.os[0] + col0;
+#pragma unroll
+      for (int d = 0; d < CW; d += 16) {
+        uint32_t r[16], q[16];
+        tmem_ld16(lanes + kColInter + col0 + d, r);
+        tmem_ld16(lanes + kColIntra + col0 + d, q);
+        ld_wait();
+        if (tile) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = 8 * u + 2 * e;
+              w[e] = pack2(fmaf(f_inter, __uint_as_float(r[x]), f_intra * __uint_as_float(q[x])),
+                           fmaf(f_inter, __uint_as_float(r[x + 1]), f_intra * __uint_as_float(q[x + 1])));
+            }
+            const int col = col0 + d + 8 * u;
+            *reinterpret_cast<uint4*>(dst + (col >> 6) * (kCh * 128) + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (t < end) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (col0 + d + e < s.dv)
+              op[d + e] = __float2bfloat16_rn(fmaf(f_inter, __uint_as_float(r[e]), f_intra * __uint_as_float(q[e])));
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&o_staged);
+      return true;
     };
     publish();
     bool alive = true;
     for (int c = 0; c < nch && alive; ++c) {
       const int m = min(kCh, (int)(end - t0) - c * kCh);
+      unsigned char* v = vs + (c % NV) * L::kTileV;
+      alive = wait(&v_full[c % NV], (c / NV) & 1);
+      if (!alive) break;
+      if (ragged && c == nch - 1) {
+        alive = wait(&k_full[c % NKQ], (c / NKQ) & 1);
+        if (!alive) break;
+        unsigned char* k = ks + (c % NKQ) * L::kTileK;
+        for (int e = tid; e < kCh * 8; e += 32 * kWorkers) {     // 16-byte units of a 64-column block
+          if ((e >> 3) < m) continue;
+          for (int d = 0; d < DK / 64; ++d) *reinterpret_cast<uint4*>(k + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+          for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      scale(v, 0, m);
+      if (OUT && c > 0) {
+        alive = outputs(c - 1);
+        if (!alive) break;
+      }
+      alive = wait(&w_free, c & 1);
+      if (!alive) break;
+      scale(v, 1, m);
+      if constexpr (OUT) {
+        alive = wait(&qk_done, c & 1);
+        if (!alive) break;
+        fence_after();
+        // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
+        uint32_t out[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 16) {
+          if (grp <= quarter) {
+            uint32_t r[16];
+            tmem_ld16(lanes + kColP + 32 * grp + x, r);
+            ld_wait();
+            if (grp < quarter) {
+              const float f = G[row - 32 * grp - 31];
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 g4 = *reinterpret_cast<const float4*>(&GR[x + e]);
+                out[(x + e) / 2] = pack2(__uint_as_float(r[e]) * (f * g4.x), __uint_as_float(r[e + 1]) * (f * g4.y));
+                out[(x + e) / 2 + 1] = pack2(__uint_as_float(r[e + 2]) * (f * g4.z), __uint_as_float(r[e + 3]) * (f * g4.w));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 2)
+                out[(x + e) / 2] = pack2(x + e <= lane ? __uint_as_float(r[e]) * GD[31 + lane - x - e] : 0.f,
+                                         x + e + 1 <= lane ? __uint_as_float(r[e + 1]) * GD[30 + lane - x - e] : 0.f);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[x / 2 + e] = 0;
+          }
+        }
+        // P takes the place of scores that the other warps of these rows read
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+        tmem_st16(lanes + kColP + 16 * grp, out);
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&p_ready);
+      }
       alive = wait(&kv_done, c & 1);
       if (!alive) break;
       fence_after();
-      const float gm = G[m];
+      {
+        const float gm = G[m];
 #pragma unroll
-      for (int e = 0; e < CW; e += 32) {
-        uint32_t r[32];
-        tmem_ld32(at + e, r);
-        ld_wait();
+        for (int d = 0; d < CW; d += 16) {
+          uint32_t r[16];
+          tmem_ld16(lanes + kColKV + col0 + d, r);
+          ld_wait();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) st[e + x] = fmaf(gm, st[e + x], __uint_as_float(r[x]));
+          for (int e = 0; e < 16; ++e) st[d + e] = fmaf(gm, st[d + e], __uint_as_float(r[e]));
+        }
       }
-      publish();
+      if constexpr (OUT) {
+        alive = wait(&qs_done, c & 1);             // the state before is not read any more
+        if (!alive) break;
+        publish();
+      }
     }
+    if (OUT && alive && nch > 0) alive = outputs(nch - 1);
     if (!alive) give_up();
     float* dst = nullptr;
     if constexpr (!OUT) dst = ws + (size_t)(seg + 1) * slot;
@@ -303,58 +364,6 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           if (col0 + e < s.dv) dst[e] = st[e];
       }
     }
-  } else if (warp < kMmaWarp) {
-    // ------------------------------------------------------------ w V as three bf16 parts
-    const int lt = tid - 32 * (kOutWarps + kStateWarps);   // 0..127
-    constexpr int UNITS = kWHalf * DV / 8 / (32 * kScaleWarps);   // 16-byte units per thread and half
-    bool alive = true;
-    for (int c = 0; c < nch && alive; ++c) {
-      const int m = min(kCh, (int)(end - t0) - c * kCh);
-      const int tv = tile_of(c, TILES - 1), tk = tile_of(c, 0);
-      unsigned char* v = tile_at(tv);
-      alive = wait(&full[tv % kSlots], (tv / kSlots) & 1);
-      if (!alive) break;
-      if (ragged && c == nch - 1) {
-        alive = wait(&full[tk % kSlots], (tk / kSlots) & 1);
-        if (!alive) break;
-        unsigned char* k = tile_at(tk);
-        for (int e = lt; e < kCh * 8; e += 32 * kScaleWarps) {   // 16-byte units of a 64-column block
-          if ((e >> 3) < m) continue;
-          for (int d = 0; d < DK / 64; ++d) *reinterpret_cast<uint4*>(k + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-          for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async();
-        asm volatile("bar.sync 1, %0;" ::"r"(32 * kScaleWarps) : "memory");
-        if (lane == 0) bar_arrive(&fixed);
-      }
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int use = 2 * c + half;
-        if (use > 0) {
-          alive = wait(&w_free, (use - 1) & 1);
-          if (!alive) break;
-        }
-#pragma unroll 4
-        for (int u = 0; u < UNITS; ++u) {
-          const int e = lt + u * (32 * kScaleWarps);       // unit of the half tile: 64-column block, row, unit
-          const int blk = e / (kWHalf * 8), rem = e & (kWHalf * 8 - 1), row = half * kWHalf + (rem >> 3);
-          const uint4 x = *reinterpret_cast<const uint4*>(v + blk * (kCh * 128) + half * (kWHalf * 128) + rem * 16);
-          const float w = row < m ? G[m - 1 - row] : 0.f;
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-          uint32_t q0[4], q1[4], q2[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) split3(w * lo_f(xs[i]), w * hi_f(xs[i]), q0[i], q1[i], q2[i]);
-          unsigned char* dst = wv + blk * (kWHalf * 128) + rem * 16;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
-          *reinterpret_cast<uint4*>(dst + L::kPart) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-          *reinterpret_cast<uint4*>(dst + 2 * L::kPart) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&w_ready);
-      }
-    }
-    if (!alive) give_up();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     const bool issuer = elect_one();
@@ -364,35 +373,30 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     bool alive = true;
     // K^T (w V) over half of the chunk, smallest parts first; rows 64..127 of a
     // 64-dimensional K repeat the first ones and are not read.
-    auto kv_half = [&](int c, int half) {
-      const uint32_t ka = saddr(tile_at(tile_of(c, 0)));
-      if (!wait(&w_ready, half)) return false;             // uses 2c + half
-      fence_after();
-      if (issuer) {
+    auto kv_half = [&](uint32_t ka, int half) {
 #pragma unroll
-        for (int part = 2; part >= 0; --part)
+      for (int part = 2; part >= 0; --part)
 #pragma unroll
-          for (int k = 0; k < kWHalf / 16; ++k)
-            mma(tmem + kColKV, desc_mn(ka + (half * kWHalf + 16 * k) * 128, DK == 128 ? kCh * 128 : 0),
-                desc_mn(wa + part * L::kPart + 16 * k * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || k > 0);
-        commit(&w_free);
-        if (half == 1) commit(&kv_done);
-      }
-      __syncwarp();
-      return true;
+        for (int k = 0; k < kWHalf / 16; ++k)
+          mma(tmem + kColKV, desc_mn(ka + (half * kWHalf + 16 * k) * 128, DK == 128 ? kCh * 128 : 0),
+              desc_mn(wa + part * L::kPart + 16 * k * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || k > 0);
     };
     for (int c = 0; c < nch && alive; ++c) {
-      const int tk = tile_of(c, 0), tv = tile_of(c, TILES - 1);
-      alive = wait(&full[tk % kSlots], (tk / kSlots) & 1);
-      if (alive && ragged && c == nch - 1) alive = wait(&fixed, 0);
+      const int sk = c % NKQ, sv = c % NV;
+      const uint32_t ka = saddr(ks + sk * L::kTileK), qa = saddr(qs + sk * L::kTileK), va = saddr(vs + sv * L::kTileV);
+      alive = wait(&k_full[sk], (c / NKQ) & 1) && wait(&w_ready, 0);      // use 2c
       if (!alive) break;
+      fence_after();
+      if (issuer) {
+        kv_half(ka, 0);
+        commit(&w_free);
+      }
+      __syncwarp();
       if constexpr (OUT) {
-        const int tq = tile_of(c, 1);
         // the scores replace P, which the product before reads
-        alive = wait(&full[tq % kSlots], (tq / kSlots) & 1) && (c == 0 || wait(&o_done, (c - 1) & 1));
+        alive = wait(&q_full[sk], (c / NKQ) & 1) && (c == 0 || wait(&o_done, (c - 1) & 1));
         if (!alive) break;
         fence_after();
-        const uint32_t ka = saddr(tile_at(tk)), qa = saddr(tile_at(tq)), va = saddr(tile_at(tv));
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k) {
@@ -402,18 +406,28 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           commit(&qk_done);
         }
         __syncwarp();
-        alive = wait(&s_ready, c & 1) && (c == 0 || wait(&o_free, (c - 1) & 1));
-        if (!alive) break;
-        fence_after();
-        if (issuer) {
+      }
+      alive = wait(&w_ready, 1);                                          // use 2c + 1
+      if (!alive) break;
+      fence_after();
+      if (issuer) {
+        kv_half(ka, 1);
+        commit(&kv_done);
+        commit(&k_empty[sk]);
+        if constexpr (OUT) {
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
             mma(tmem + kColInter, desc_k(qa + (k / 4) * (kCh * 128) + (k % 4) * 32), desc_mn(sa + 16 * k * 128, DK * 128),
                 id_qs, k > 0);
-          commit(&empty[tq % kSlots]);
+          commit(&qs_done);
+          commit(&q_empty[sk]);
+        } else {
+          commit(&v_empty[sv]);
         }
-        __syncwarp();
-        alive = kv_half(c, 0) && wait(&p_ready, c & 1);
+      }
+      __syncwarp();
+      if constexpr (OUT) {
+        alive = wait(&p_ready, c & 1);
         if (!alive) break;
         fence_after();
         if (issuer) {
@@ -423,17 +437,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           commit(&o_done);
         }
         __syncwarp();
-      } else {
-        alive = wait(&s_ready, c & 1) && kv_half(c, 0);
-        if (!alive) break;
       }
-      alive = kv_half(c, 1);
-      if (!alive) break;
-      if (issuer) {
-        commit(&empty[tk % kSlots]);
-        commit(&empty[tv % kSlots]);
-      }
-      __syncwarp();
     }
     if (!alive) give_up();
     // shared and tensor memory are released only once the MMAs issued are done
@@ -441,32 +445,70 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     __syncwarp();
     bar_wait(&drained, 0, kDefaultWaitLimit);
   } else {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ TMA
     const bool issuer = elect_one();
     bool alive = true;
-    int t = 0;
-    const int total = nch * TILES;
-    for (; t < total && alive; ++t) {
-      const int c = t / TILES, which = t - c * TILES, sl = t % kSlots;
-      if (t >= kSlots) {
-        alive = wait(&empty[sl], (t / kSlots - 1) & 1);
-        if (!alive) break;
-      }
+    int nk = 0, nq = 0, nv = 0;                    // tiles asked for
+    auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, int c, int zb, int zh) {
       if (issuer) {
-        const int pos = (int)t0 + c * kCh;
-        unsigned char* dst = tile_at(t);
-        const bool is_v = which == TILES - 1, is_k = which == 0;
-        const int D = is_v ? DV : DK;
-        bar_expect(&full[sl], D * 2 * kCh);
-        const CUtensorMap* map = is_v ? &vmap : is_k ? &kmap : &qmap;
-        const int mb = is_v ? mul.vb : is_k ? mul.kb : mul.qb, mh = is_v ? mul.vh : is_k ? mul.kh : mul.qh;
-        for (int d = 0; d < D; d += 64) tma_4d(dst + (d / 64) * (kCh * 128), map, &full[sl], d, pos, b * mb, h * mh);
+        bar_expect(bar, D * 2 * kCh);
+        for (int d = 0; d < D; d += 64) tma_4d(dst + (d / 64) * (kCh * 128), &map, bar, d, (int)t0 + c * kCh, zb, zh);
       }
       __syncwarp();
+    };
+    auto load_v = [&](int c) {
+      load(vs + (c % NV) * L::kTileV, DV, vmap, &v_full[c % NV], c, b * mul.vb, h * mul.vh);
+      ++nv;
+    };
+    auto load_k = [&](int c) {
+      load(ks + (c % NKQ) * L::kTileK, DK, kmap, &k_full[c % NKQ], c, b * mul.kb, h * mul.kh);
+      ++nk;
+    };
+    auto load_q = [&](int c) {
+      load(qs + (c % NKQ) * L::kTileK, DK, qmap, &q_full[c % NKQ], c, b * mul.qb, h * mul.qh);
+      ++nq;
+    };
+    for (int c = 0; c < NKQ && c < nch; ++c) {
+      load_v(c);
+      load_k(c);
+      if constexpr (OUT) load_q(c);
+    }
+    for (int c = NKQ; c < NV && c < nch; ++c) load_v(c);
+    for (int c = 0; c < nch; ++c) {                // what follows chunk c
+      if (c + NKQ < nch) {
+        alive = wait(&k_empty[c % NKQ], (c / NKQ) & 1);
+        if (!alive) break;
+        load_k(c + NKQ);
+        if constexpr (OUT) {
+          alive = wait(&q_empty[c % NKQ], (c / NKQ) & 1);
+          if (!alive) break;
+          load_q(c + NKQ);
+        }
+      }
+      if constexpr (OUT) {
+        alive = wait(&o_staged, c & 1);
+        if (!alive) break;
+        if (issuer && tma_out && !(ragged && c == nch - 1)) {
+          for (int d = 0; d < DV; d += 64)
+            tma_store_4d(&omap, vs + (c % NV) * L::kTileV + (d / 64) * (kCh * 128), d, (int)t0 + c * kCh, b, h);
+          bulk_commit();
+          bulk_wait_read();                        // the tile may be loaded into again
+        }
+        __syncwarp();
+        if (c + NV < nch) load_v(c + NV);
+      } else if (c + NV < nch) {
+        alive = wait(&v_empty[c % NV], (c / NV) & 1);
+        if (!alive) break;
+        load_v(c + NV);
+      }
     }
     if (!alive) give_up();
     // no copy of this CTA may still be in flight when it ends
-    for (int i = t > kSlots ? t - kSlots : 0; i < t; ++i) bar_wait(&full[i % kSlots], (i / kSlots) & 1, kDefaultWaitLimit);
+    if (issuer) bulk_wait();
+    __syncwarp();
+    for (int i = max(0, nv - NV); i < nv; ++i) bar_wait(&v_full[i % NV], (i / NV) & 1, kDefaultWaitLimit);
+    for (int i = max(0, nk - NKQ); i < nk; ++i) bar_wait(&k_full[i % NKQ], (i / NKQ) & 1, kDefaultWaitLimit);
+    for (int i = max(0, nq - NKQ); i < nq; ++i) bar_wait(&q_full[i % NKQ], (i / NKQ) & 1, kDefaultWaitLimit);
   }
   fence_before();
   __syncthreads();
@@ -495,13 +537,13 @@ bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const La
 template <int DK, int DV>
 cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
   constexpr size_t smem = LaSmem<DK, DV>::bytes;
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm, om{};
   LaMul mul{};
+  int ob, oh;
   if (!map_heads(&qm, a.q, s.qs, s, s.dk, &mul.qb, &mul.qh) || !map_heads(&km, a.k, s.ks, s, s.dk, &mul.kb, &mul.kh) ||
       !map_heads(&vm, a.v, s.vs, s, s.dv, &mul.vb, &mul.vh))
     return cudaErrorInvalidValue;
-  const bool out16 = ((uintptr_t)a.o & 15) == 0 && s.dv % 8 == 0 && (s.n == 1 || s.os[0] % 8 == 0) &&
-                     (s.B == 1 || s.os[1] % 8 == 0) && (s.H == 1 || s.os[2] % 8 == 0);
+  const bool tma_out = mappable(a.o, s.os, s) && map_heads(&om, a.o, s.os, s, s.dv, &ob, &oh);
   const bool state16 = s.dv % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -516,12 +558,12 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t
   cudaError_t e;
   if (p.G > 1) {
     if ((e = allow_smem<k_linattn_tc<DK, DV, false>>(smem)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, false>, s, p, a, qm, km, vm, mul, (int)out16, (int)state16,
+    if ((e = cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, false>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
                                 (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
   if ((e = allow_smem<k_linattn_tc<DK, DV, true>>(smem)) != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, true>, s, p, a, qm, km, vm, mul, (int)out16, (int)state16,
+  return cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, true>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
                             (int)kDefaultWaitLimit);
 }
 

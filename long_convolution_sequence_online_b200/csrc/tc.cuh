@@ -40,19 +40,24 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
       : "=r"(ok) : "r"(saddr(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
-// Bounded waits: the first gives up after `limit` checks, the second also once
-// another role of the CTA has given up.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int limit) {
-  for (int it = 0; it < limit; ++it)
-    if (bar_try(bar, parity)) return true;
-  return false;
-}
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag) {
+// Bounded waits of a whole warp (or of a single thread: the first form), which give
+// up after `limit` checks; the second also once another role of the CTA has given
+// up. A phase that is complete already, the usual case in a pipeline, is seen by
+// the first check: 45 cycles, where the loop around it costs 160.
+static __device__ __noinline__ bool bar_wait_loop(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag) {
   for (int it = 0; it < limit; ++it) {
     if (bar_try(bar, parity)) return true;
-    if (*abort_flag) return false;
+    if (abort_flag && *abort_flag) return false;
   }
   return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag = nullptr) {
+  if (limit > 0 && bar_try(bar, parity)) return true;
+  return bar_wait_loop(bar, parity, limit, abort_flag);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag) {
+  if (limit > 0 && __all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+  return __all_sync(0xffffffffu, bar_wait_loop(bar, parity, limit, abort_flag));
 }
 
 // ---------------------------------------------------------------- TMA
@@ -66,6 +71,14 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
       ::"r"(saddr(dst)), "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+// From shared memory; parts outside the tensor are not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+               ::"l"(map), "r"(saddr(src)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
