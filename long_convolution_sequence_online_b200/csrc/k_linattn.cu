@@ -330,7 +330,7 @@ size_t linattn_prefill_workspace(const LaShape& s, int num_sms) {
 }
 
 cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sms, cudaStream_t st) {
-  if (linattn_tc_fits(s, a)) return launch_linattn_tc(s, linattn_tc_plan(s, num_sms), a, st);
+  if (linattn_tc_fits(s, a)) return launch_linattn_tc(s, linattn_tc_plan(s, num_sms), a, num_sms, st);
   const LaPlan p = la_plan(s, num_sms);
   return s.bf16 ? prefill_dk<__nv_bfloat16>(s, p, a, st) : prefill_dk<float>(s, p, a, st);
 }

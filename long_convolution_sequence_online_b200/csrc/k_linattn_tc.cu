@@ -24,8 +24,11 @@
 // run in the order KV (first half), Q K^T, KV (second half), Q S, P V. Each phase
 // of the workers then overlaps MMAs that do not need it, and an arrival on
 // w_ready tells the issuer that everything before it in the workers' order is done
-// as well. (Warps with a role each - P and outputs 4, state 8, w V 4 - took 10400
-// cycles a chunk at 128 x 128: a role's few warps do not hide their latency.)
+// as well. CTAs are persistent: the copies run ahead into the next task. (Warps
+// with a role each - P and outputs 4, state 8, w V 4 - took 10400 cycles a chunk at
+// 128 x 128, two groups of eight, w V and state beside P and outputs, 9000: a few
+// warps do not hide their own latency, and more code at a time misses the
+// instruction cache.)
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -50,8 +53,11 @@ struct LaSmem {
   static constexpr int kSlotsKQ = DK == 128 && DV == 128 ? 1 : 2, kSlotsV = 2;
   static constexpr int kTileK = kCh * 2 * DK, kTileV = kCh * 2 * DV;
   static constexpr int kPart = kWHalf * 2 * DV;
+  // the state passes through in fp32 rows of 64 columns and 16 bytes on its way in and out
+  static constexpr int kLd = 64 + 4, kStage = 128 * kLd * 4;
+  static constexpr int kW = 3 * kPart > kStage ? 3 * kPart : kStage;
   static constexpr int kState = DK * 2 * DV;
-  static constexpr size_t bytes = 1024 + (size_t)2 * kSlotsKQ * kTileK + kSlotsV * kTileV + 3 * kPart + kState;
+  static constexpr size_t bytes = 1024 + (size_t)2 * kSlotsKQ * kTileK + kSlotsV * kTileV + kW + kState;
 };
 
 // Coordinates of a tensor map [dim][position][sequence][head]; a stride of 0
@@ -63,6 +69,29 @@ struct LaMul {
 // TMEM columns.
 constexpr uint32_t kColP = 0, kColInter = 128, kColIntra = 256, kColKV = 384;
 
+// What a CTA does for one (sequence, head) and segment.
+struct LaTask {
+  int bh, b, h, seg, len, end, nch;
+  int64_t t0;
+  bool ragged;    // the last chunk ends inside a longer batch: what stands behind is cleared in the tiles
+};
+template <bool OUT>
+__device__ __forceinline__ LaTask la_task(const LaShape& s, const LaPlan& p, const LaPtrs& a, int i) {
+  LaTask t;
+  t.bh = i % (s.B * s.H);                // segments of a head far apart: the early ones end first
+  t.seg = i / (s.B * s.H);
+  t.b = t.bh / s.H;
+  t.h = t.bh - t.b * s.H;
+  t.len = la_length(a.lengths, t.b, s.n);
+  t.t0 = (int64_t)t.seg * p.seg;
+  t.end = (int)min((int64_t)t.len, t.t0 + p.seg);
+  // the state's launch skips a segment that none follows
+  const bool work = OUT ? t.t0 < t.len : t.t0 + p.seg < t.len;
+  t.nch = work ? (int)((t.end - t.t0 + kCh - 1) / kCh) : 0;
+  t.ragged = t.end == t.len && t.len < s.n && (t.end - t.t0) % kCh != 0;
+  return t;
+}
+
 template <int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
@@ -70,43 +99,25 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
              const __grid_constant__ CUtensorMap omap, LaMul mul, int tma_out, int vec_state, int wait_limit) {
   using L = LaSmem<DK, DV>;
   constexpr int NKQ = L::kSlotsKQ, NV = L::kSlotsV;
-  constexpr int CW = DV / 4;             // a worker's columns of the state and of the outputs
+  constexpr int CW = DV / 4;             // a warp's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: not with outputs
   __shared__ uint64_t w_ready, w_free, qk_done, kv_done, qs_done, p_ready, o_done, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
-  __shared__ float GD[63];               // GD[31 + i] = g^i, i = 0 .. 31 (masked below)
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
+  __shared__ float GD[63];               // GD[31 + i] = g^i, i = 0 .. 31 (masked below)
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   unsigned char* ks = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
   unsigned char* qs = ks + NKQ * L::kTileK;
   unsigned char* vs = qs + NKQ * L::kTileK;
-  unsigned char* wv = vs + NV * L::kTileV;
-  unsigned char* sop = wv + 3 * L::kPart;
+  unsigned char* sop = vs + NV * L::kTileV;
+  unsigned char* wv = sop + L::kState;
   pdl_launch_dependents();
-  pdl_wait_primary();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H, seg = blockIdx.y;
-  const int len = la_length(a.lengths, b, s.n);
-  const int64_t t0 = (int64_t)seg * p.seg;
+  const int tasks = s.B * s.H * p.G;
   const size_t slot = (size_t)s.dk * s.dv;
-  float* ws = a.ws ? a.ws + (size_t)bh * p.G * slot : nullptr;
-  const float* s_in = a.state_in ? a.state_in + (size_t)bh * slot : nullptr;
-  if constexpr (!OUT) {
-    if (seg == 0 && s_in)
-      for (size_t e = tid; e < slot; e += kLaTcThreads) ws[e] = s_in[e];
-    if (t0 + p.seg >= len) return;       // no segment after this one
-  } else {
-    if (t0 >= len && seg > 0) return;
-  }
-  const int end = (int)min((int64_t)len, t0 + p.seg);
-  const int nch = (int)((end - t0 + kCh - 1) / kCh);
-  const float ld2 = la_log2_decay(__ldg(a.log_decay + h));
   if (warp == 0) tmem_alloc(&tmem_s, 512);
-  if (tid >= 64 && tid < 64 + kCh + 1) G[tid - 64] = la_pow(ld2, tid - 64);
-  if (tid >= 256 && tid < 288) GR[tid - 256] = la_pow(ld2, 31 - (tid - 256));
-  if (tid >= 288 && tid < 288 + 63) GD[tid - 288] = la_pow(ld2, max(0, tid - 288 - 31));
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&k_full[i], 1);
@@ -131,21 +142,24 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   fence_before();
   __syncthreads();
   fence_after();
+  pdl_wait_primary();
   const uint32_t tmem = tmem_s;
   volatile int* abort_flag = &abort_s;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return warp_wait(bar, parity, wait_limit, abort_flag);
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, wait_limit, abort_flag); };
   auto give_up = [&]() {
     if (lane == 0) {
       *abort_flag = 1;
       atomicExch(&g_linattn_error, 1);
     }
   };
-
-  // The last chunk of a sequence shorter than the batch: what stands behind its
-  // end (anything, NaN too) is cleared in the tiles before they are multiplied.
-  const bool ragged = end == len && len < s.n && (end - t0) % kCh != 0;
+  // The arithmetic warps meet at barriers of their own, so after a wait that gave up
+  // they run on to the end (no wait lasts any more, the results are not valid).
+  auto need = [&](uint64_t* bar, uint32_t parity) {
+    if (!wait(bar, parity)) give_up();
+  };
+  // `it` counts a CTA's chunks over all its tasks; barrier phases go by it.
+  bool alive = true;
+  int it = 0;
 
   if (warp < kWorkers) {
     // ------------------------------------------------------------ workers
@@ -153,33 +167,9 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     const int row = 32 * quarter + lane;           // of the chunk (P, outputs) and of the state (key dimension)
     const int col0 = grp * CW;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    float* stage = reinterpret_cast<float*>(wv);   // [128][kLd], when w V is not in use
+    auto sync = [] { asm volatile("bar.sync 5, %0;" ::"n"(32 * kWorkers) : "memory"); };
     float st[CW];                                  // S, row `row`, columns col0 ..
-#pragma unroll
-    for (int e = 0; e < CW; ++e) st[e] = 0.f;
-    if constexpr (OUT) {
-      const float* src = p.G > 1 ? ws : s_in;
-      if (src && row < s.dk)
-        for (int g = s_in ? 0 : 1; g <= seg; ++g) {
-          // slot 0: the state before the prompt; slot g: segment g - 1's contribution
-          const float f = la_pow(ld2, (g == 0 ? seg : seg - g) * p.seg);
-          const float* sp = src + (size_t)g * slot + (size_t)row * s.dv + col0;
-          if (vec_state) {
-#pragma unroll
-            for (int e = 0; e < CW; e += 4)
-              if (col0 + e < s.dv) {
-                const float4 v = *reinterpret_cast<const float4*>(sp + e);
-                st[e] = fmaf(f, v.x, st[e]);
-                st[e + 1] = fmaf(f, v.y, st[e + 1]);
-                st[e + 2] = fmaf(f, v.z, st[e + 2]);
-                st[e + 3] = fmaf(f, v.w, st[e + 3]);
-              }
-          } else {
-#pragma unroll
-            for (int e = 0; e < CW; ++e)
-              if (col0 + e < s.dv) st[e] = fmaf(f, sp[e], st[e]);
-          }
-        }
-    }
     // S as the B operand of Q S: rows of 64 bf16 columns, 128-byte swizzle.
     auto publish = [&]() {
       if (OUT && row < DK) {
@@ -217,120 +207,171 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       __syncwarp();
       if (lane == 0) bar_arrive(&w_ready);
     };
-    // Outputs of chunk c: rows `row`, columns col0 .., 16 at a time (more would not
-    // fit the registers beside the state, and a spill goes to L2: shared memory
-    // leaves little L1). They go to V's tile, which is not read any more, and from
-    // there by TMA (a lane per row, stores from registers touch 32 lines each and
-    // took 2500 cycles a chunk); rows behind the end of a sequence, which a tile
-    // would overwrite, and an o that no tensor map describes, go directly.
-    auto outputs = [&](int c) {
-      if (!wait(&o_done, c & 1)) return false;
+    // Outputs of a task's chunk c (the CTA's chunk j): rows `row`, columns col0 .., 16 at
+    // a time (more would not fit the registers beside the state, and a spill goes to
+    // L2: shared memory leaves little L1). They go to V's tile, which is not read any
+    // more, and from there by TMA (a lane per row, stores from registers touch 32
+    // lines each and took 2500 cycles a chunk); rows behind the end of a sequence,
+    // which a tile would overwrite, and an o that no tensor map describes, go directly.
+    auto outputs = [&](const LaTask& k, int c, int j) {
+      need(&o_done, j & 1);
       fence_after();
-      const int64_t t = t0 + (int64_t)c * kCh + row;
+      const int64_t t = k.t0 + (int64_t)c * kCh + row;
       const float f_inter = s.scale * G[row + 1], f_intra = s.scale;
-      const bool tile = tma_out && !(ragged && c == nch - 1);
-      unsigned char* dst = vs + (c % NV) * L::kTileV + row * 128;
-      __nv_bfloat16* op = (__nv_bfloat16*)a.o + b * s.os[1] + h * s.os[2] + t * s.os[0] + col0;
+      const bool tile = tma_out && !(k.ragged && c == k.nch - 1);
+      unsigned char* dst = vs + (j % NV) * L::kTileV + row * 128;
+      __nv_bfloat16* op = (__nv_bfloat16*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + col0;
 #pragma unroll
       for (int d = 0; d < CW; d += 16) {
         uint32_t r[16], q[16];
         tmem_ld16(lanes + kColInter + col0 + d, r);
         tmem_ld16(lanes + kColIntra + col0 + d, q);
         ld_wait();
-        if (tile) {
+        uint32_t w[8];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t w[4];
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack2(fmaf(f_inter, __uint_as_float(r[2 * e]), f_intra * __uint_as_float(q[2 * e])),
+                       fmaf(f_inter, __uint_as_float(r[2 * e + 1]), f_intra * __uint_as_float(q[2 * e + 1])));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int x = 8 * u + 2 * e;
-              w[e] = pack2(fmaf(f_inter, __uint_as_float(r[x]), f_intra * __uint_as_float(q[x])),
-                           fmaf(f_inter, __uint_as_float(r[x + 1]), f_intra * __uint_as_float(q[x + 1])));
+        for (int u = 0; u < 2; ++u) {
+          const int col = col0 + d + 8 * u;
+          const uint4 v = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+          if (tile) {
+            *reinterpret_cast<uint4*>(dst + (col >> 6) * (kCh * 128) + ((((col & 63) >> 3) ^ (row & 7)) << 4)) = v;
+          } else if (t < k.end) {
+            if (tma_out && col + 8 <= s.dv) {
+              *reinterpret_cast<uint4*>(op + d + 8 * u) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (col + e < s.dv)
+                  reinterpret_cast<unsigned short*>(op)[d + 8 * u + e] = (unsigned short)(w[4 * u + e / 2] >> (16 * (e & 1)));
             }
-            const int col = col0 + d + 8 * u;
-            *reinterpret_cast<uint4*>(dst + (col >> 6) * (kCh * 128) + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else if (t < end) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (col0 + d + e < s.dv)
-              op[d + e] = __float2bfloat16_rn(fmaf(f_inter, __uint_as_float(r[e]), f_intra * __uint_as_float(q[e])));
         }
       }
       fence_async();
+      fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&o_staged);
-      return true;
     };
-    publish();
-    bool alive = true;
-    for (int c = 0; c < nch && alive; ++c) {
-      const int m = min(kCh, (int)(end - t0) - c * kCh);
-      unsigned char* v = vs + (c % NV) * L::kTileV;
-      alive = wait(&v_full[c % NV], (c / NV) & 1);
-      if (!alive) break;
-      if (ragged && c == nch - 1) {
-        alive = wait(&k_full[c % NKQ], (c / NKQ) & 1);
-        if (!alive) break;
-        unsigned char* k = ks + (c % NKQ) * L::kTileK;
-        for (int e = tid; e < kCh * 8; e += 32 * kWorkers) {     // 16-byte units of a 64-column block
-          if ((e >> 3) < m) continue;
-          for (int d = 0; d < DK / 64; ++d) *reinterpret_cast<uint4*>(k + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-          for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
+      const LaTask k = la_task<OUT>(s, p, a, i);
+      float* ws = a.ws ? a.ws + (size_t)k.bh * p.G * slot : nullptr;
+      const float* s_in = a.state_in ? a.state_in + (size_t)k.bh * slot : nullptr;
+      if (!OUT && k.seg == 0 && s_in)
+        for (size_t e = tid; e < slot; e += 32 * kWorkers) ws[e] = s_in[e];
+      if (k.nch == 0 && !(OUT && k.seg == 0 && k.len == 0)) continue;
+      const float ld2 = la_log2_decay(__ldg(a.log_decay + k.h));
+      sync();                                      // the task before is done with the tables and the stage
+      if (tid <= kCh) G[tid] = la_pow(ld2, tid);
+      if (tid >= 160 && tid < 192) GR[tid - 160] = la_pow(ld2, 191 - tid);
+      if (tid >= 192 && tid < 192 + 63) GD[tid - 192] = la_pow(ld2, max(0, tid - 192 - 31));
+#pragma unroll
+      for (int e = 0; e < CW; ++e) st[e] = 0.f;
+      const float* src = !OUT ? nullptr : p.G > 1 ? ws : s_in;
+      const int g0 = s_in ? 0 : 1;
+      constexpr int PER = DV / 8;                  // float4s of half a row of the state
+      if (src && g0 <= k.seg) {
+        // slot 0: the state before the prompt; slot g: segment g - 1's contribution
+        if (vec_state) {
+          // half of the columns at a time: along the rows into the stage, then a row per lane
+          for (int hc = 0; hc < 2; ++hc) {
+#pragma unroll
+            for (int u = 0; u < 128 * PER / (32 * kWorkers); ++u) {
+              const int e = tid + u * (32 * kWorkers), r = e / PER, c = hc * (DV / 2) + 4 * (e % PER);
+              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (r < s.dk && c < s.dv)
+                for (int g = g0; g <= k.seg; ++g) {
+                  const float f = la_pow(ld2, (g == 0 ? k.seg : k.seg - g) * p.seg);
+                  const float4 v = *reinterpret_cast<const float4*>(src + (size_t)g * slot + (size_t)r * s.dv + c);
+                  x.x = fmaf(f, v.x, x.x);
+                  x.y = fmaf(f, v.y, x.y);
+                  x.z = fmaf(f, v.z, x.z);
+                  x.w = fmaf(f, v.w, x.w);
+                }
+              *reinterpret_cast<float4*>(stage + r * L::kLd + 4 * (e % PER)) = x;
+            }
+            sync();
+            if (grp / 2 == hc) {
+#pragma unroll
+              for (int e = 0; e < CW; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(stage + row * L::kLd + (grp & 1) * CW + e);
+                st[e] = v.x; st[e + 1] = v.y; st[e + 2] = v.z; st[e + 3] = v.w;
+              }
+            }
+            sync();
+          }
+        } else if (row < s.dk) {
+          for (int g = g0; g <= k.seg; ++g) {
+            const float f = la_pow(ld2, (g == 0 ? k.seg : k.seg - g) * p.seg);
+            const float* sp = src + (size_t)g * slot + (size_t)row * s.dv + col0;
+#pragma unroll
+            for (int e = 0; e < CW; ++e)
+              if (col0 + e < s.dv) st[e] = fmaf(f, sp[e], st[e]);
+          }
         }
       }
-      scale(v, 0, m);
-      if (OUT && c > 0) {
-        alive = outputs(c - 1);
-        if (!alive) break;
-      }
-      alive = wait(&w_free, c & 1);
-      if (!alive) break;
-      scale(v, 1, m);
-      if constexpr (OUT) {
-        alive = wait(&qk_done, c & 1);
-        if (!alive) break;
-        fence_after();
-        // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
-        uint32_t out[16];
+      sync();                                      // the tables are there, the stage is free
+      publish();                                   // no Q S of the task before is left: its qs_done was waited for
+      for (int c = 0; c < k.nch; ++c, ++it) {
+        const int m = min(kCh, (int)(k.end - k.t0) - c * kCh), sv = it % NV;
+        unsigned char* v = vs + sv * L::kTileV;
+        need(&v_full[sv], (it / NV) & 1);
+        if (k.ragged && c == k.nch - 1) {
+          const int sk = it % NKQ;
+          need(&k_full[sk], (it / NKQ) & 1);
+          unsigned char* kt = ks + sk * L::kTileK;
+          for (int e = tid; e < kCh * 8; e += 32 * kWorkers) {     // 16-byte units of a 64-column block
+            if ((e >> 3) < m) continue;
+            for (int d = 0; d < DK / 64; ++d) *reinterpret_cast<uint4*>(kt + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+            for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        scale(v, 0, m);
+        if (OUT && c > 0) outputs(k, c - 1, it - 1);
+        need(&w_free, it & 1);
+        scale(v, 1, m);
+        if constexpr (OUT) {
+          need(&qk_done, it & 1);
+          fence_after();
+          // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
+          uint32_t out[16];
 #pragma unroll
-        for (int x = 0; x < 32; x += 16) {
-          if (grp <= quarter) {
-            uint32_t r[16];
-            tmem_ld16(lanes + kColP + 32 * grp + x, r);
-            ld_wait();
-            if (grp < quarter) {
-              const float f = G[row - 32 * grp - 31];
+          for (int x = 0; x < 32; x += 16) {
+            if (grp <= quarter) {
+              uint32_t r[16];
+              tmem_ld16(lanes + kColP + 32 * grp + x, r);
+              ld_wait();
+              if (grp < quarter) {
+                const float f = G[row - 32 * grp - 31];
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(&GR[x + e]);
-                out[(x + e) / 2] = pack2(__uint_as_float(r[e]) * (f * g4.x), __uint_as_float(r[e + 1]) * (f * g4.y));
-                out[(x + e) / 2 + 1] = pack2(__uint_as_float(r[e + 2]) * (f * g4.z), __uint_as_float(r[e + 3]) * (f * g4.w));
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 g4 = *reinterpret_cast<const float4*>(&GR[x + e]);
+                  out[(x + e) / 2] = pack2(__uint_as_float(r[e]) * (f * g4.x), __uint_as_float(r[e + 1]) * (f * g4.y));
+                  out[(x + e) / 2 + 1] = pack2(__uint_as_float(r[e + 2]) * (f * g4.z), __uint_as_float(r[e + 3]) * (f * g4.w));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 2)
+                  out[(x + e) / 2] = pack2(x + e <= lane ? __uint_as_float(r[e]) * GD[31 + lane - x - e] : 0.f,
+                                           x + e + 1 <= lane ? __uint_as_float(r[e + 1]) * GD[30 + lane - x - e] : 0.f);
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 16; e += 2)
-                out[(x + e) / 2] = pack2(x + e <= lane ? __uint_as_float(r[e]) * GD[31 + lane - x - e] : 0.f,
-                                         x + e + 1 <= lane ? __uint_as_float(r[e + 1]) * GD[30 + lane - x - e] : 0.f);
+              for (int e = 0; e < 8; ++e) out[x / 2 + e] = 0;
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) out[x / 2 + e] = 0;
           }
+          // P takes the place of scores that the other warps of these rows read
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+          tmem_st16(lanes + kColP + 16 * grp, out);
+          st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_ready);
         }
-        // P takes the place of scores that the other warps of these rows read
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
-        tmem_st16(lanes + kColP + 16 * grp, out);
-        st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&p_ready);
-      }
-      alive = wait(&kv_done, c & 1);
-      if (!alive) break;
-      fence_after();
-      {
+        need(&kv_done, it & 1);
+        fence_after();
         const float gm = G[m];
 #pragma unroll
         for (int d = 0; d < CW; d += 16) {
@@ -340,28 +381,36 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
           for (int e = 0; e < 16; ++e) st[d + e] = fmaf(gm, st[d + e], __uint_as_float(r[e]));
         }
+        if constexpr (OUT) {
+          need(&qs_done, it & 1);                  // the state before is not read any more
+          publish();
+        }
       }
-      if constexpr (OUT) {
-        alive = wait(&qs_done, c & 1);             // the state before is not read any more
-        if (!alive) break;
-        publish();
-      }
-    }
-    if (OUT && alive && nch > 0) alive = outputs(nch - 1);
-    if (!alive) give_up();
-    float* dst = nullptr;
-    if constexpr (!OUT) dst = ws + (size_t)(seg + 1) * slot;
-    else if (a.state_out && end == len) dst = a.state_out + (size_t)bh * slot;   // this segment holds the last position
-    if (dst && row < s.dk) {
-      dst += (size_t)row * s.dv + col0;
+      if (OUT && k.nch > 0) outputs(k, k.nch - 1, it - 1);
+      float* dst = nullptr;
+      if constexpr (!OUT) dst = ws + (size_t)(k.seg + 1) * slot;
+      else if (a.state_out && k.end == k.len) dst = a.state_out + (size_t)k.bh * slot;   // this segment holds the last position
+      if (!dst) continue;
       if (vec_state) {
+        for (int hc = 0; hc < 2; ++hc) {
+          sync();
+          if (grp / 2 == hc) {
 #pragma unroll
-        for (int e = 0; e < CW; e += 4)
-          if (col0 + e < s.dv) *reinterpret_cast<float4*>(dst + e) = make_float4(st[e], st[e + 1], st[e + 2], st[e + 3]);
-      } else {
+            for (int e = 0; e < CW; e += 4)
+              *reinterpret_cast<float4*>(stage + row * L::kLd + (grp & 1) * CW + e) = make_float4(st[e], st[e + 1], st[e + 2], st[e + 3]);
+          }
+          sync();
+#pragma unroll
+          for (int u = 0; u < 128 * PER / (32 * kWorkers); ++u) {
+            const int e = tid + u * (32 * kWorkers), r = e / PER, c = hc * (DV / 2) + 4 * (e % PER);
+            if (r < s.dk && c < s.dv)
+              *reinterpret_cast<float4*>(dst + (size_t)r * s.dv + c) = *reinterpret_cast<const float4*>(stage + r * L::kLd + 4 * (e % PER));
+          }
+        }
+      } else if (row < s.dk) {
 #pragma unroll
         for (int e = 0; e < CW; ++e)
-          if (col0 + e < s.dv) dst[e] = st[e];
+          if (col0 + e < s.dv) dst[(size_t)row * s.dv + col0 + e] = st[e];
       }
     }
   } else if (warp == kMmaWarp) {
@@ -370,73 +419,75 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     constexpr uint32_t id_qk = idesc(128, 128), id_qs = idesc(128, DV, false, true), id_pv = idesc(128, DV, false, true),
                        id_kv = idesc(128, DV, true, true);
     const uint32_t wa = saddr(wv), sa = saddr(sop);
-    bool alive = true;
     // K^T (w V) over half of the chunk, smallest parts first; rows 64..127 of a
     // 64-dimensional K repeat the first ones and are not read.
     auto kv_half = [&](uint32_t ka, int half) {
 #pragma unroll
       for (int part = 2; part >= 0; --part)
 #pragma unroll
-        for (int k = 0; k < kWHalf / 16; ++k)
-          mma(tmem + kColKV, desc_mn(ka + (half * kWHalf + 16 * k) * 128, DK == 128 ? kCh * 128 : 0),
-              desc_mn(wa + part * L::kPart + 16 * k * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || k > 0);
+        for (int x = 0; x < kWHalf / 16; ++x)
+          mma(tmem + kColKV, desc_mn(ka + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
+              desc_mn(wa + part * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || x > 0);
     };
-    for (int c = 0; c < nch && alive; ++c) {
-      const int sk = c % NKQ, sv = c % NV;
-      const uint32_t ka = saddr(ks + sk * L::kTileK), qa = saddr(qs + sk * L::kTileK), va = saddr(vs + sv * L::kTileV);
-      alive = wait(&k_full[sk], (c / NKQ) & 1) && wait(&w_ready, 0);      // use 2c
-      if (!alive) break;
-      fence_after();
-      if (issuer) {
-        kv_half(ka, 0);
-        commit(&w_free);
-      }
-      __syncwarp();
-      if constexpr (OUT) {
-        // the scores replace P, which the product before reads
-        alive = wait(&q_full[sk], (c / NKQ) & 1) && (c == 0 || wait(&o_done, (c - 1) & 1));
+    for (int i = blockIdx.x; i < tasks && alive; i += gridDim.x) {
+      const LaTask k = la_task<OUT>(s, p, a, i);
+      for (int c = 0; c < k.nch; ++c, ++it) {
+        const int sk = it % NKQ, sv = it % NV;
+        const uint32_t ka = saddr(ks + sk * L::kTileK), qa = saddr(qs + sk * L::kTileK), va = saddr(vs + sv * L::kTileV);
+        alive = wait(&k_full[sk], (it / NKQ) & 1) && wait(&w_ready, 0);   // use 2 it
         if (!alive) break;
         fence_after();
         if (issuer) {
-#pragma unroll
-          for (int k = 0; k < DK / 16; ++k) {
-            const uint32_t o = (k / 4) * (kCh * 128) + (k % 4) * 32;
-            mma(tmem + kColP, desc_k(qa + o), desc_k(ka + o), id_qk, k > 0);
-          }
-          commit(&qk_done);
+          kv_half(ka, 0);
+          commit(&w_free);
         }
         __syncwarp();
-      }
-      alive = wait(&w_ready, 1);                                          // use 2c + 1
-      if (!alive) break;
-      fence_after();
-      if (issuer) {
-        kv_half(ka, 1);
-        commit(&kv_done);
-        commit(&k_empty[sk]);
         if constexpr (OUT) {
+          // the scores replace P, which the product before reads
+          alive = wait(&q_full[sk], (it / NKQ) & 1) && (it == 0 || wait(&o_done, (it - 1) & 1));
+          if (!alive) break;
+          fence_after();
+          if (issuer) {
 #pragma unroll
-          for (int k = 0; k < DK / 16; ++k)
-            mma(tmem + kColInter, desc_k(qa + (k / 4) * (kCh * 128) + (k % 4) * 32), desc_mn(sa + 16 * k * 128, DK * 128),
-                id_qs, k > 0);
-          commit(&qs_done);
-          commit(&q_empty[sk]);
-        } else {
-          commit(&v_empty[sv]);
+            for (int x = 0; x < DK / 16; ++x) {
+              const uint32_t o = (x / 4) * (kCh * 128) + (x % 4) * 32;
+              mma(tmem + kColP, desc_k(qa + o), desc_k(ka + o), id_qk, x > 0);
+            }
+            commit(&qk_done);
+          }
+          __syncwarp();
         }
-      }
-      __syncwarp();
-      if constexpr (OUT) {
-        alive = wait(&p_ready, c & 1);
+        alive = wait(&w_ready, 1);                                        // use 2 it + 1
         if (!alive) break;
         fence_after();
         if (issuer) {
+          kv_half(ka, 1);
+          commit(&kv_done);
+          commit(&k_empty[sk]);
+          if constexpr (OUT) {
 #pragma unroll
-          for (int k = 0; k < kCh / 16; ++k)
-            mma_ta(tmem + kColIntra, tmem + kColP + 8 * k, desc_mn(va + 16 * k * 128, kCh * 128), id_pv, k > 0);
-          commit(&o_done);
+            for (int x = 0; x < DK / 16; ++x)
+              mma(tmem + kColInter, desc_k(qa + (x / 4) * (kCh * 128) + (x % 4) * 32), desc_mn(sa + 16 * x * 128, DK * 128),
+                  id_qs, x > 0);
+            commit(&qs_done);
+            commit(&q_empty[sk]);
+          } else {
+            commit(&v_empty[sv]);
+          }
         }
         __syncwarp();
+        if constexpr (OUT) {
+          alive = wait(&p_ready, it & 1);
+          if (!alive) break;
+          fence_after();
+          if (issuer) {
+#pragma unroll
+            for (int x = 0; x < kCh / 16; ++x)
+              mma_ta(tmem + kColIntra, tmem + kColP + 8 * x, desc_mn(va + 16 * x * 128, kCh * 128), id_pv, x > 0);
+            commit(&o_done);
+          }
+          __syncwarp();
+        }
       }
     }
     if (!alive) give_up();
@@ -446,69 +497,93 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     bar_wait(&drained, 0, kDefaultWaitLimit);
   } else {
     // ------------------------------------------------------------ TMA
+    // Loads of chunk `it` go out as soon as the tiles' last readers are done, over
+    // the ends of tasks: a walk ahead (nk, nv: chunks whose K and Q, V were asked
+    // for), behind it the walk of the outputs.
     const bool issuer = elect_one();
-    bool alive = true;
-    int nk = 0, nq = 0, nv = 0;                    // tiles asked for
-    auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, int c, int zb, int zh) {
+    struct Walk {
+      int i, c, j;                                           // task, its chunk, the CTA's chunk
+      LaTask k;
+    };
+    auto settle = [&](Walk& w) {                             // on to a task with a chunk left
+      while (w.i < tasks && w.c >= w.k.nch) {
+        w.i += gridDim.x;
+        w.c = 0;
+        if (w.i < tasks) w.k = la_task<OUT>(s, p, a, w.i);
+      }
+    };
+    auto next = [&](Walk& w) {
+      ++w.c;
+      ++w.j;
+      settle(w);
+    };
+    Walk wk{(int)blockIdx.x, 0, 0, la_task<OUT>(s, p, a, min((int)blockIdx.x, tasks - 1))};
+    settle(wk);
+    Walk wv_ = wk, wo = wk;
+    auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, const Walk& w, int zb, int zh) {
       if (issuer) {
         bar_expect(bar, D * 2 * kCh);
-        for (int d = 0; d < D; d += 64) tma_4d(dst + (d / 64) * (kCh * 128), &map, bar, d, (int)t0 + c * kCh, zb, zh);
+        for (int d = 0; d < D; d += 64) tma_4d(dst + (d / 64) * (kCh * 128), &map, bar, d, (int)w.k.t0 + w.c * kCh, zb, zh);
       }
       __syncwarp();
     };
-    auto load_v = [&](int c) {
-      load(vs + (c % NV) * L::kTileV, DV, vmap, &v_full[c % NV], c, b * mul.vb, h * mul.vh);
-      ++nv;
+    auto load_v = [&]() {
+      load(vs + (wv_.j % NV) * L::kTileV, DV, vmap, &v_full[wv_.j % NV], wv_, wv_.k.b * mul.vb, wv_.k.h * mul.vh);
+      next(wv_);
     };
-    auto load_k = [&](int c) {
-      load(ks + (c % NKQ) * L::kTileK, DK, kmap, &k_full[c % NKQ], c, b * mul.kb, h * mul.kh);
-      ++nk;
+    auto load_k = [&]() {
+      load(ks + (wk.j % NKQ) * L::kTileK, DK, kmap, &k_full[wk.j % NKQ], wk, wk.k.b * mul.kb, wk.k.h * mul.kh);
     };
-    auto load_q = [&](int c) {
-      load(qs + (c % NKQ) * L::kTileK, DK, qmap, &q_full[c % NKQ], c, b * mul.qb, h * mul.qh);
-      ++nq;
+    auto load_q = [&]() {
+      load(qs + (wk.j % NKQ) * L::kTileK, DK, qmap, &q_full[wk.j % NKQ], wk, wk.k.b * mul.qb, wk.k.h * mul.qh);
     };
-    for (int c = 0; c < NKQ && c < nch; ++c) {
-      load_v(c);
-      load_k(c);
-      if constexpr (OUT) load_q(c);
+    for (int c = 0; c < NV; ++c) {
+      if (wv_.i < tasks) load_v();
+      if (c < NKQ && wk.i < tasks) {
+        load_k();
+        if constexpr (OUT) load_q();
+        next(wk);
+      }
     }
-    for (int c = NKQ; c < NV && c < nch; ++c) load_v(c);
-    for (int c = 0; c < nch; ++c) {                // what follows chunk c
-      if (c + NKQ < nch) {
-        alive = wait(&k_empty[c % NKQ], (c / NKQ) & 1);
+    for (; wo.i < tasks && alive; next(wo)) {                // what follows chunk wo.j
+      const int j = wo.j;
+      if (wk.i < tasks) {                                    // chunk j + NKQ
+        alive = wait(&k_empty[j % NKQ], (j / NKQ) & 1);
         if (!alive) break;
-        load_k(c + NKQ);
+        load_k();
         if constexpr (OUT) {
-          alive = wait(&q_empty[c % NKQ], (c / NKQ) & 1);
+          alive = wait(&q_empty[j % NKQ], (j / NKQ) & 1);
           if (!alive) break;
-          load_q(c + NKQ);
+          load_q();
         }
+        next(wk);
       }
       if constexpr (OUT) {
-        alive = wait(&o_staged, c & 1);
+        alive = wait(&o_staged, j & 1);
         if (!alive) break;
-        if (issuer && tma_out && !(ragged && c == nch - 1)) {
+        if (issuer && tma_out && !(wo.k.ragged && wo.c == wo.k.nch - 1)) {
           for (int d = 0; d < DV; d += 64)
-            tma_store_4d(&omap, vs + (c % NV) * L::kTileV + (d / 64) * (kCh * 128), d, (int)t0 + c * kCh, b, h);
+            tma_store_4d(&omap, vs + (j % NV) * L::kTileV + (d / 64) * (kCh * 128), d, (int)wo.k.t0 + wo.c * kCh, wo.k.b, wo.k.h);
           bulk_commit();
-          bulk_wait_read();                        // the tile may be loaded into again
+          bulk_wait_read();                                  // the tile may be loaded into again
         }
         __syncwarp();
-        if (c + NV < nch) load_v(c + NV);
-      } else if (c + NV < nch) {
-        alive = wait(&v_empty[c % NV], (c / NV) & 1);
+        if (wv_.i < tasks) load_v();                         // chunk j + NV
+      } else if (wv_.i < tasks) {
+        alive = wait(&v_empty[j % NV], (j / NV) & 1);
         if (!alive) break;
-        load_v(c + NV);
+        load_v();
       }
     }
     if (!alive) give_up();
     // no copy of this CTA may still be in flight when it ends
     if (issuer) bulk_wait();
     __syncwarp();
-    for (int i = max(0, nv - NV); i < nv; ++i) bar_wait(&v_full[i % NV], (i / NV) & 1, kDefaultWaitLimit);
-    for (int i = max(0, nk - NKQ); i < nk; ++i) bar_wait(&k_full[i % NKQ], (i / NKQ) & 1, kDefaultWaitLimit);
-    for (int i = max(0, nq - NKQ); i < nq; ++i) bar_wait(&q_full[i % NKQ], (i / NKQ) & 1, kDefaultWaitLimit);
+    for (int x = max(0, wv_.j - NV); x < wv_.j; ++x) bar_wait(&v_full[x % NV], (x / NV) & 1, kDefaultWaitLimit);
+    for (int x = max(0, wk.j - NKQ); x < wk.j; ++x) {
+      bar_wait(&k_full[x % NKQ], (x / NKQ) & 1, kDefaultWaitLimit);
+      if constexpr (OUT) bar_wait(&q_full[x % NKQ], (x / NKQ) & 1, kDefaultWaitLimit);
+    }
   }
   fence_before();
   __syncthreads();
@@ -535,7 +610,7 @@ bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const La
 }
 
 template <int DK, int DV>
-cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
+cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
   constexpr size_t smem = LaSmem<DK, DV>::bytes;
   CUtensorMap qm, km, vm, om{};
   LaMul mul{};
@@ -549,7 +624,8 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(s.B * s.H), (unsigned)p.G);
+  const int tasks = s.B * s.H * p.G;
+  cfg.gridDim = dim3((unsigned)(tasks < num_sms ? tasks : num_sms));
   cfg.blockDim = dim3(kLaTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -597,9 +673,9 @@ LaPlan linattn_tc_plan(const LaShape& s, int num_sms) {
   return LaPlan{(int)best, (int)(c * kCh)};
 }
 
-cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
-  if (s.dk <= 64) return s.dv <= 64 ? run<64, 64>(s, p, a, st) : run<64, 128>(s, p, a, st);
-  return s.dv <= 64 ? run<128, 64>(s, p, a, st) : run<128, 128>(s, p, a, st);
+cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
+  if (s.dk <= 64) return s.dv <= 64 ? run<64, 64>(s, p, a, num_sms, st) : run<64, 128>(s, p, a, num_sms, st);
+  return s.dv <= 64 ? run<128, 64>(s, p, a, num_sms, st) : run<128, 128>(s, p, a, num_sms, st);
 }
 
 cudaError_t linattn_take_error(cudaStream_t st, int* flag) {

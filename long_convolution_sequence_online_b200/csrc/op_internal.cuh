@@ -63,7 +63,7 @@ cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sm
 // tensor map can describe.
 bool linattn_tc_fits(const LaShape& s, const LaPtrs& a);
 LaPlan linattn_tc_plan(const LaShape& s, int num_sms);
-cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st);
+cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st);
 // Whether a bounded wait gave up in these kernels since the last check
 // (synchronises the stream; the flag is cleared).
 cudaError_t linattn_take_error(cudaStream_t st, int* flag);

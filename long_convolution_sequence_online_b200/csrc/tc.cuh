@@ -44,7 +44,8 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
 // up after `limit` checks; the second also once another role of the CTA has given
 // up. A phase that is complete already, the usual case in a pipeline, is seen by
 // the first check: 45 cycles, where the loop around it costs 160.
-static __device__ __noinline__ bool bar_wait_loop(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag) {
+__device__ __forceinline__ bool bar_wait_loop(uint64_t* bar, uint32_t parity, int limit, volatile int* abort_flag) {
+#pragma unroll 1
   for (int it = 0; it < limit; ++it) {
     if (bar_try(bar, parity)) return true;
     if (abort_flag && *abort_flag) return false;
