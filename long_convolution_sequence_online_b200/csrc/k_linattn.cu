@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   using vec = typename std::conditional<V == 4, float4, typename std::conditional<V == 2, float2, float>::type>::type;
   __shared__ float qs[256], ks[256];
   __shared__ float part[8][32 * V];
+  pdl_launch_dependents();
+  pdl_wait_primary();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H;
   const int c = (blockIdx.y * 32 + lane) * V;
@@ -246,16 +248,26 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   __syncthreads();
   float* sp = state + (size_t)bh * s.dk * s.dv + c;
   if (in) {
-#pragma unroll 4
-    for (int d = warp; d < s.dk; d += 8) {
-      float x[V];
-      *reinterpret_cast<vec*>(x) = *reinterpret_cast<const vec*>(sp + (size_t)d * s.dv);
+    // eight rows' loads before the first is used, past the caches' order: the state
+    // is read and written once
+    for (int d0 = warp; d0 < s.dk; d0 += 64) {
+      vec x[8];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        x[e] = fmaf(ks[d], vv[e], g * x[e]);
-        acc[e] = fmaf(qs[d], x[e], acc[e]);
+      for (int u = 0; u < 8; ++u)
+        if (d0 + 8 * u < s.dk) x[u] = __ldcs(reinterpret_cast<const vec*>(sp + (size_t)(d0 + 8 * u) * s.dv));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int d = d0 + 8 * u;
+        if (d >= s.dk) break;
+        float f[V];
+        *reinterpret_cast<vec*>(f) = x[u];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          f[e] = fmaf(ks[d], vv[e], g * f[e]);
+          acc[e] = fmaf(qs[d], f[e], acc[e]);
+        }
+        __stcs(reinterpret_cast<vec*>(sp + (size_t)d * s.dv), *reinterpret_cast<const vec*>(f));
       }
-      *reinterpret_cast<vec*>(sp + (size_t)d * s.dv) = *reinterpret_cast<const vec*>(x);
     }
   }
 #pragma unroll
@@ -294,9 +306,16 @@ cudaError_t prefill_dk(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaS
 template <typename T, int V>
 cudaError_t step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay, float* state,
                  void* o, cudaStream_t st) {
-  const dim3 grid((unsigned)(s.B * s.H), (unsigned)((s.dv + 32 * V - 1) / (32 * V)));
-  k_linattn_step<T, V><<<grid, 256, 0, st>>>(s, (const T*)q, (const T*)k, (const T*)v, log_decay, state, (T*)o);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(s.B * s.H), (unsigned)((s.dv + 32 * V - 1) / (32 * V)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_linattn_step<T, V>, s, (const T*)q, (const T*)k, (const T*)v, log_decay, state, (T*)o);
 }
 
 template <typename T>

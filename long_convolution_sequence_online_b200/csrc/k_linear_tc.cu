@@ -42,6 +42,8 @@ __device__ int g_linear_error;   // a bounded wait gave up since the last check
 // 128 bytes). The units are the parts of fp32 values, or two blocks of the
 // contraction: a stage's waits and signals take 350 to 450 cycles whatever its
 // size, more than the 264 that the MMAs of one block take at BN = 128.
+// fp32: blocks that share an accumulator before the epilogue warps add them up.
+constexpr int kSumBlocks = 2;
 template <int PARTS>
 constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
 template <int BN, int PARTS>
@@ -67,59 +69,47 @@ __device__ __forceinline__ void tile_at(const LinTiles& g, int t, int& m, int& n
   m = gi * g.group + r - n * rows;
 }
 
+template <typename T, int ACT>
+__device__ __forceinline__ float activate(float u) {
+  if constexpr (sizeof(T) == 2) return linear_act_bf16<ACT>(u);
+  else return linear_act<ACT>(u);
+}
+
 // act(acc + bias) + residual of 32 columns of a row per lane, to y. Vector form:
-// the lane stores its row's columns; otherwise through shared memory, so that
-// a warp's stores run along the columns.
+// the lane finishes and stores its row's columns. Otherwise the sums pass through
+// shared memory and a lane finishes a column's rows, so that loads and stores run
+// along the columns, all residuals of a lane in flight at once.
 template <typename T, int ACT>
 __device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], const T* bias, const T* residual, T* y,
                                             int64_t row0, int c0, bool vec, float* stg, int lane) {
   if (c0 >= s.N) return;
-  if (bias) {
-    if (vec && c0 + 32 <= s.N) {
-      constexpr int E = 16 / sizeof(T);
+  if (vec && c0 + 32 <= s.N) {
+    constexpr int E = 16 / sizeof(T);
+    auto add = [&](const uint4& b, int u) {
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int u = 0; u < 32 / E; ++u) {
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(bias + c0) + u);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (sizeof(T) == 2) {
-            v[u * 8 + 2 * e] += lo_f(w[e]);
-            v[u * 8 + 2 * e + 1] += hi_f(w[e]);
-          } else {
-            v[u * 4 + e] += __uint_as_float(w[e]);
-          }
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          v[u * 8 + 2 * e] += lo_f(w[e]);
+          v[u * 8 + 2 * e + 1] += hi_f(w[e]);
+        } else {
+          v[u * 4 + e] += __uint_as_float(w[e]);
         }
       }
-    } else {
+    };
+    if (bias) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (c0 + e < s.N) v[e] += op_load(bias + c0 + e);
+      for (int u = 0; u < 32 / E; ++u) add(__ldg(reinterpret_cast<const uint4*>(bias + c0) + u), u);
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = sizeof(T) == 2 ? linear_act_bf16<ACT>(v[e]) : linear_act<ACT>(v[e]);
-  if (vec && c0 + 32 <= s.N) {
+    for (int e = 0; e < 32; ++e) v[e] = activate<T, ACT>(v[e]);
     const int64_t row = row0 + lane;
     if (row >= s.n) return;
-    constexpr int E = 16 / sizeof(T);
     T* yp = y + row * s.ldy + c0;
     if (residual) {
       const T* rp = residual + row * s.ldr + c0;
 #pragma unroll
-      for (int u = 0; u < 32 / E; ++u) {
-        const uint4 b = *(reinterpret_cast<const uint4*>(rp) + u);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (sizeof(T) == 2) {
-            v[u * 8 + 2 * e] += lo_f(w[e]);
-            v[u * 8 + 2 * e + 1] += hi_f(w[e]);
-          } else {
-            v[u * 4 + e] += __uint_as_float(w[e]);
-          }
-        }
-      }
+      for (int u = 0; u < 32 / E; ++u) add(*(reinterpret_cast<const uint4*>(rp) + u), u);
     }
 #pragma unroll
     for (int u = 0; u < 32 / E; ++u) {
@@ -134,27 +124,25 @@ __device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], c
     }
     return;
   }
+  const int rows = (int)min((int64_t)32, s.n - row0);
 #pragma unroll
   for (int h = 0; h < 32; h += kStagingCols) {
+    const int cl = lane & 15, c = c0 + h + cl, r0 = lane >> 4;   // a lane's column; rows r0, r0 + 2, ...
+    const bool in = c < s.N;
+    const float bv = bias && in ? op_load(bias + c) : 0.f;
+    const T* rp = residual + row0 * s.ldr + c;
+    float res[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      res[r] = residual && in && r0 + 2 * r < rows ? op_load(rp + (int64_t)(r0 + 2 * r) * s.ldr) : 0.f;
 #pragma unroll
     for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[h + e];
     __syncwarp();
-    const int cl = lane & 15, c = c0 + h + cl;      // a lane's column; rows lane / 16, + 2, ...
-    if (c < s.N) {
-      const int rows = (int)min((int64_t)32, s.n - row0);
-      T* yp = y + row0 * s.ldy + c;
-      const T* rp = residual + row0 * s.ldr + c;
-#pragma unroll 1
-      for (int r0 = lane >> 4; r0 < rows; r0 += 16) {
-        float w[8];
+    T* yp = y + row0 * s.ldy + c;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          w[r] = residual && r0 + 2 * r < rows ? op_load(rp + (int64_t)(r0 + 2 * r) * s.ldr) : 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r0 + 2 * r < rows) op_store(yp + (int64_t)(r0 + 2 * r) * s.ldy, stg[(r0 + 2 * r) * kStagingLd + cl] + w[r]);
-      }
-    }
+    for (int r = 0; r < 16; ++r)
+      if (in && r0 + 2 * r < rows)
+        op_store(yp + (int64_t)(r0 + 2 * r) * s.ldy, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv) + res[r]);
     __syncwarp();
   }
 }
@@ -244,7 +232,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         float acc[CW];
 #pragma unroll
         for (int e = 0; e < CW; ++e) acc[e] = 0.f;
-        for (int kb = 0; kb < nk; ++kb, ++unit) {
+        for (int kb = 0; kb < nk; kb += kSumBlocks, ++unit) {
           alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
           if (!alive) break;
           fence_after();
@@ -281,14 +269,14 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       for (int t = first; t < g.tiles && alive; t += stride) {
         for (int kb = 0; kb < nk; ++kb, ++kbs) {
           const int st = kbs % ST;
-          if (PARTS > 1 || kb == 0)
+          if (PARTS > 1 ? kb % kSumBlocks == 0 : kb == 0)
             alive = unit < 2 || bar_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
           alive = __all_sync(0xffffffffu, alive && bar_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag));
           if (!alive) break;
           fence_after();
           const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + UNITS * XB;
           const uint32_t d = tmem + (unit & 1) * BN;
-          const bool last = PARTS > 1 || kb == nk - 1;
+          const bool last = kb == nk - 1 || (PARTS > 1 && kb % kSumBlocks == kSumBlocks - 1);
           if (issuer) {
             if constexpr (PARTS == 1) {
               const int steps = min(KS * kBK / 16, (s.K - kb * KS * kBK + 15) / 16);   // of 16
@@ -304,7 +292,8 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
               for (int p = 0; p < 6; ++p)
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, p > 0 || k > 0);
+                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id,
+                       kb % kSumBlocks > 0 || p > 0 || k > 0);
             }
             commit2(&empty_bar[st]);
             if (last) commit2(&acc_full[unit & 1]);
