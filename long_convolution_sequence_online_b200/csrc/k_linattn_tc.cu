@@ -48,16 +48,18 @@ __device__ int g_linattn_error;          // a bounded wait gave up since the las
 
 // DK, DV: key and value dimensions padded to 64 or 128. V is always double
 // buffered (the next chunk's w V starts first), K and Q where there is room.
-template <int DK, int DV>
+// The launch that forms states only has room for two halves of w V.
+template <int DK, int DV, bool OUT>
 struct LaSmem {
-  static constexpr int kSlotsKQ = DK == 128 && DV == 128 ? 1 : 2, kSlotsV = 2;
+  static constexpr int kSlotsKQ = DK == 128 && DV == 128 ? 1 : 2, kSlotsV = 2, kHalves = OUT ? 1 : 2;
   static constexpr int kTileK = kCh * 2 * DK, kTileV = kCh * 2 * DV;
   static constexpr int kPart = kWHalf * 2 * DV;
   // the state passes through in fp32 rows of 64 columns and 16 bytes on its way in and out
   static constexpr int kLd = 64 + 4, kStage = 128 * kLd * 4;
-  static constexpr int kW = 3 * kPart > kStage ? 3 * kPart : kStage;
-  static constexpr int kState = DK * 2 * DV;
-  static constexpr size_t bytes = 1024 + (size_t)2 * kSlotsKQ * kTileK + kSlotsV * kTileV + kW + kState;
+  static constexpr int kHalf = 3 * kPart;
+  static constexpr int kW = kHalves * kHalf > kStage ? kHalves * kHalf : kStage;
+  static constexpr int kState = OUT ? DK * 2 * DV : 0;
+  static constexpr size_t bytes = 1024 + (size_t)(OUT ? 2 : 1) * kSlotsKQ * kTileK + kSlotsV * kTileV + kW + kState;
 };
 
 // Coordinates of a tensor map [dim][position][sequence][head]; a stride of 0
@@ -97,12 +99,12 @@ __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
              const __grid_constant__ CUtensorMap omap, LaMul mul, int tma_out, int vec_state, int wait_limit) {
-  using L = LaSmem<DK, DV>;
+  using L = LaSmem<DK, DV, OUT>;
   constexpr int NKQ = L::kSlotsKQ, NV = L::kSlotsV;
   constexpr int CW = DV / 4;             // a warp's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: not with outputs
-  __shared__ uint64_t w_ready, w_free, qk_done, kv_done, qs_done, p_ready, o_done, o_staged, drained;
+  __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs_done, p_ready, o_done, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
   __shared__ float GD[63];               // GD[31 + i] = g^i, i = 0 .. 31 (masked below)
@@ -110,7 +112,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   __shared__ int abort_s;
   unsigned char* ks = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
   unsigned char* qs = ks + NKQ * L::kTileK;
-  unsigned char* vs = qs + NKQ * L::kTileK;
+  unsigned char* vs = qs + (OUT ? NKQ * L::kTileK : 0);
   unsigned char* sop = vs + NV * L::kTileV;
   unsigned char* wv = sop + L::kState;
   pdl_launch_dependents();
@@ -126,11 +128,11 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       bar_init(&q_empty[i], 1);
       bar_init(&v_full[i], 1);
       bar_init(&v_empty[i], 1);
+      bar_init(&w_ready[i], kWorkers);             // by half of the chunk
+      bar_init(&w_free[i], 1);
+      bar_init(&kv_done[i], 1);                    // by the CTA's chunk, odd and even
     }
-    bar_init(&w_ready, kWorkers);
-    bar_init(&w_free, 1);
     bar_init(&qk_done, 1);
-    bar_init(&kv_done, 1);
     bar_init(&qs_done, 1);
     bar_init(&p_ready, kWorkers);
     bar_init(&o_done, 1);
@@ -197,7 +199,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         uint32_t q0[4], q1[4], q2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3(w * lo_f(xs[i]), w * hi_f(xs[i]), q0[i], q1[i], q2[i]);
-        unsigned char* dst = wv + blk * (kWHalf * 128) + rem * 16;
+        unsigned char* dst = wv + (L::kHalves > 1 ? half * L::kHalf : 0) + blk * (kWHalf * 128) + rem * 16;
         *reinterpret_cast<uint4*>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
         *reinterpret_cast<uint4*>(dst + L::kPart) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
         *reinterpret_cast<uint4*>(dst + 2 * L::kPart) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
@@ -205,7 +207,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       fence_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(&w_ready);
+      if (lane == 0) bar_arrive(&w_ready[half]);
     };
     // Outputs of a task's chunk c (the CTA's chunk j): rows `row`, columns col0 .., 16 at
     // a time (more would not fit the registers beside the state, and a spill goes to
@@ -314,6 +316,21 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       }
       sync();                                      // the tables are there, the stage is free
       publish();                                   // no Q S of the task before is left: its qs_done was waited for
+      // S <- g^m S + KV of the task's chunk c, the CTA's chunk j
+      auto update = [&](int c, int j) {
+        need(&kv_done[j & 1], (j >> 1) & 1);
+        fence_after();
+        const float gm = G[min(kCh, (int)(k.end - k.t0) - c * kCh)];
+        const uint32_t at = lanes + col0 + (OUT ? kColKV : kColKV - 128 * (j & 1));
+#pragma unroll
+        for (int d = 0; d < CW; d += 16) {
+          uint32_t r[16];
+          tmem_ld16(at + d, r);
+          ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) st[d + e] = fmaf(gm, st[d + e], __uint_as_float(r[e]));
+        }
+      };
       for (int c = 0; c < k.nch; ++c, ++it) {
         const int m = min(kCh, (int)(k.end - k.t0) - c * kCh), sv = it % NV;
         unsigned char* v = vs + sv * L::kTileV;
@@ -328,9 +345,18 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
             for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
           }
         }
+        if constexpr (!OUT) {
+          // the products of chunk c - 1 go on while w V of chunk c is formed
+          if (it > 0) need(&w_free[0], (it - 1) & 1);
+          scale(v, 0, m);
+          if (it > 0) need(&w_free[1], (it - 1) & 1);
+          scale(v, 1, m);
+          if (c > 0) update(c - 1, it - 1);
+          continue;
+        }
         scale(v, 0, m);
         if (OUT && c > 0) outputs(k, c - 1, it - 1);
-        need(&w_free, it & 1);
+        need(&w_free[0], it & 1);
         scale(v, 1, m);
         if constexpr (OUT) {
           need(&qk_done, it & 1);
@@ -370,23 +396,14 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           __syncwarp();
           if (lane == 0) bar_arrive(&p_ready);
         }
-        need(&kv_done, it & 1);
-        fence_after();
-        const float gm = G[m];
-#pragma unroll
-        for (int d = 0; d < CW; d += 16) {
-          uint32_t r[16];
-          tmem_ld16(lanes + kColKV + col0 + d, r);
-          ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) st[d + e] = fmaf(gm, st[d + e], __uint_as_float(r[e]));
-        }
+        update(c, it);
         if constexpr (OUT) {
           need(&qs_done, it & 1);                  // the state before is not read any more
           publish();
         }
       }
       if (OUT && k.nch > 0) outputs(k, k.nch - 1, it - 1);
+      if (!OUT) update(k.nch - 1, it - 1);
       float* dst = nullptr;
       if constexpr (!OUT) dst = ws + (size_t)(k.seg + 1) * slot;
       else if (a.state_out && k.end == k.len) dst = a.state_out + (size_t)k.bh * slot;   // this segment holds the last position
@@ -422,24 +439,25 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // K^T (w V) over half of the chunk, smallest parts first; rows 64..127 of a
     // 64-dimensional K repeat the first ones and are not read.
     auto kv_half = [&](uint32_t ka, int half) {
+      const uint32_t d = tmem + (OUT ? kColKV : kColKV - 128 * (it & 1)), w = wa + (L::kHalves > 1 ? half * L::kHalf : 0);
 #pragma unroll
       for (int part = 2; part >= 0; --part)
 #pragma unroll
         for (int x = 0; x < kWHalf / 16; ++x)
-          mma(tmem + kColKV, desc_mn(ka + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
-              desc_mn(wa + part * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || x > 0);
+          mma(d, desc_mn(ka + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
+              desc_mn(w + part * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || x > 0);
     };
     for (int i = blockIdx.x; i < tasks && alive; i += gridDim.x) {
       const LaTask k = la_task<OUT>(s, p, a, i);
       for (int c = 0; c < k.nch; ++c, ++it) {
         const int sk = it % NKQ, sv = it % NV;
         const uint32_t ka = saddr(ks + sk * L::kTileK), qa = saddr(qs + sk * L::kTileK), va = saddr(vs + sv * L::kTileV);
-        alive = wait(&k_full[sk], (it / NKQ) & 1) && wait(&w_ready, 0);   // use 2 it
+        alive = wait(&k_full[sk], (it / NKQ) & 1) && wait(&w_ready[0], it & 1);
         if (!alive) break;
         fence_after();
         if (issuer) {
           kv_half(ka, 0);
-          commit(&w_free);
+          commit(&w_free[0]);
         }
         __syncwarp();
         if constexpr (OUT) {
@@ -457,12 +475,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           }
           __syncwarp();
         }
-        alive = wait(&w_ready, 1);                                        // use 2 it + 1
+        alive = wait(&w_ready[1], it & 1);
         if (!alive) break;
         fence_after();
         if (issuer) {
           kv_half(ka, 1);
-          commit(&kv_done);
+          if constexpr (!OUT) commit(&w_free[1]);
+          commit(&kv_done[it & 1]);
           commit(&k_empty[sk]);
           if constexpr (OUT) {
 #pragma unroll
@@ -611,7 +630,6 @@ bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const La
 
 template <int DK, int DV>
 cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
-  constexpr size_t smem = LaSmem<DK, DV>::bytes;
   CUtensorMap qm, km, vm, om{};
   LaMul mul{};
   int ob, oh;
@@ -627,18 +645,19 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
   const int tasks = s.B * s.H * p.G;
   cfg.gridDim = dim3((unsigned)(tasks < num_sms ? tasks : num_sms));
   cfg.blockDim = dim3(kLaTcThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.G > 1) {
-    if ((e = allow_smem<k_linattn_tc<DK, DV, false>>(smem)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = LaSmem<DK, DV, false>::bytes;
+    if ((e = allow_smem<k_linattn_tc<DK, DV, false>>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
     if ((e = cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, false>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
                                 (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
-  if ((e = allow_smem<k_linattn_tc<DK, DV, true>>(smem)) != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = LaSmem<DK, DV, true>::bytes;
+  if ((e = allow_smem<k_linattn_tc<DK, DV, true>>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, true>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
                             (int)kDefaultWaitLimit);
 }

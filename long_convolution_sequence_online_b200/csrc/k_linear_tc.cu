@@ -75,86 +75,92 @@ __device__ __forceinline__ float activate(float u) {
   else return linear_act<ACT>(u);
 }
 
-// act(acc + bias) + residual of 32 columns of a row per lane, to y. Vector form:
-// the lane finishes and stores its row's columns. Otherwise the sums pass through
-// shared memory and a lane finishes a column's rows, so that loads and stores run
-// along the columns, all residuals of a lane in flight at once.
+// act(acc + bias) + residual of 32 columns of a row per lane, to y: the lane
+// finishes and stores its row's columns, 16 bytes at a time.
 template <typename T, int ACT>
-__device__ __forceinline__ void store_chunk(const LinShape& s, float (&v)[32], const T* bias, const T* residual, T* y,
-                                            int64_t row0, int c0, bool vec, float* stg, int lane) {
-  if (c0 >= s.N) return;
-  if (vec && c0 + 32 <= s.N) {
-    constexpr int E = 16 / sizeof(T);
-    auto add = [&](const uint4& b, int u) {
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void store_vec(const LinShape& s, float (&v)[32], const T* bias, const T* residual, T* y,
+                                          int64_t row, int c0) {
+  constexpr int E = 16 / sizeof(T);
+  auto add = [&](const uint4& b, int u) {
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2) {
-          v[u * 8 + 2 * e] += lo_f(w[e]);
-          v[u * 8 + 2 * e + 1] += hi_f(w[e]);
-        } else {
-          v[u * 4 + e] += __uint_as_float(w[e]);
-        }
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 2) {
+        v[u * 8 + 2 * e] += lo_f(w[e]);
+        v[u * 8 + 2 * e + 1] += hi_f(w[e]);
+      } else {
+        v[u * 4 + e] += __uint_as_float(w[e]);
       }
-    };
-    if (bias) {
-#pragma unroll
-      for (int u = 0; u < 32 / E; ++u) add(__ldg(reinterpret_cast<const uint4*>(bias + c0) + u), u);
     }
+  };
+  if (bias) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = activate<T, ACT>(v[e]);
-    const int64_t row = row0 + lane;
-    if (row >= s.n) return;
-    T* yp = y + row * s.ldy + c0;
-    if (residual) {
-      const T* rp = residual + row * s.ldr + c0;
-#pragma unroll
-      for (int u = 0; u < 32 / E; ++u) add(*(reinterpret_cast<const uint4*>(rp) + u), u);
-    }
-#pragma unroll
-    for (int u = 0; u < 32 / E; ++u) {
-      uint4 o;
-      if constexpr (sizeof(T) == 2)
-        o = make_uint4(pack2(v[u * 8], v[u * 8 + 1]), pack2(v[u * 8 + 2], v[u * 8 + 3]),
-                       pack2(v[u * 8 + 4], v[u * 8 + 5]), pack2(v[u * 8 + 6], v[u * 8 + 7]));
-      else
-        o = make_uint4(__float_as_uint(v[u * 4]), __float_as_uint(v[u * 4 + 1]), __float_as_uint(v[u * 4 + 2]),
-                       __float_as_uint(v[u * 4 + 3]));
-      *(reinterpret_cast<uint4*>(yp) + u) = o;
-    }
-    return;
+    for (int u = 0; u < 32 / E; ++u) add(__ldg(reinterpret_cast<const uint4*>(bias + c0) + u), u);
   }
-  const int rows = (int)min((int64_t)32, s.n - row0);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = activate<T, ACT>(v[e]);
+  if (row >= s.n) return;
+  if (residual) {
+    const T* rp = residual + row * s.ldr + c0;
+#pragma unroll
+    for (int u = 0; u < 32 / E; ++u) add(*(reinterpret_cast<const uint4*>(rp) + u), u);
+  }
+  T* yp = y + row * s.ldy + c0;
+#pragma unroll
+  for (int u = 0; u < 32 / E; ++u) {
+    uint4 o;
+    if constexpr (sizeof(T) == 2)
+      o = make_uint4(pack2(v[u * 8], v[u * 8 + 1]), pack2(v[u * 8 + 2], v[u * 8 + 3]),
+                     pack2(v[u * 8 + 4], v[u * 8 + 5]), pack2(v[u * 8 + 6], v[u * 8 + 7]));
+    else
+      o = make_uint4(__float_as_uint(v[u * 4]), __float_as_uint(v[u * 4 + 1]), __float_as_uint(v[u * 4 + 2]),
+                     __float_as_uint(v[u * 4 + 3]));
+    *(reinterpret_cast<uint4*>(yp) + u) = o;
+  }
+}
+
+// The same where columns end inside the chunk or rows start at no 16-byte boundary:
+// the sums pass through shared memory and a lane finishes a column's rows (column
+// c0 + lane % 16 or + 16, rows lane / 16, + 2, ...), so that loads and stores run
+// along the columns.
+template <typename T, int ACT>
+__device__ __forceinline__ void store_apart(const LinShape& s, const float (&v)[32], const T* bias, const T* residual, T* y,
+                                            int64_t row0, int c0, float* stg, int lane) {
+  const int rows = (int)min((int64_t)32, s.n - row0), cl = lane & 15, r0 = lane >> 4;
 #pragma unroll
   for (int h = 0; h < 32; h += kStagingCols) {
-    const int cl = lane & 15, c = c0 + h + cl, r0 = lane >> 4;   // a lane's column; rows r0, r0 + 2, ...
-    const bool in = c < s.N;
-    const float bv = bias && in ? op_load(bias + c) : 0.f;
-    const T* rp = residual + row0 * s.ldr + c;
-    float res[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      res[r] = residual && in && r0 + 2 * r < rows ? op_load(rp + (int64_t)(r0 + 2 * r) * s.ldr) : 0.f;
 #pragma unroll
     for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[h + e];
-    __syncwarp();
-    T* yp = y + row0 * s.ldy + c;
+    const int c = c0 + h + cl;
+    const bool in = c < s.N;
+    const float bv = bias && in ? op_load(bias + c) : 0.f;
+    const T* rp = residual + (row0 + r0) * s.ldr + c;
+    T* yp = y + (row0 + r0) * s.ldy + c;
+    float res[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (in && r0 + 2 * r < rows)
-        op_store(yp + (int64_t)(r0 + 2 * r) * s.ldy, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv) + res[r]);
+    for (int r = 0; r < 16; ++r) {
+      res[r] = residual && in && r0 + 2 * r < rows ? op_load(rp) : 0.f;
+      rp += 2 * s.ldr;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if (in && r0 + 2 * r < rows) op_store(yp, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv) + res[r]);
+      yp += 2 * s.ldy;
+    }
     __syncwarp();
   }
 }
 
 // BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32; part p of a matrix is its rows
-// p n .. (p + 1) n). An epilogue warp drains tensor-memory lanes 32 (w % 4) .. + 31,
+// p n .. (p + 1) n). VEC: rows of y, bias and residual at 16-byte boundaries and
+// whole chunks of 32 columns only. An epilogue warp drains tensor-memory lanes 32 (w % 4) .. + 31,
 // column half w / 4.
-template <int BN, int PARTS, typename T, int ACT>
+template <int BN, int PARTS, bool VEC, typename T, int ACT>
 __global__ void __launch_bounds__(kLinThreads, 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
             const T* __restrict__ bias, const T* residual, T* y,
-            int vec_store, int wait_limit) {
+            int wait_limit) {
   constexpr int BW = BN / 2;                       // W rows in this CTA's stages
   constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
   constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
@@ -208,12 +214,16 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       const int64_t row0 = (int64_t)m * TM + rank * kBM + 32 * q;
       const int col0 = n * BN + half * CW;
       const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + half * CW;
+      auto store = [&](float (&v)[32], int c) {
+        if (row0 >= s.n || col0 + c >= s.N) return;
+        if constexpr (VEC) store_vec<T, ACT>(s, v, bias, residual, y, row0 + lane, col0 + c);
+        else store_apart<T, ACT>(s, v, bias, residual, y, row0, col0 + c, stg, lane);
+      };
       if constexpr (PARTS == 1) {
-        alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
+        alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
         if (!alive) break;
         fence_after();
-#pragma unroll 1                                   // straight-line code would be fetched once per launch
-        for (int c = 0; c < CW; c += 32) {
+        auto load = [&](int c, float (&v)[32]) {
           uint32_t r[32];
           tmem_ld32(at + (unit & 1) * BN + c, r);
           ld_wait();
@@ -222,10 +232,14 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
             __syncwarp();
             if (lane == 0) bar_arrive_leader(&acc_empty[unit & 1]);
           }
-          float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-          if (row0 < s.n) store_chunk<T, ACT>(s, v, bias, residual, y, row0, col0 + c, vec_store, stg, lane);
+        };
+#pragma unroll 1                                   // straight-line code would be fetched once per launch
+        for (int c = 0; c < CW; c += 32) {
+          float v[32];
+          load(c, v);
+          store(v, c);
         }
         ++unit;
       } else {
@@ -233,7 +247,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
 #pragma unroll
         for (int e = 0; e < CW; ++e) acc[e] = 0.f;
         for (int kb = 0; kb < nk; kb += kSumBlocks, ++unit) {
-          alive = __all_sync(0xffffffffu, bar_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag));
+          alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
 #pragma unroll
@@ -254,7 +268,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
           float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = acc[c + e];
-          if (row0 < s.n) store_chunk<T, ACT>(s, v, bias, residual, y, row0, col0 + c, vec_store, stg, lane);
+          store(v, c);
         }
       }
     }
@@ -270,8 +284,8 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         for (int kb = 0; kb < nk; ++kb, ++kbs) {
           const int st = kbs % ST;
           if (PARTS > 1 ? kb % kSumBlocks == 0 : kb == 0)
-            alive = unit < 2 || bar_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
-          alive = __all_sync(0xffffffffu, alive && bar_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag));
+            alive = unit < 2 || warp_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
+          alive = alive && warp_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
           const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + UNITS * XB;
@@ -317,8 +331,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       tile_at(g, t, m, n);
       for (int kb = 0; kb < nk; ++kb, ++kbs) {
         const int st = kbs % ST, k = kb * KS * kBK;
-        alive = __all_sync(0xffffffffu,
-                           kbs < ST || bar_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag));
+        alive = kbs < ST || warp_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag);
         if (!alive) break;
         if (issuer) {
           unsigned char* dst = ring + (size_t)st * SB;
@@ -392,10 +405,10 @@ __global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand 
   }
 }
 
-template <int BN, int PARTS, typename T, int ACT>
-cudaError_t run(const LinCall& c) {
+template <int BN, int PARTS, bool VEC, typename T, int ACT>
+cudaError_t run_vec(const LinCall& c) {
   const LinShape& s = c.s;
-  constexpr auto kern = k_linear_tc<BN, PARTS, T, ACT>;
+  constexpr auto kern = k_linear_tc<BN, PARTS, VEC, T, ACT>;
   constexpr int TM = 2 * kBM;
   constexpr size_t smem = smem_bytes<BN, PARTS>();
   cudaError_t e = allow_smem<kern>(smem);
@@ -409,8 +422,6 @@ cudaError_t run(const LinCall& c) {
   g.nt = (s.N + BN - 1) / BN;
   g.group = g.mt < 8 ? g.mt : 8;
   g.tiles = g.mt * g.nt;
-  const int vec_store = linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
-                        (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
   const int pairs = g.tiles < c.num_sms / 2 ? g.tiles : c.num_sms / 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -425,8 +436,15 @@ cudaError_t run(const LinCall& c) {
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, vec_store,
-                            (int)kDefaultWaitLimit);
+  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, (int)kDefaultWaitLimit);
+}
+
+template <int BN, int PARTS, typename T, int ACT>
+cudaError_t run(const LinCall& c) {
+  const LinShape& s = c.s;
+  const bool vec = s.N % 32 == 0 && linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
+                   (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
+  return vec ? run_vec<BN, PARTS, true, T, ACT>(c) : run_vec<BN, PARTS, false, T, ACT>(c);
 }
 
 template <int BN, int PARTS, typename T>
