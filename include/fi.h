@@ -290,10 +290,14 @@ typedef struct {
   int32_t reserved[4]; /* must be 0 */
 } fi_linattn_config;
 
-/* Device bytes of scratch that fi_linattn_prefill needs for n positions (may be
- * 0). Depends on the sizes, strides, pointer alignment and the current device only.
+/* Device bytes of scratch that fi_linattn_prefill needs for n positions of these q,
+ * k and v (may be 0): states of the segments that a long prompt is cut into, and
+ * copies of inputs that the tensor cores cannot read as they stand (fp32 ones, and
+ * bf16 ones whose address or strides are no multiples of 16 bytes). Depends on the
+ * sizes, the strides, the addresses modulo 16 and the current device only.
  * Errors: FI_E_INVALID, FI_E_CUDA. */
-FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t* bytes);
+FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
+                                      uint64_t* bytes);
 
 /* A prompt of n positions (chunked form: matrix products inside chunks of
  * positions, the state carried between them).

@@ -341,15 +341,19 @@ static LaPlan la_plan(const LaShape& s, int num_sms) {
   return LaPlan{(int)((chunks + c - 1) / c), (int)(c * kC)};
 }
 
-size_t linattn_prefill_workspace(const LaShape& s, int num_sms) {
-  const size_t w = la_workspace_bytes(s, la_plan(s, num_sms));
-  if (!s.bf16 || s.dk > 128 || s.dv > 128) return w;
-  const size_t t = la_workspace_bytes(s, linattn_tc_plan(s, num_sms));
-  return w > t ? w : t;
+size_t linattn_prefill_workspace(const LaShape& s, const LaPtrs& a, int num_sms) {
+  if (s.n == 0) return 0;
+  if (!linattn_tc_fits(s)) return la_workspace_bytes(s, la_plan(s, num_sms));
+  return la_workspace_bytes(s, linattn_tc_plan(s, num_sms)) + linattn_tc_layout_bytes(s, a);
 }
 
-cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sms, cudaStream_t st) {
-  if (linattn_tc_fits(s, a)) return launch_linattn_tc(s, linattn_tc_plan(s, num_sms), a, num_sms, st);
+cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& ptrs, void* workspace, int num_sms, cudaStream_t st) {
+  LaPtrs a = ptrs;
+  a.ws = (float*)workspace;
+  if (linattn_tc_fits(s)) {
+    const LaPlan p = linattn_tc_plan(s, num_sms);
+    return launch_linattn_tc(s, p, a, (unsigned char*)workspace + la_workspace_bytes(s, p), num_sms, st);
+  }
   const LaPlan p = la_plan(s, num_sms);
   return s.bf16 ? prefill_dk<__nv_bfloat16>(s, p, a, st) : prefill_dk<float>(s, p, a, st);
 }

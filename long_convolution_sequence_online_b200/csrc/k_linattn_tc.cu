@@ -29,6 +29,8 @@
 // 128 x 128, two groups of eight, w V and state beside P and outputs, 9000: a few
 // warps do not hide their own latency, and more code at a time misses the
 // instruction cache.)
+#include <type_traits>
+
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -49,16 +51,19 @@ __device__ int g_linattn_error;          // a bounded wait gave up since the las
 // DK, DV: key and value dimensions padded to 64 or 128. V is always double
 // buffered (the next chunk's w V starts first), K and Q where there is room.
 // The launch that forms states only has room for two halves of w V.
-template <int DK, int DV, bool OUT>
+// PARTS: bf16 parts of an input, 1 or 3 (fp32).
+template <int DK, int DV, bool OUT, int PARTS>
 struct LaSmem {
-  static constexpr int kSlotsKQ = DK == 128 && DV == 128 ? 1 : 2, kSlotsV = 2, kHalves = OUT ? 1 : 2;
-  static constexpr int kTileK = kCh * 2 * DK, kTileV = kCh * 2 * DV;
+  static constexpr int kSlotsKQ = PARTS == 3 || (DK == 128 && DV == 128) ? 1 : 2, kSlotsV = PARTS == 3 ? 1 : 2;
+  static constexpr int kHalves = OUT ? 1 : 2;
+  static constexpr int kPlaneK = kCh * 2 * DK, kPlaneV = kCh * 2 * DV;   // a part of a tile
+  static constexpr int kTileK = PARTS * kPlaneK, kTileV = PARTS * kPlaneV;
   static constexpr int kPart = kWHalf * 2 * DV;
   // the state passes through in fp32 rows of 64 columns and 16 bytes on its way in and out
   static constexpr int kLd = 64 + 4, kStage = 128 * kLd * 4;
   static constexpr int kHalf = 3 * kPart;
   static constexpr int kW = kHalves * kHalf > kStage ? kHalves * kHalf : kStage;
-  static constexpr int kState = OUT ? DK * 2 * DV : 0;
+  static constexpr int kStatePart = DK * 2 * DV, kState = OUT ? PARTS * kStatePart : 0;
   static constexpr size_t bytes = 1024 + (size_t)(OUT ? 2 : 1) * kSlotsKQ * kTileK + kSlotsV * kTileV + kW + kState;
 };
 
@@ -68,8 +73,17 @@ struct LaMul {
   int qb, qh, kb, kh, vb, vh;
 };
 
-// TMEM columns.
-constexpr uint32_t kColP = 0, kColInter = 128, kColIntra = 256, kColKV = 384;
+// TMEM columns: scores, P (over the scores, or three parts beside them), Q S, P V
+// and K^T (w V), the last twice in the launch that forms states only.
+template <int PARTS>
+struct LaCols {
+  static constexpr uint32_t scores = 0, p = PARTS == 3 ? 128 : 0, inter = PARTS == 3 ? 320 : 128,
+                            intra = PARTS == 3 ? 384 : 256, kv = PARTS == 3 ? 448 : 384;
+};
+// Which parts a product takes, smallest products first: two bits per product.
+// Three parts on both sides: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0); one against three:
+// (0,2) (0,1) (0,0).
+constexpr uint32_t kPairA = 0x052, kPairB = 0x118, kSingleB = 0x006;
 
 // What a CTA does for one (sequence, head) and segment.
 struct LaTask {
@@ -77,7 +91,7 @@ struct LaTask {
   int64_t t0;
   bool ragged;    // the last chunk ends inside a longer batch: what stands behind is cleared in the tiles
 };
-template <bool OUT>
+template <bool OUT, int PARTS>
 __device__ __forceinline__ LaTask la_task(const LaShape& s, const LaPlan& p, const LaPtrs& a, int i) {
   LaTask t;
   t.bh = i % (s.B * s.H);                // segments of a head far apart: the early ones end first
@@ -90,20 +104,24 @@ __device__ __forceinline__ LaTask la_task(const LaShape& s, const LaPlan& p, con
   // the state's launch skips a segment that none follows
   const bool work = OUT ? t.t0 < t.len : t.t0 + p.seg < t.len;
   t.nch = work ? (int)((t.end - t.t0 + kCh - 1) / kCh) : 0;
-  t.ragged = t.end == t.len && t.len < s.n && (t.end - t.t0) % kCh != 0;
+  // behind the longest sequence stand zeros, or (parts one after the other) the next part's start
+  t.ragged = t.end == t.len && (t.len < s.n || PARTS == 3) && (t.end - t.t0) % kCh != 0;
   return t;
 }
 
-template <int DK, int DV, bool OUT>
+template <int DK, int DV, bool OUT, int PARTS>
 __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-             const __grid_constant__ CUtensorMap omap, LaMul mul, int tma_out, int vec_state, int wait_limit) {
-  using L = LaSmem<DK, DV, OUT>;
+             const __grid_constant__ CUtensorMap omap, LaMul mul, int vec_out, int vec_state, int wait_limit) {
+  using L = LaSmem<DK, DV, OUT, PARTS>;
+  using C = LaCols<PARTS>;
+  using T = typename std::conditional<PARTS == 3, float, __nv_bfloat16>::type;
+  constexpr bool STAGED = OUT && PARTS == 1;   // outputs leave by way of V's tile
   constexpr int NKQ = L::kSlotsKQ, NV = L::kSlotsV;
   constexpr int CW = DV / 4;             // a warp's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: not with outputs
+  __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: unless outputs pass through V's tile
   __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs_done, p_ready, o_done, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
@@ -179,8 +197,17 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         for (int e = 0; e < CW; e += 8) {
           const int col = col0 + e, unit = (col & 63) >> 3;
           unsigned char* dst = sop + (col >> 6) * (DK * 128) + row * 128 + ((unit ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(st[e], st[e + 1]), pack2(st[e + 2], st[e + 3]),
-                                                      pack2(st[e + 4], st[e + 5]), pack2(st[e + 6], st[e + 7]));
+          if constexpr (PARTS == 1) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(st[e], st[e + 1]), pack2(st[e + 2], st[e + 3]),
+                                                        pack2(st[e + 4], st[e + 5]), pack2(st[e + 6], st[e + 7]));
+          } else {
+            uint32_t q[3][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) split3(st[e + 2 * x], st[e + 2 * x + 1], q[0][x], q[1][x], q[2][x]);
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+              *reinterpret_cast<uint4*>(dst + x * L::kStatePart) = make_uint4(q[x][0], q[x][1], q[x][2], q[x][3]);
+          }
         }
       }
     };
@@ -192,13 +219,23 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       for (int u = 0; u < UNITS; ++u) {
         const int e = tid + u * (32 * kWorkers);   // 64-column block, row, unit
         const int blk = e / (kWHalf * 8), rem = e & (kWHalf * 8 - 1), r = half * kWHalf + (rem >> 3);
-        uint4 x = *reinterpret_cast<const uint4*>(v + blk * (kCh * 128) + half * (kWHalf * 128) + rem * 16);
+        const unsigned char* src = v + blk * (kCh * 128) + half * (kWHalf * 128) + rem * 16;
         const float w = r < m ? G[m - 1 - r] : 0.f;
-        if (r >= m) x = make_uint4(0, 0, 0, 0);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        float f[8];
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part) {   // their sum is exact
+          uint4 x = *reinterpret_cast<const uint4*>(src + part * L::kPlaneV);
+          if (r >= m) x = make_uint4(0, 0, 0, 0);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = part == PARTS - 1 ? lo_f(xs[i]) : f[2 * i] + lo_f(xs[i]);
+            f[2 * i + 1] = part == PARTS - 1 ? hi_f(xs[i]) : f[2 * i + 1] + hi_f(xs[i]);
+          }
+        }
         uint32_t q0[4], q1[4], q2[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split3(w * lo_f(xs[i]), w * hi_f(xs[i]), q0[i], q1[i], q2[i]);
+        for (int i = 0; i < 4; ++i) split3(w * f[2 * i], w * f[2 * i + 1], q0[i], q1[i], q2[i]);
         unsigned char* dst = wv + (L::kHalves > 1 ? half * L::kHalf : 0) + blk * (kWHalf * 128) + rem * 16;
         *reinterpret_cast<uint4*>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
         *reinterpret_cast<uint4*>(dst + L::kPart) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
@@ -220,15 +257,32 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       fence_after();
       const int64_t t = k.t0 + (int64_t)c * kCh + row;
       const float f_inter = s.scale * G[row + 1], f_intra = s.scale;
-      const bool tile = tma_out && !(k.ragged && c == k.nch - 1);
+      const bool tile = STAGED && vec_out && !(k.ragged && c == k.nch - 1);
       unsigned char* dst = vs + (j % NV) * L::kTileV + row * 128;
-      __nv_bfloat16* op = (__nv_bfloat16*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + col0;
+      T* op = (T*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + col0;
 #pragma unroll
       for (int d = 0; d < CW; d += 16) {
         uint32_t r[16], q[16];
-        tmem_ld16(lanes + kColInter + col0 + d, r);
-        tmem_ld16(lanes + kColIntra + col0 + d, q);
+        tmem_ld16(lanes + C::inter + col0 + d, r);
+        tmem_ld16(lanes + C::intra + col0 + d, q);
         ld_wait();
+        if constexpr (PARTS == 3) {
+          if (t >= k.end) continue;
+          float w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = fmaf(f_inter, __uint_as_float(r[e]), f_intra * __uint_as_float(q[e]));
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            if (vec_out && col0 + d + e + 4 <= s.dv) {
+              *reinterpret_cast<float4*>(op + d + e) = make_float4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (col0 + d + e + x < s.dv) op_store(op + d + e + x, w[e + x]);
+            }
+          }
+          continue;
+        }
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -241,7 +295,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           if (tile) {
             *reinterpret_cast<uint4*>(dst + (col >> 6) * (kCh * 128) + ((((col & 63) >> 3) ^ (row & 7)) << 4)) = v;
           } else if (t < k.end) {
-            if (tma_out && col + 8 <= s.dv) {
+            if (vec_out && col + 8 <= s.dv) {
               *reinterpret_cast<uint4*>(op + d + 8 * u) = v;
             } else {
 #pragma unroll
@@ -252,13 +306,15 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           }
         }
       }
-      fence_async();
       fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&o_staged);
+      if constexpr (STAGED) {
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&o_staged);
+      }
     };
     for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
-      const LaTask k = la_task<OUT>(s, p, a, i);
+      const LaTask k = la_task<OUT, PARTS>(s, p, a, i);
       float* ws = a.ws ? a.ws + (size_t)k.bh * p.G * slot : nullptr;
       const float* s_in = a.state_in ? a.state_in + (size_t)k.bh * slot : nullptr;
       if (!OUT && k.seg == 0 && s_in)
@@ -321,7 +377,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         need(&kv_done[j & 1], (j >> 1) & 1);
         fence_after();
         const float gm = G[min(kCh, (int)(k.end - k.t0) - c * kCh)];
-        const uint32_t at = lanes + col0 + (OUT ? kColKV : kColKV - 128 * (j & 1));
+        const uint32_t at = lanes + col0 + (OUT ? C::kv : C::kv - 128 * (j & 1));
 #pragma unroll
         for (int d = 0; d < CW; d += 16) {
           uint32_t r[16];
@@ -341,8 +397,8 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           unsigned char* kt = ks + sk * L::kTileK;
           for (int e = tid; e < kCh * 8; e += 32 * kWorkers) {     // 16-byte units of a 64-column block
             if ((e >> 3) < m) continue;
-            for (int d = 0; d < DK / 64; ++d) *reinterpret_cast<uint4*>(kt + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-            for (int d = 0; d < DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+            for (int d = 0; d < PARTS * DK / 64; ++d) *reinterpret_cast<uint4*>(kt + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+            for (int d = 0; d < PARTS * DV / 64; ++d) *reinterpret_cast<uint4*>(v + d * (kCh * 128) + e * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         if constexpr (!OUT) {
@@ -362,35 +418,42 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           need(&qk_done, it & 1);
           fence_after();
           // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
-          uint32_t out[16];
+          uint32_t out[PARTS][16];
 #pragma unroll
           for (int x = 0; x < 32; x += 16) {
+            float f[16];
             if (grp <= quarter) {
               uint32_t r[16];
-              tmem_ld16(lanes + kColP + 32 * grp + x, r);
+              tmem_ld16(lanes + C::scores + 32 * grp + x, r);
               ld_wait();
               if (grp < quarter) {
-                const float f = G[row - 32 * grp - 31];
+                const float gi = G[row - 32 * grp - 31];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                   const float4 g4 = *reinterpret_cast<const float4*>(&GR[x + e]);
-                  out[(x + e) / 2] = pack2(__uint_as_float(r[e]) * (f * g4.x), __uint_as_float(r[e + 1]) * (f * g4.y));
-                  out[(x + e) / 2 + 1] = pack2(__uint_as_float(r[e + 2]) * (f * g4.z), __uint_as_float(r[e + 3]) * (f * g4.w));
+                  f[e] = __uint_as_float(r[e]) * (gi * g4.x);
+                  f[e + 1] = __uint_as_float(r[e + 1]) * (gi * g4.y);
+                  f[e + 2] = __uint_as_float(r[e + 2]) * (gi * g4.z);
+                  f[e + 3] = __uint_as_float(r[e + 3]) * (gi * g4.w);
                 }
               } else {
 #pragma unroll
-                for (int e = 0; e < 16; e += 2)
-                  out[(x + e) / 2] = pack2(x + e <= lane ? __uint_as_float(r[e]) * GD[31 + lane - x - e] : 0.f,
-                                           x + e + 1 <= lane ? __uint_as_float(r[e + 1]) * GD[30 + lane - x - e] : 0.f);
+                for (int e = 0; e < 16; ++e) f[e] = x + e <= lane ? __uint_as_float(r[e]) * GD[31 + lane - x - e] : 0.f;
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) out[x / 2 + e] = 0;
+              for (int e = 0; e < 16; ++e) f[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              if constexpr (PARTS == 1) out[0][(x + e) / 2] = pack2(f[e], f[e + 1]);
+              else split3(f[e], f[e + 1], out[0][(x + e) / 2], out[PARTS / 2][(x + e) / 2], out[PARTS - 1][(x + e) / 2]);
             }
           }
           // P takes the place of scores that the other warps of these rows read
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
-          tmem_st16(lanes + kColP + 16 * grp, out);
+          if constexpr (PARTS == 1) asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) tmem_st16(lanes + C::p + 64 * part + 16 * grp, out[part]);
           st_wait();
           fence_before();
           __syncwarp();
@@ -439,16 +502,19 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // K^T (w V) over half of the chunk, smallest parts first; rows 64..127 of a
     // 64-dimensional K repeat the first ones and are not read.
     auto kv_half = [&](uint32_t ka, int half) {
-      const uint32_t d = tmem + (OUT ? kColKV : kColKV - 128 * (it & 1)), w = wa + (L::kHalves > 1 ? half * L::kHalf : 0);
+      const uint32_t d = tmem + (OUT ? C::kv : C::kv - 128 * (it & 1)), w = wa + (L::kHalves > 1 ? half * L::kHalf : 0);
 #pragma unroll
-      for (int part = 2; part >= 0; --part)
+      for (int c = 0; c < (PARTS == 3 ? 6 : 3); ++c) {
+        const uint32_t kp = PARTS == 3 ? kPairA >> 2 * c & 3 : 0, wp = (PARTS == 3 ? kPairB : kSingleB) >> 2 * c & 3;
 #pragma unroll
         for (int x = 0; x < kWHalf / 16; ++x)
-          mma(d, desc_mn(ka + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
-              desc_mn(w + part * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || part < 2 || x > 0);
+          mma(d, desc_mn(ka + kp * L::kPlaneK + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
+              desc_mn(w + wp * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || c > 0 || x > 0);
+      }
     };
+    constexpr int NC = PARTS == 3 ? 6 : 1;         // products of parts
     for (int i = blockIdx.x; i < tasks && alive; i += gridDim.x) {
-      const LaTask k = la_task<OUT>(s, p, a, i);
+      const LaTask k = la_task<OUT, PARTS>(s, p, a, i);
       for (int c = 0; c < k.nch; ++c, ++it) {
         const int sk = it % NKQ, sv = it % NV;
         const uint32_t ka = saddr(ks + sk * L::kTileK), qa = saddr(qs + sk * L::kTileK), va = saddr(vs + sv * L::kTileV);
@@ -467,9 +533,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           fence_after();
           if (issuer) {
 #pragma unroll
-            for (int x = 0; x < DK / 16; ++x) {
-              const uint32_t o = (x / 4) * (kCh * 128) + (x % 4) * 32;
-              mma(tmem + kColP, desc_k(qa + o), desc_k(ka + o), id_qk, x > 0);
+            for (int c = 0; c < NC; ++c) {
+              const uint32_t qp = NC > 1 ? kPairA >> 2 * c & 3 : 0, kp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
+#pragma unroll
+              for (int x = 0; x < DK / 16; ++x) {
+                const uint32_t o = (x / 4) * (kCh * 128) + (x % 4) * 32;
+                mma(tmem + C::scores, desc_k(qa + qp * L::kPlaneK + o), desc_k(ka + kp * L::kPlaneK + o), id_qk, c > 0 || x > 0);
+              }
             }
             commit(&qk_done);
           }
@@ -485,9 +555,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           commit(&k_empty[sk]);
           if constexpr (OUT) {
 #pragma unroll
-            for (int x = 0; x < DK / 16; ++x)
-              mma(tmem + kColInter, desc_k(qa + (x / 4) * (kCh * 128) + (x % 4) * 32), desc_mn(sa + 16 * x * 128, DK * 128),
-                  id_qs, x > 0);
+            for (int c = 0; c < NC; ++c) {
+              const uint32_t qp = NC > 1 ? kPairA >> 2 * c & 3 : 0, sp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
+#pragma unroll
+              for (int x = 0; x < DK / 16; ++x)
+                mma(tmem + C::inter, desc_k(qa + qp * L::kPlaneK + (x / 4) * (kCh * 128) + (x % 4) * 32),
+                    desc_mn(sa + sp * L::kStatePart + 16 * x * 128, DK * 128), id_qs, c > 0 || x > 0);
+            }
             commit(&qs_done);
             commit(&q_empty[sk]);
           } else {
@@ -501,9 +575,15 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           fence_after();
           if (issuer) {
 #pragma unroll
-            for (int x = 0; x < kCh / 16; ++x)
-              mma_ta(tmem + kColIntra, tmem + kColP + 8 * x, desc_mn(va + 16 * x * 128, kCh * 128), id_pv, x > 0);
+            for (int c = 0; c < NC; ++c) {
+              const uint32_t pp = NC > 1 ? kPairA >> 2 * c & 3 : 0, vp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
+#pragma unroll
+              for (int x = 0; x < kCh / 16; ++x)
+                mma_ta(tmem + C::intra, tmem + C::p + 64 * pp + 8 * x, desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
+                       id_pv, c > 0 || x > 0);
+            }
             commit(&o_done);
+            if constexpr (!STAGED) commit(&v_empty[sv]);
           }
           __syncwarp();
         }
@@ -528,7 +608,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       while (w.i < tasks && w.c >= w.k.nch) {
         w.i += gridDim.x;
         w.c = 0;
-        if (w.i < tasks) w.k = la_task<OUT>(s, p, a, w.i);
+        if (w.i < tasks) w.k = la_task<OUT, PARTS>(s, p, a, w.i);
       }
     };
     auto next = [&](Walk& w) {
@@ -536,13 +616,15 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       ++w.j;
       settle(w);
     };
-    Walk wk{(int)blockIdx.x, 0, 0, la_task<OUT>(s, p, a, min((int)blockIdx.x, tasks - 1))};
+    Walk wk{(int)blockIdx.x, 0, 0, la_task<OUT, PARTS>(s, p, a, min((int)blockIdx.x, tasks - 1))};
     settle(wk);
     Walk wv_ = wk, wo = wk;
     auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, const Walk& w, int zb, int zh) {
       if (issuer) {
-        bar_expect(bar, D * 2 * kCh);
-        for (int d = 0; d < D; d += 64) tma_4d(dst + (d / 64) * (kCh * 128), &map, bar, d, (int)w.k.t0 + w.c * kCh, zb, zh);
+        bar_expect(bar, PARTS * D * 2 * kCh);
+        for (int part = 0; part < PARTS; ++part)
+          for (int d = 0; d < D; d += 64)
+            tma_4d(dst + (part * D + d) / 64 * (kCh * 128), &map, bar, d, part * s.n + (int)w.k.t0 + w.c * kCh, zb, zh);
       }
       __syncwarp();
     };
@@ -577,10 +659,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         }
         next(wk);
       }
-      if constexpr (OUT) {
+      if constexpr (STAGED) {
         alive = wait(&o_staged, j & 1);
         if (!alive) break;
-        if (issuer && tma_out && !(wo.k.ragged && wo.c == wo.k.nch - 1)) {
+        if (issuer && vec_out && !(wo.k.ragged && wo.c == wo.k.nch - 1)) {
           for (int d = 0; d < DV; d += 64)
             tma_store_4d(&omap, vs + (j % NV) * L::kTileV + (d / 64) * (kCh * 128), d, (int)wo.k.t0 + wo.c * kCh, wo.k.b, wo.k.h);
           bulk_commit();
@@ -619,25 +701,89 @@ bool mappable(const void* x, const int64_t (&st)[3], const LaShape& s) {
     if (count[i] > 1 && (st[i] % 8 != 0 || st[i] * 2 >= ((int64_t)1 << 40) || (i == 0 && st[i] == 0))) return false;
   return true;
 }
-bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const LaShape& s, int d, int* mb, int* mh) {
+bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const LaShape& s, int parts, int d, int* mb, int* mh) {
   *mb = s.B > 1 && st[1] != 0;
   *mh = s.H > 1 && st[2] != 0;
-  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)s.n, *mb ? (uint64_t)s.B : 1, *mh ? (uint64_t)s.H : 1};
-  const uint64_t strides[3] = {s.n > 1 ? (uint64_t)st[0] * 2 : 256, *mb ? (uint64_t)st[1] * 2 : 256, *mh ? (uint64_t)st[2] * 2 : 256};
+  const int64_t rows = (int64_t)parts * s.n;
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)rows, *mb ? (uint64_t)s.B : 1, *mh ? (uint64_t)s.H : 1};
+  const uint64_t strides[3] = {rows > 1 ? (uint64_t)st[0] * 2 : 256, *mb ? (uint64_t)st[1] * 2 : 256, *mh ? (uint64_t)st[2] * 2 : 256};
   const uint32_t box[4] = {64, (uint32_t)kCh, 1, 1};
   return encode_map(map, x, 4, dims, strides, box);
 }
 
-template <int DK, int DV>
+// Inputs that no tensor map describes, and fp32 ones, as bf16 parts [part][n][B][H][d
+// rounded up to 8]: 8 elements per thread.
+struct LaOperand {
+  const void* src;
+  __nv_bfloat16* dst;
+  int64_t st[3];
+  int d, vec;            // vec: rows start at 16-byte boundaries
+};
+struct LaOperands {
+  LaOperand x[3];
+  int64_t end[3];        // units of 8 elements up to and with each
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_linattn_layout(LaOperands ops, int B, int H, int64_t rows) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < ops.end[2]; u += (int64_t)gridDim.x * 256) {
+    const int i = u < ops.end[0] ? 0 : u < ops.end[1] ? 1 : 2;
+    const LaOperand& o = ops.x[i];
+    const int64_t v = i ? u - ops.end[i - 1] : u;
+    const int per = (o.d + 7) / 8;
+    const int64_t r = v / per;             // (position, sequence, head)
+    const int k = (int)(v - r * per) * 8, h = (int)(r % H), b = (int)(r / H % B);
+    const int64_t t = r / H / B;
+    const T* p = (const T*)o.src + t * o.st[0] + b * o.st[1] + h * o.st[2] + k;
+    __nv_bfloat16* d = o.dst + r * (8 * per) + k;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < o.d) w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) << (16 * (e & 1));
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float f[8];
+      if (o.vec && k + 8 <= o.d) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = k + e < o.d ? __ldg(p + e) : 0.f;
+      }
+      uint32_t q[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split3(f[2 * e], f[2 * e + 1], q[0][e], q[1][e], q[2][e]);
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        *reinterpret_cast<uint4*>(d + x * rows * (8 * per)) = make_uint4(q[x][0], q[x][1], q[x][2], q[x][3]);
+    }
+  }
+}
+
+// 16-byte address and strides of the dimensions that are stepped over.
+bool aligned_heads(const void* x, const int64_t (&st)[3], const LaShape& s) {
+  const int e = s.bf16 ? 8 : 4;
+  const int64_t count[3] = {s.n, s.B, s.H};
+  if ((uintptr_t)x & 15) return false;
+  for (int i = 0; i < 3; ++i)
+    if (count[i] > 1 && st[i] % e != 0) return false;
+  return true;
+}
+
+template <int DK, int DV, int PARTS>
 cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
   CUtensorMap qm, km, vm, om{};
   LaMul mul{};
   int ob, oh;
-  if (!map_heads(&qm, a.q, s.qs, s, s.dk, &mul.qb, &mul.qh) || !map_heads(&km, a.k, s.ks, s, s.dk, &mul.kb, &mul.kh) ||
-      !map_heads(&vm, a.v, s.vs, s, s.dv, &mul.vb, &mul.vh))
+  if (!map_heads(&qm, a.q, s.qs, s, PARTS, s.dk, &mul.qb, &mul.qh) || !map_heads(&km, a.k, s.ks, s, PARTS, s.dk, &mul.kb, &mul.kh) ||
+      !map_heads(&vm, a.v, s.vs, s, PARTS, s.dv, &mul.vb, &mul.vh))
     return cudaErrorInvalidValue;
-  const bool tma_out = mappable(a.o, s.os, s) && map_heads(&om, a.o, s.os, s, s.dv, &ob, &oh);
-  const bool state16 = s.dv % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
+  const int vec_out = PARTS == 1 ? mappable(a.o, s.os, s) && map_heads(&om, a.o, s.os, s, 1, s.dv, &ob, &oh)
+                                 : aligned_heads(a.o, s.os, s);
+  const int vec_state = s.dv % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -650,23 +796,35 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.G > 1) {
-    cfg.dynamicSmemBytes = LaSmem<DK, DV, false>::bytes;
-    if ((e = allow_smem<k_linattn_tc<DK, DV, false>>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, false>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
-                                (int)kDefaultWaitLimit)) != cudaSuccess)
+    constexpr auto kern = k_linattn_tc<DK, DV, false, PARTS>;
+    cfg.dynamicSmemBytes = LaSmem<DK, DV, false, PARTS>::bytes;
+    if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
-  cfg.dynamicSmemBytes = LaSmem<DK, DV, true>::bytes;
-  if ((e = allow_smem<k_linattn_tc<DK, DV, true>>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, k_linattn_tc<DK, DV, true>, s, p, a, qm, km, vm, om, mul, (int)tma_out, (int)state16,
-                            (int)kDefaultWaitLimit);
+  constexpr auto kern = k_linattn_tc<DK, DV, true, PARTS>;
+  cfg.dynamicSmemBytes = LaSmem<DK, DV, true, PARTS>::bytes;
+  if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit);
+}
+
+size_t operand_bytes(const LaShape& s, int d) {
+  return ((size_t)(s.bf16 ? 1 : 3) * s.n * s.B * s.H * ((d + 7) / 8 * 8) * 2 + 255) / 256 * 256;
 }
 
 }  // namespace
 
-bool linattn_tc_fits(const LaShape& s, const LaPtrs& a) {
-  return s.bf16 && s.n > 0 && s.dk <= 128 && s.dv <= 128 && mappable(a.q, s.qs, s) && mappable(a.k, s.ks, s) &&
-         mappable(a.v, s.vs, s);
+bool linattn_tc_fits(const LaShape& s) {
+  // the three parts of an fp32 position index stay below 2^31; its tiles fit shared memory up to 64 dimensions
+  return s.n > 0 && (s.bf16 ? s.dk <= 128 && s.dv <= 128 : s.dk <= 64 && s.dv <= 64 && s.n <= (1 << 29));
+}
+
+size_t linattn_tc_layout_bytes(const LaShape& s, const LaPtrs& a) {
+  size_t n = 0;
+  if (!s.bf16 || !mappable(a.q, s.qs, s)) n += operand_bytes(s, s.dk);
+  if (!s.bf16 || !mappable(a.k, s.ks, s)) n += operand_bytes(s, s.dk);
+  if (!s.bf16 || !mappable(a.v, s.vs, s)) n += operand_bytes(s, s.dv);
+  return n;
 }
 
 // Segments: a CTA fills an SM, so B x H x G CTAs run in rounds of num_sms; the
@@ -692,9 +850,49 @@ LaPlan linattn_tc_plan(const LaShape& s, int num_sms) {
   return LaPlan{(int)best, (int)(c * kCh)};
 }
 
-cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
-  if (s.dk <= 64) return s.dv <= 64 ? run<64, 64>(s, p, a, num_sms, st) : run<64, 128>(s, p, a, num_sms, st);
-  return s.dv <= 64 ? run<128, 64>(s, p, a, num_sms, st) : run<128, 128>(s, p, a, num_sms, st);
+cudaError_t launch_linattn_tc(const LaShape& shape, const LaPlan& p, const LaPtrs& ptrs, void* layout, int num_sms,
+                              cudaStream_t st) {
+  LaShape s = shape;
+  LaPtrs a = ptrs;
+  LaOperands ops{};
+  unsigned char* at = (unsigned char*)layout;
+  int64_t units = 0;
+  int n = 0;
+  const int64_t rows = (int64_t)s.n * s.B * s.H;
+  auto lay = [&](const void*& x, int64_t (&xs)[3], int d) {
+    if (s.bf16 && mappable(x, xs, s)) return;
+    LaOperand& o = ops.x[n];
+    o = LaOperand{x, (__nv_bfloat16*)at, {xs[0], xs[1], xs[2]}, d, aligned_heads(x, xs, s)};
+    units += rows * ((d + 7) / 8);
+    ops.end[n++] = units;
+    at += operand_bytes(s, d);
+    x = o.dst;
+    xs[2] = (d + 7) / 8 * 8;
+    xs[1] = xs[2] * s.H;
+    xs[0] = xs[1] * s.B;
+  };
+  lay(a.q, s.qs, s.dk);
+  lay(a.k, s.ks, s.dk);
+  lay(a.v, s.vs, s.dv);
+  if (n > 0) {
+    for (int i = n; i < 3; ++i) ops.end[i] = units;
+    const int64_t blocks = (units + 255) / 256, most = (int64_t)num_sms * 16;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = s.bf16 ? cudaLaunchKernelEx(&cfg, k_linattn_layout<__nv_bfloat16>, ops, s.B, s.H, rows)
+                                 : cudaLaunchKernelEx(&cfg, k_linattn_layout<float>, ops, s.B, s.H, rows);
+    if (e != cudaSuccess) return e;
+  }
+  if (!s.bf16) return run<64, 64, 3>(s, p, a, num_sms, st);
+  if (s.dk <= 64) return s.dv <= 64 ? run<64, 64, 1>(s, p, a, num_sms, st) : run<64, 128, 1>(s, p, a, num_sms, st);
+  return s.dv <= 64 ? run<128, 64, 1>(s, p, a, num_sms, st) : run<128, 128, 1>(s, p, a, num_sms, st);
 }
 
 cudaError_t linattn_take_error(cudaStream_t st, int* flag) {

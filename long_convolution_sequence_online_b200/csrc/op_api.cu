@@ -105,7 +105,8 @@ fi_status check_linear(const fi_linear_config* c, int32_t n, bool residual, LinS
 
 extern "C" {
 
-fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t* bytes) {
+fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
+                               uint64_t* bytes) {
   if (!bytes) return invalid("bytes is NULL");
   *bytes = 0;
   if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^30]");
@@ -117,7 +118,8 @@ fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, uint64_t
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  *bytes = linattn_prefill_workspace(s, sms);
+  const LaPtrs a{q, k, v, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+  *bytes = linattn_prefill_workspace(s, a, sms);
   return FI_OK;
 }
 
@@ -137,11 +139,11 @@ fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const size_t need = n > 0 ? linattn_prefill_workspace(s, sms) : 0;
+  const LaPtrs a{q, k, v, log_decay, lengths, state_in, state_out, o, nullptr};
+  const size_t need = linattn_prefill_workspace(s, a, sms);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return invalid("workspace: " + std::to_string(need) + " bytes, 256-byte aligned, are needed");
-  const LaPtrs a{q, k, v, log_decay, lengths, state_in, state_out, o, need ? (float*)workspace : nullptr};
-  e = launch_linattn_prefill(s, a, sms, (cudaStream_t)stream);
+  e = launch_linattn_prefill(s, a, need ? workspace : nullptr, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention prefill launch");
 }
 

@@ -44,7 +44,7 @@ struct LaPlan {
 // Scratch of a plan: slot 0 of (sequence, head) holds the state before the
 // prompt, slot g the contribution of segment g - 1.
 inline size_t la_workspace_bytes(const LaShape& s, const LaPlan& p) {
-  return p.G > 1 ? (size_t)s.B * s.H * p.G * s.dk * s.dv * sizeof(float) : 0;
+  return p.G > 1 ? ((size_t)s.B * s.H * p.G * s.dk * s.dv * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
 struct LaPtrs {
@@ -56,14 +56,15 @@ struct LaPtrs {
   void* o;
   float* ws;
 };
-// Scratch of either kernel below, whichever the pointers' alignment allows.
-size_t linattn_prefill_workspace(const LaShape& s, int num_sms);
-cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, int num_sms, cudaStream_t st);
-// Tensor-core form (k_linattn_tc.cu): bf16, dimensions up to 128, tensors that a
-// tensor map can describe.
-bool linattn_tc_fits(const LaShape& s, const LaPtrs& a);
+// Scratch of a prompt: the segments' states, then inputs that are laid out first.
+size_t linattn_prefill_workspace(const LaShape& s, const LaPtrs& a, int num_sms);
+cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, void* workspace, int num_sms, cudaStream_t st);
+// Tensor-core form (k_linattn_tc.cu): dimensions up to 128, fp32 up to 64. `layout`:
+// scratch for inputs that no tensor map describes, and all fp32 ones.
+bool linattn_tc_fits(const LaShape& s);
+size_t linattn_tc_layout_bytes(const LaShape& s, const LaPtrs& a);
 LaPlan linattn_tc_plan(const LaShape& s, int num_sms);
-cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, void* layout, int num_sms, cudaStream_t st);
 // Whether a bounded wait gave up in these kernels since the last check
 // (synchronises the stream; the flag is cleared).
 cudaError_t linattn_take_error(cudaStream_t st, int* flag);

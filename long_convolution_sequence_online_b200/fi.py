@@ -84,7 +84,7 @@ def _load():
         "fi_set_mlp_block": [vp, i32, vp, vp, vp, vp],
         "fi_profile_read_sides": [vp, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32),
                                   ctypes.POINTER(ctypes.c_double)],
-        "fi_linattn_workspace": [vp, i32, ctypes.POINTER(ctypes.c_uint64)],
+        "fi_linattn_workspace": [vp, i32, vp, vp, vp, ctypes.POINTER(ctypes.c_uint64)],
         "fi_linattn_prefill": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
         "fi_linattn_step": [vp, vp, vp, vp, vp, vp, vp, vp],
         "fi_op_sync": [vp],
@@ -338,7 +338,8 @@ def _linattn_config(key, q, k, v, log_decay, o, states, lengths, scale, n):
         getattr(cfg, name)[:] = t.stride()[:-1] if n is not None else (0, *t.stride()[:-1])
     need = ctypes.c_uint64()
     if n is not None:
-        _check(lib.fi_linattn_workspace(ctypes.addressof(cfg), n, ctypes.byref(need)), "fi_linattn_workspace")
+        _check(lib.fi_linattn_workspace(ctypes.addressof(cfg), n, q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(need)),
+               "fi_linattn_workspace")
     return _keep(key, cfg, need.value)
 
 
@@ -350,14 +351,15 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
     strides with a contiguous innermost dimension; log_decay [H] float32;
     lengths [B] int32 or None; state_in, state_out [B][H][key_dim][value_dim]
     float32, contiguous, or None (they may be the same tensor)."""
+    pq, pk, pv = q.data_ptr(), k.data_ptr(), v.data_ptr()
     key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
            o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), _look(log_decay), _look(state_in),
-           _look(state_out), _look(lengths), scale)
+           _look(state_out), _look(lengths), scale, pq & 15, pk & 15, pv & 15)
     at, need, _ = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state_in, state_out), lengths, scale,
                                                        int(q.shape[0]))
     st = _op_stream(stream, key[12])
     ws = _scratch(need, q, stream, st) if need else None
-    s = lib.fi_linattn_prefill(at, q.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+    s = lib.fi_linattn_prefill(at, q.shape[0], pq, pk, pv, log_decay.data_ptr(),
                                None if lengths is None else lengths.data_ptr(),
                                None if state_in is None else state_in.data_ptr(),
                                None if state_out is None else state_out.data_ptr(), o.data_ptr(),

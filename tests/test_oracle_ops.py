@@ -94,7 +94,7 @@ def test_linattn_refuses_bad_configurations(kw, why):
     fi = _fi()
     cfg = _la(fi, **kw)
     need = ctypes.c_uint64(7)
-    calls = [lambda: fi.lib.fi_linattn_workspace(ctypes.addressof(cfg), 5, ctypes.byref(need)),
+    calls = [lambda: fi.lib.fi_linattn_workspace(ctypes.addressof(cfg), 5, P, P, P, ctypes.byref(need)),
              lambda: fi.lib.fi_linattn_prefill(ctypes.addressof(cfg), 5, P, P, P, P, None, None, None, P, None, 0, None)]
     if kw.get("o_stride", (0,))[0] != 95:      # a step has no position dimension
         calls.append(lambda: fi.lib.fi_linattn_step(ctypes.addressof(cfg), P, P, P, P, P, P, None))
@@ -111,7 +111,7 @@ def test_linattn_refuses_nulls_and_alignment():
     assert L.fi_linattn_prefill(None, 5, P, P, P, P, None, None, None, P, None, 0, None) == fi.FI_E_INVALID
     assert L.fi_linattn_prefill(at, -1, P, P, P, P, None, None, None, P, None, 0, None) == fi.FI_E_INVALID
     assert L.fi_linattn_prefill(at, (1 << 30) + 1, P, P, P, P, None, None, None, P, None, 0, None) == fi.FI_E_INVALID
-    assert L.fi_linattn_workspace(at, 5, None) == fi.FI_E_INVALID
+    assert L.fi_linattn_workspace(at, 5, P, P, P, None) == fi.FI_E_INVALID
     for miss in range(5):
         a = [P] * 5
         a[miss] = None
