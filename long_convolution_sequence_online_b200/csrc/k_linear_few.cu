@@ -15,12 +15,17 @@ constexpr int kFewThreads = 128;
 
 __device__ int g_few_error;               // a bounded wait gave up since the last check
 
-template <int NT>
-constexpr int few_stage() { return (kBM + NT) * 128; }
-template <int NT>
-constexpr int few_stages() { return 98304 / few_stage<NT>(); }   // two CTAs per SM
-template <int NT>
-constexpr size_t few_smem() { return 1024 + (size_t)few_stages<NT>() * few_stage<NT>(); }
+// A stage: a block of 64 of W's and x's rows, in 1 (bf16) or 3 (fp32) parts. bf16: two
+// CTAs per SM.
+template <int NT, int PARTS>
+constexpr int few_stage() { return PARTS * (kBM + NT) * 128; }
+template <int NT, int PARTS>
+constexpr int few_stages() { return (PARTS == 1 ? 98304 : 221184) / few_stage<NT, PARTS>(); }
+template <int NT, int PARTS>
+constexpr size_t few_smem() { return 1024 + (size_t)few_stages<NT, PARTS>() * few_stage<NT, PARTS>(); }
+// fp32: blocks whose products share an accumulator (the tensor core's sums are not
+// rounded to nearest; the accumulators are added up afterwards).
+constexpr int kSumBlocks = 2;
 
 __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
   uint32_t at;
@@ -33,14 +38,11 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
 // Cluster of `split` CTAs: the same 128 rows of W, consecutive parts of the
 // contraction. Each leaves its sums [NT][128] in shared memory; each then adds up
 // 128 / split rows of all of them (in rank order) and finishes those outputs.
-template <int NT, int ACT>
+template <int NT, int PARTS, typename T, int ACT>
 __global__ void __launch_bounds__(kFewThreads)
 k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-             const __nv_bfloat16* __restrict__ bias, const __nv_bfloat16* residual, __nv_bfloat16* y, int split,
-             int vec, int wait_limit) {
-  using T = __nv_bfloat16;
-  constexpr int ST = few_stages<NT>(), SB = few_stage<NT>();
-  constexpr uint32_t kCols = NT < 32 ? 32 : NT;
+             const T* __restrict__ bias, const T* residual, T* y, int split, int cols, int vec, int wait_limit) {
+  constexpr int ST = few_stages<NT, PARTS>(), SB = few_stage<NT, PARTS>(), WB = kBM * 128, XB = NT * 128;
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t full[ST], empty[ST], done;
   __shared__ uint32_t tmem_s;
@@ -52,7 +54,7 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   const int row0 = (int)(blockIdx.x / split) * kBM;
   const int blocks = (s.K + kBK - 1) / kBK;
   const int b0 = (int)((int64_t)blocks * rank / split), b1 = (int)((int64_t)blocks * (rank + 1) / split);
-  if (warp == 0) tmem_alloc(&tmem_s, kCols);
+  if (warp == 0) tmem_alloc(&tmem_s, cols);
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
       bar_init(&full[i], 1);
@@ -80,13 +82,15 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
     int i = 0;
     for (; i < b1 - b0; ++i) {
       const int st = i % ST;
-      alive = __all_sync(0xffffffffu, i < ST || bar_wait(&empty[st], (i / ST - 1) & 1, wait_limit, abort_flag));
+      alive = i < ST || warp_wait(&empty[st], (i / ST - 1) & 1, wait_limit, abort_flag);
       if (!alive) break;
       if (issuer) {
         unsigned char* dst = ring + st * SB;
         bar_expect(&full[st], SB);
-        tma_2d(dst, &wmap, &full[st], (b0 + i) * kBK, row0);
-        tma_2d(dst + kBM * 128, &xmap, &full[st], (b0 + i) * kBK, 0);
+        for (int part = 0; part < PARTS; ++part) {
+          tma_2d(dst + part * WB, &wmap, &full[st], (b0 + i) * kBK, part * s.N + row0);
+          tma_2d(dst + PARTS * WB + part * XB, &xmap, &full[st], (b0 + i) * kBK, part * s.n);
+        }
       }
       __syncwarp();
     }
@@ -99,13 +103,23 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
     bool alive = true;
     for (int i = 0; i < b1 - b0; ++i) {
       const int st = i % ST;
-      alive = __all_sync(0xffffffffu, bar_wait(&full[st], (i / ST) & 1, wait_limit, abort_flag));
+      alive = warp_wait(&full[st], (i / ST) & 1, wait_limit, abort_flag);
       if (!alive) break;
       fence_after();
       if (issuer) {
-        const uint32_t wa = saddr(ring + st * SB), xa = wa + kBM * 128;
+        const uint32_t wa = saddr(ring + st * SB), xa = wa + PARTS * WB;
+        if constexpr (PARTS == 1) {
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) mma(tmem, desc_k(wa + 32 * k), desc_k(xa + 32 * k), id, i > 0 || k > 0);
+          for (int k = 0; k < kBK / 16; ++k) mma(tmem, desc_k(wa + 32 * k), desc_k(xa + 32 * k), id, i > 0 || k > 0);
+        } else {
+          constexpr int pw[6] = {2, 0, 1, 1, 0, 0}, px[6] = {0, 2, 1, 0, 1, 0};   // smallest first
+          const uint32_t d = tmem + i / kSumBlocks * NT;
+#pragma unroll
+          for (int p = 0; p < 6; ++p)
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+              mma(d, desc_k(wa + pw[p] * WB + 32 * k), desc_k(xa + px[p] * XB + 32 * k), id, i % kSumBlocks > 0 || p > 0 || k > 0);
+        }
         commit(&empty[st]);
       }
       __syncwarp();
@@ -124,11 +138,19 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
 #pragma unroll
   for (int c = 0; c < NT; c += 16) {
     if (c >= s.n) break;
-    uint32_t r[16];
-    tmem_ld16(at + c, r);
-    ld_wait();
+    float sum[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) part[(c + e) * kBM + tid] = b1 > b0 ? __uint_as_float(r[e]) : 0.f;
+    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+    const int sums = PARTS == 1 ? (b1 > b0) : (b1 - b0 + kSumBlocks - 1) / kSumBlocks;
+    for (int g = 0; g < sums; ++g) {
+      uint32_t r[16];
+      tmem_ld16(at + g * NT + c, r);
+      ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(r[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[(c + e) * kBM + tid] = sum[e];
   }
   if (split > 1) cluster_sync();
   else __syncthreads();
@@ -158,8 +180,8 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
       const T* rp = residual + t * s.ldr + c;
       T* yp = y + t * s.ldy + c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = linear_act_bf16<ACT>(u[e] + bv[e]);
-      if (vec) {                                           // N, the strides and the addresses allow it
+      for (int e = 0; e < 4; ++e) u[e] = sizeof(T) == 2 ? linear_act_bf16<ACT>(u[e] + bv[e]) : linear_act<ACT>(u[e] + bv[e]);
+      if (sizeof(T) == 2 && vec) {                         // N, the strides and the addresses allow it
         if (residual) {
           const uint2 x = *reinterpret_cast<const uint2*>(rp);
           u[0] += lo_f(x.x);
@@ -179,103 +201,116 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   if (split > 1) cluster_sync_relaxed();                   // others may still read this CTA's sums
   else __syncthreads();
   fence_after();
-  if (warp == 0) tmem_free(tmem, kCols);
+  if (warp == 0) tmem_free(tmem, cols);
 }
 
-// fp32, and bf16 rows at no 16-byte boundary: a warp per row of W, its lanes
-// along the contraction, applied to kGroup rows of x at once.
-constexpr int kGroup = 8;
+// At most kWarpRows rows of x, operands as they stand: a warp per row of W, its lanes
+// along the contraction, applied to all rows of x, which the CTA holds in shared
+// memory in fp32, kRowsK columns at a time.
+constexpr int kRowsK = 1024;
 template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __restrict__ x, const T* __restrict__ w,
                                                     const T* __restrict__ bias, const T* residual, T* y) {
+  __shared__ __align__(16) float xs[kWarpRows][kRowsK];
   pdl_launch_dependents();
   pdl_wait_primary();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 8 + warp;
-  const int t0 = blockIdx.y * kGroup, nt = min(kGroup, s.n - t0);
-  if (c >= s.N) return;
-  const T* wr = w + (int64_t)c * s.ldw;
-  const T* xr = x + (int64_t)t0 * s.ldx;
-  float acc[kGroup] = {};
+  const T* wr = w + (int64_t)min(c, s.N - 1) * s.ldw;
+  float acc[kWarpRows] = {};
   constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;          // elements per load
   constexpr int U = VEC ? 4 : 8;                            // loads of W in flight
-  for (int k0 = lane * E; k0 < s.K; k0 += 32 * E * U) {
-    float wv[U][E];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * 32 * E;
-      if constexpr (VEC) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (k < s.K) q = __ldg(reinterpret_cast<const uint4*>(wr + k));
-        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (sizeof(T) == 2) {
-            wv[u][2 * e] = lo_f(v[e]);
-            wv[u][2 * e + 1] = hi_f(v[e]);
-          } else {
-            wv[u][e] = __uint_as_float(v[e]);
-          }
-        }
-      } else {
-        wv[u][0] = k < s.K ? op_load(wr + k) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kGroup; ++t) {
-      if (t >= nt) break;
+  for (int base = 0; base < s.K; base += kRowsK) {
+    const int kn = min(kRowsK, s.K - base);
+    __syncthreads();
+    for (int t = 0; t < s.n; ++t)
+      for (int k = threadIdx.x; k < kn; k += 256) xs[t][k] = op_load(x + t * s.ldx + base + k);
+    __syncthreads();
+    for (int k0 = lane * E; k0 < kn; k0 += 32 * E * U) {
+      float wv[U][E];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * 32 * E;
-        if (k >= s.K) break;
-        const T* xp = xr + t * s.ldx + k;
         if constexpr (VEC) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(xp));
+          uint4 q = make_uint4(0, 0, 0, 0);
+          if (k < kn) q = __ldcs(reinterpret_cast<const uint4*>(wr + base + k));
           const uint32_t v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (sizeof(T) == 2) {
-              acc[t] = fmaf(wv[u][2 * e], lo_f(v[e]), acc[t]);
-              acc[t] = fmaf(wv[u][2 * e + 1], hi_f(v[e]), acc[t]);
+              wv[u][2 * e] = lo_f(v[e]);
+              wv[u][2 * e + 1] = hi_f(v[e]);
             } else {
-              acc[t] = fmaf(wv[u][e], __uint_as_float(v[e]), acc[t]);
+              wv[u][e] = __uint_as_float(v[e]);
             }
           }
         } else {
-          acc[t] = fmaf(wv[u][0], op_load(xp), acc[t]);
+          wv[u][0] = k < kn ? op_load(wr + base + k) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kWarpRows; ++t) {
+        if (t >= s.n) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * 32 * E;
+          if (k >= kn) break;
+          if constexpr (VEC) {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&xs[t][k + e]);
+              acc[t] = fmaf(wv[u][e], f.x, acc[t]);
+              acc[t] = fmaf(wv[u][e + 1], f.y, acc[t]);
+              acc[t] = fmaf(wv[u][e + 2], f.z, acc[t]);
+              acc[t] = fmaf(wv[u][e + 3], f.w, acc[t]);
+            }
+          } else {
+            acc[t] = fmaf(wv[u][0], xs[t][k], acc[t]);
+          }
         }
       }
     }
   }
+  if (c >= s.N) return;
   float out = 0.f;
 #pragma unroll
-  for (int t = 0; t < kGroup; ++t) {
-    if (t >= nt) break;
+  for (int t = 0; t < kWarpRows; ++t) {
+    if (t >= s.n) break;
     float v = acc[t];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == t) out = v;
   }
-  if (lane < nt) {
-    const int64_t t = t0 + lane;
+  if (lane < s.n) {
     float u = linear_act<ACT>(out + (bias ? op_load(bias + c) : 0.f));
-    if (residual) u += op_load(residual + t * s.ldr + c);
-    op_store(y + t * s.ldy + c, u);
+    if (residual) u += op_load(residual + lane * s.ldr + c);
+    op_store(y + lane * s.ldy + c, u);
   }
 }
 
-template <int NT, int ACT>
+// CTAs that share the contraction of 128 rows of W: enough for two per SM.
+int few_split(const LinShape& s, int num_sms) {
+  const int tiles = (s.N + kBM - 1) / kBM, blocks = (s.K + kBK - 1) / kBK;
+  int split = 1;
+  while (split < 8 && 2 * split * tiles <= 2 * num_sms && 2 * split <= blocks) split *= 2;
+  return split;
+}
+
+template <int NT, int PARTS, typename T, int ACT>
 cudaError_t run_few(const LinCall& c) {
   const LinShape& s = c.s;
-  constexpr auto kern = k_linear_few<NT, ACT>;
-  constexpr size_t smem = few_smem<NT>();
+  constexpr auto kern = k_linear_few<NT, PARTS, T, ACT>;
+  constexpr size_t smem = few_smem<NT, PARTS>();
   cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap, wmap;
-  if (!linear_map(&xmap, c.x, s.n, s.K, s.ldx, NT) || !linear_map(&wmap, c.w, s.N, s.K, s.ldw, kBM)) return cudaErrorInvalidValue;
-  const int tiles = (s.N + kBM - 1) / kBM, blocks = (s.K + kBK - 1) / kBK;
-  int split = 1;
-  while (split < 8 && 2 * split * tiles <= 2 * c.num_sms && 2 * split <= blocks) split *= 2;
+  if (!linear_map(&xmap, c.x, (int64_t)PARTS * s.n, s.K, s.ldx, NT) || !linear_map(&wmap, c.w, (int64_t)PARTS * s.N, s.K, s.ldw, kBM))
+    return cudaErrorInvalidValue;
+  const int split = few_split(s, c.num_sms), blocks = (s.K + kBK - 1) / kBK;
+  int cols = NT;
+  if (PARTS == 3) cols *= ((blocks + split - 1) / split + kSumBlocks - 1) / kSumBlocks;
+  int alloc = 32;
+  while (alloc < cols) alloc *= 2;
   const int vec = s.N % 4 == 0 && (uintptr_t)c.y % 8 == 0 && s.ldy % 4 == 0 &&
                   (!c.residual || ((uintptr_t)c.residual % 8 == 0 && s.ldr % 4 == 0));
   cudaLaunchAttribute attr[2];
@@ -285,22 +320,28 @@ cudaError_t run_few(const LinCall& c) {
   attr[1].val.clusterDim.x = split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.gridDim = dim3((unsigned)((s.N + kBM - 1) / kBM * split));
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, s, xmap, wmap, (const __nv_bfloat16*)c.bias, (const __nv_bfloat16*)c.residual,
-                            (__nv_bfloat16*)c.y, split, vec, (int)kDefaultWaitLimit);
+  return cudaLaunchKernelEx(&cfg, kern, s, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, split, alloc, vec,
+                            (int)kDefaultWaitLimit);
 }
 
 template <int ACT>
 cudaError_t run_few_nt(const LinCall& c) {
-  if (c.s.n <= 16) return run_few<16, ACT>(c);
-  if (c.s.n <= 32) return run_few<32, ACT>(c);
-  if (c.s.n <= 64) return run_few<64, ACT>(c);
-  return run_few<128, ACT>(c);
+  using H = __nv_bfloat16;
+  if (!c.s.bf16) {
+    if (c.s.n <= 16) return run_few<16, 3, float, ACT>(c);
+    if (c.s.n <= 32) return run_few<32, 3, float, ACT>(c);
+    return run_few<64, 3, float, ACT>(c);
+  }
+  if (c.s.n <= 16) return run_few<16, 1, H, ACT>(c);
+  if (c.s.n <= 32) return run_few<32, 1, H, ACT>(c);
+  if (c.s.n <= 64) return run_few<64, 1, H, ACT>(c);
+  return run_few<128, 1, H, ACT>(c);
 }
 
 template <typename T, int ACT>
@@ -312,7 +353,7 @@ cudaError_t run_rows(const LinCall& c) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((s.N + 7) / 8), (unsigned)((s.n + kGroup - 1) / kGroup));
+  cfg.gridDim = dim3((unsigned)((s.N + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = c.st;
   cfg.attrs = attr;
@@ -322,6 +363,14 @@ cudaError_t run_rows(const LinCall& c) {
 }
 
 }  // namespace
+
+bool linear_few_fits(const LinShape& s, int num_sms) {
+  if (s.bf16) return s.n <= kFewRows;
+  if (s.n > 64) return false;
+  // an accumulator for every two blocks of a CTA's part of the contraction
+  const int blocks = (s.K + kBK - 1) / kBK, split = few_split(s, num_sms), nt = s.n <= 16 ? 16 : s.n <= 32 ? 32 : 64;
+  return ((blocks + split - 1) / split + kSumBlocks - 1) / kSumBlocks * nt <= 512;
+}
 
 cudaError_t launch_linear_few(const LinCall& c) {
   switch (c.s.act) {

@@ -466,6 +466,9 @@ bool direct_x(const LinShape& s, const void* x) {
 }
 bool direct_w(const LinShape& s, const void* w) { return s.bf16 && linear_aligned16(w, s.ldw, s.N, 2); }
 int padded(int K) { return (K + 7) / 8 * 8; }
+// Rows of x up to which operands that would have to be laid out are read as they
+// stand: laying out W alone moves its bytes three times (fp32: four and a half).
+int warp_rows(const LinShape& s) { return s.bf16 ? 2 : kWarpRows; }
 size_t operand_bytes(const LinShape& s, int64_t rows) {
   return ((size_t)(s.bf16 ? 1 : 3) * rows * padded(s.K) * 2 + 255) / 256 * 256;
 }
@@ -474,7 +477,7 @@ size_t operand_bytes(const LinShape& s, int64_t rows) {
 
 size_t linear_workspace(const LinShape& s, const void* x, const void* w) {
   const bool dx = direct_x(s, x), dw = direct_w(s, w);
-  if ((dx && dw) || s.n <= kWarpRows) return 0;
+  if ((dx && dw) || s.n <= warp_rows(s)) return 0;
   return (dx ? 0 : operand_bytes(s, s.n)) + (dw ? 0 : operand_bytes(s, s.N));
 }
 
@@ -511,7 +514,7 @@ cudaError_t launch_linear(const LinShape& shape, const void* x, const void* w, c
   LinCall c{s, x, w, bias, residual, y, num_sms, st};
   const bool dx = direct_x(s, x), dw = direct_w(s, w);
   if (!dx || !dw) {
-    if (s.n <= kWarpRows) return launch_linear_rows(c);
+    if (s.n <= warp_rows(s)) return launch_linear_rows(c);
     const int Kp = padded(s.K);
     LinOperand a{}, b{};
     unsigned char* at = (unsigned char*)workspace;
@@ -541,8 +544,8 @@ cudaError_t launch_linear(const LinShape& shape, const void* x, const void* w, c
                                  : cudaLaunchKernelEx(&cfg, k_linear_layout<float>, a, b, s.K, Kp, ua, units);
     if (e != cudaSuccess) return e;
   }
+  if (linear_few_fits(s, num_sms)) return launch_linear_few(c);
   if (!s.bf16) return run_act<128, 3, float>(c);
-  if (s.n <= kFewRows) return launch_linear_few(c);
   const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM);
   if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, __nv_bfloat16>(c);
   return run_act<128, 1, __nv_bfloat16>(c);

@@ -104,9 +104,10 @@ struct LinCall {
   int num_sms;
   cudaStream_t st;
 };
-// Few rows (k_linear_few.cu): tensor cores with W's rows as the wide side (bf16,
-// operands by TMA, n <= kFewRows), or a warp per row of W (any operands).
+// Few rows (k_linear_few.cu): tensor cores with W's rows as the wide side (operands
+// by TMA), or a warp per row of W (any operands, n <= kWarpRows).
 constexpr int kFewRows = 128, kWarpRows = 8;
+bool linear_few_fits(const LinShape& s, int num_sms);
 cudaError_t launch_linear_few(const LinCall& c);
 cudaError_t launch_linear_rows(const LinCall& c);
 // 16-byte aligned address and row stride.
