@@ -204,22 +204,25 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   if (warp == 0) tmem_free(tmem, cols);
 }
 
-// At most kWarpRows rows of x, operands as they stand: a warp per row of W, its lanes
-// along the contraction, applied to all rows of x, which the CTA holds in shared
-// memory in fp32, kRowsK columns at a time.
+// At most kWarpRows rows of x, operands as they stand: a warp per RW rows of W, its
+// lanes along the contraction, applied to all rows of x, which the CTA holds in
+// shared memory in fp32, kRowsK columns at a time. RW = 2 halves the reads of x,
+// which bound it from a few rows on (8 rows, 8192 -> 8192 fp32: 147 us with RW = 1).
 constexpr int kRowsK = 1024;
-template <typename T, int ACT, bool VEC>
+template <typename T, int ACT, bool VEC, int RW>
 __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __restrict__ x, const T* __restrict__ w,
                                                     const T* __restrict__ bias, const T* residual, T* y) {
   __shared__ __align__(16) float xs[kWarpRows][kRowsK];
   pdl_launch_dependents();
   pdl_wait_primary();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 8 + warp;
-  const T* wr = w + (int64_t)min(c, s.N - 1) * s.ldw;
-  float acc[kWarpRows] = {};
+  const int c0 = (blockIdx.x * 8 + warp) * RW;
+  const T* wr[RW];
+#pragma unroll
+  for (int r = 0; r < RW; ++r) wr[r] = w + (int64_t)min(c0 + r, s.N - 1) * s.ldw;
+  float acc[RW][kWarpRows] = {};
   constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;          // elements per load
-  constexpr int U = VEC ? 4 : 8;                            // loads of W in flight
+  constexpr int U = VEC ? 4 / RW : 8 / RW;                  // loads of a row of W in flight
   for (int base = 0; base < s.K; base += kRowsK) {
     const int kn = min(kRowsK, s.K - base);
     __syncthreads();
@@ -227,27 +230,29 @@ __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __rest
       for (int k = threadIdx.x; k < kn; k += 256) xs[t][k] = op_load(x + t * s.ldx + base + k);
     __syncthreads();
     for (int k0 = lane * E; k0 < kn; k0 += 32 * E * U) {
-      float wv[U][E];
+      float wv[RW][U][E];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * 32 * E;
-        if constexpr (VEC) {
-          uint4 q = make_uint4(0, 0, 0, 0);
-          if (k < kn) q = __ldcs(reinterpret_cast<const uint4*>(wr + base + k));
-          const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (sizeof(T) == 2) {
-              wv[u][2 * e] = lo_f(v[e]);
-              wv[u][2 * e + 1] = hi_f(v[e]);
-            } else {
-              wv[u][e] = __uint_as_float(v[e]);
+        for (int r = 0; r < RW; ++r) {
+          const int k = k0 + u * 32 * E;
+          if constexpr (VEC) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (k < kn) q = __ldcs(reinterpret_cast<const uint4*>(wr[r] + base + k));
+            const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(T) == 2) {
+                wv[r][u][2 * e] = lo_f(v[e]);
+                wv[r][u][2 * e + 1] = hi_f(v[e]);
+              } else {
+                wv[r][u][e] = __uint_as_float(v[e]);
+              }
             }
+          } else {
+            wv[r][u][0] = k < kn ? op_load(wr[r] + base + k) : 0.f;
           }
-        } else {
-          wv[u][0] = k < kn ? op_load(wr + base + k) : 0.f;
         }
-      }
 #pragma unroll
       for (int t = 0; t < kWarpRows; ++t) {
         if (t >= s.n) break;
@@ -259,32 +264,41 @@ __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __rest
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
               const float4 f = *reinterpret_cast<const float4*>(&xs[t][k + e]);
-              acc[t] = fmaf(wv[u][e], f.x, acc[t]);
-              acc[t] = fmaf(wv[u][e + 1], f.y, acc[t]);
-              acc[t] = fmaf(wv[u][e + 2], f.z, acc[t]);
-              acc[t] = fmaf(wv[u][e + 3], f.w, acc[t]);
+#pragma unroll
+              for (int r = 0; r < RW; ++r) {
+                acc[r][t] = fmaf(wv[r][u][e], f.x, acc[r][t]);
+                acc[r][t] = fmaf(wv[r][u][e + 1], f.y, acc[r][t]);
+                acc[r][t] = fmaf(wv[r][u][e + 2], f.z, acc[r][t]);
+                acc[r][t] = fmaf(wv[r][u][e + 3], f.w, acc[r][t]);
+              }
             }
           } else {
-            acc[t] = fmaf(wv[u][0], xs[t][k], acc[t]);
+            const float f = xs[t][k];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) acc[r][t] = fmaf(wv[r][u][0], f, acc[r][t]);
           }
         }
       }
     }
   }
-  if (c >= s.N) return;
-  float out = 0.f;
 #pragma unroll
-  for (int t = 0; t < kWarpRows; ++t) {
-    if (t >= s.n) break;
-    float v = acc[t];
+  for (int r = 0; r < RW; ++r) {
+    const int c = c0 + r;
+    if (c >= s.N) return;
+    float out = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == t) out = v;
-  }
-  if (lane < s.n) {
-    float u = linear_act<ACT>(out + (bias ? op_load(bias + c) : 0.f));
-    if (residual) u += op_load(residual + lane * s.ldr + c);
-    op_store(y + lane * s.ldy + c, u);
+    for (int t = 0; t < kWarpRows; ++t) {
+      if (t >= s.n) break;
+      float v = acc[r][t];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == t) out = v;
+    }
+    if (lane < s.n) {
+      float u = linear_act<ACT>(out + (bias ? op_load(bias + c) : 0.f));
+      if (residual) u += op_load(residual + lane * s.ldr + c);
+      op_store(y + lane * s.ldy + c, u);
+    }
   }
 }
 
@@ -353,12 +367,15 @@ cudaError_t run_rows(const LinCall& c) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((s.N + 7) / 8));
+  // two rows of W per warp where that still leaves every SM a few CTAs
+  const int rw = s.n > 2 && s.N >= 16 * 2 * c.num_sms ? 2 : 1;
+  cfg.gridDim = dim3((unsigned)((s.N + 8 * rw - 1) / (8 * rw)));
   cfg.blockDim = dim3(256);
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = vec ? k_linear_rows<T, ACT, true> : k_linear_rows<T, ACT, false>;
+  auto kern = rw == 2 ? (vec ? k_linear_rows<T, ACT, true, 2> : k_linear_rows<T, ACT, false, 2>)
+                      : (vec ? k_linear_rows<T, ACT, true, 1> : k_linear_rows<T, ACT, false, 1>);
   return cudaLaunchKernelEx(&cfg, kern, s, (const T*)c.x, (const T*)c.w, (const T*)c.bias, (const T*)c.residual, (T*)c.y);
 }
 
