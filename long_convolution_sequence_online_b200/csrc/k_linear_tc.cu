@@ -48,12 +48,17 @@ template <int PARTS>
 constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
 template <int BN, int PARTS>
 constexpr int stage_bytes() { return PARTS * kStageBlocks<PARTS> * (kBM + BN / 2) * 128; }
-template <int BN, int PARTS>
-constexpr int num_stages() { return 196608 / stage_bytes<BN, PARTS>(); }
+// VEC kernels need no staging and have room for more: fp32 3 stages instead of 2.
+template <int BN, int PARTS, bool VEC>
+constexpr int num_stages() { return (VEC ? 229376 : 196608) / stage_bytes<BN, PARTS>(); }
 constexpr int kStagingCols = 16, kStagingLd = kStagingCols + 1;
 constexpr int kStagingBytes = kEpiWarps * 32 * kStagingLd * 4;
-template <int BN, int PARTS>
-constexpr size_t smem_bytes() { return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kStagingBytes; }
+template <int BN, int PARTS, bool VEC>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)num_stages<BN, PARTS, VEC>() * stage_bytes<BN, PARTS>() + (VEC ? 0 : kStagingBytes);
+}
+template <int BN>
+constexpr uint32_t acc_cols() { return BN <= 128 ? 256 : 512; }   // two accumulators
 
 struct LinTiles {
   int mt, nt, group;   // row tiles, column tiles, row tiles per group
@@ -127,25 +132,28 @@ template <typename T, int ACT>
 __device__ __forceinline__ void store_apart(const LinShape& s, const float (&v)[32], const T* bias, const T* residual, T* y,
                                             int64_t row0, int c0, float* stg, int lane) {
   const int rows = (int)min((int64_t)32, s.n - row0), cl = lane & 15, r0 = lane >> 4;
+  float res[2][16], bv[2];
 #pragma unroll
-  for (int h = 0; h < 32; h += kStagingCols) {
-#pragma unroll
-    for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[h + e];
-    const int c = c0 + h + cl;
-    const bool in = c < s.N;
-    const float bv = bias && in ? op_load(bias + c) : 0.f;
+  for (int h = 0; h < 2; ++h) {            // everything that comes from memory first
+    const int c = c0 + 16 * h + cl;
+    bv[h] = bias && c < s.N ? op_load(bias + c) : 0.f;
     const T* rp = residual + (row0 + r0) * s.ldr + c;
-    T* yp = y + (row0 + r0) * s.ldy + c;
-    float res[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      res[r] = residual && in && r0 + 2 * r < rows ? op_load(rp) : 0.f;
+      res[h][r] = residual && c < s.N && r0 + 2 * r < rows ? op_load(rp) : 0.f;
       rp += 2 * s.ldr;
     }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[16 * h + e];
+    const int c = c0 + 16 * h + cl;
+    T* yp = y + (row0 + r0) * s.ldy + c;
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      if (in && r0 + 2 * r < rows) op_store(yp, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv) + res[r]);
+      if (c < s.N && r0 + 2 * r < rows) op_store(yp, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv[h]) + res[h][r]);
       yp += 2 * s.ldy;
     }
     __syncwarp();
@@ -163,7 +171,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
             int wait_limit) {
   constexpr int BW = BN / 2;                       // W rows in this CTA's stages
   constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
-  constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
+  constexpr int ST = num_stages<BN, PARTS, VEC>(), SB = stage_bytes<BN, PARTS>();
   constexpr int XB = kBM * 128, WB = BW * 128;
   constexpr int TM = 2 * kBM;                      // rows of a tile
   extern __shared__ unsigned char raw_smem[];
@@ -177,7 +185,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   pdl_launch_dependents();
   const int rank = (int)cluster_rank();
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-  if (warp == 0) tmem_alloc2(&tmem_s, 2 * BN);
+  if (warp == 0) tmem_alloc2(&tmem_s, acc_cols<BN>());
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
       bar_init(&full_bar[i], 1);
@@ -214,6 +222,12 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       const int64_t row0 = (int64_t)m * TM + rank * kBM + 32 * q;
       const int col0 = n * BN + half * CW;
       const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + half * CW;
+      // the tile's residual on its way into L2 while the tile is multiplied: a lane per row
+      if (residual && row0 + lane < s.n) {
+        const char* rp = reinterpret_cast<const char*>(residual + (row0 + lane) * s.ldr + col0);
+        const int bytes = min(CW, s.N - col0) * (int)sizeof(T);
+        for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + o));
+      }
       auto store = [&](float (&v)[32], int c) {
         if (row0 >= s.n || col0 + c >= s.N) return;
         if constexpr (VEC) store_vec<T, ACT>(s, v, bias, residual, y, row0 + lane, col0 + c);
@@ -355,7 +369,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   fence_before();
   cluster_sync_relaxed();                          // neither CTA ends while the other may still signal it
   fence_after();
-  if (warp == 0) tmem_free2(tmem, 2 * BN);
+  if (warp == 0) tmem_free2(tmem, acc_cols<BN>());
 }
 
 // An operand that TMA cannot take (fp32, or rows at no 16-byte boundary) as
@@ -410,7 +424,7 @@ cudaError_t run_vec(const LinCall& c) {
   const LinShape& s = c.s;
   constexpr auto kern = k_linear_tc<BN, PARTS, VEC, T, ACT>;
   constexpr int TM = 2 * kBM;
-  constexpr size_t smem = smem_bytes<BN, PARTS>();
+  constexpr size_t smem = smem_bytes<BN, PARTS, VEC>();
   cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap, wmap;
@@ -546,8 +560,13 @@ cudaError_t launch_linear(const LinShape& shape, const void* x, const void* w, c
   }
   if (linear_few_fits(s, num_sms)) return launch_linear_few(c);
   if (!s.bf16) return run_act<128, 3, float>(c);
-  const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM);
-  if (mt * ((s.N + 255) / 256) >= num_sms / 2) return run_act<256, 1, __nv_bfloat16>(c);
+  // Columns of a tile: the rounds of tiles over the CTA pairs times a tile's time,
+  // which goes with its columns and about 48 more (wider tiles read W less often, but
+  // leave a last round emptier).
+  const int64_t mt = ((int64_t)s.n + 2 * kBM - 1) / (2 * kBM), pairs = num_sms / 2;
+  auto cost = [&](int bn) { return (mt * ((s.N + bn - 1) / bn) + pairs - 1) / pairs * (bn + 48); };
+  if (cost(256) <= cost(192) && cost(256) <= cost(128)) return run_act<256, 1, __nv_bfloat16>(c);
+  if (cost(192) <= cost(128)) return run_act<192, 1, __nv_bfloat16>(c);
   return run_act<128, 1, __nv_bfloat16>(c);
 }
 
