@@ -275,7 +275,8 @@ FI_API fi_status fi_op_sync(void* stream);
  * with R as above. Strides are in elements, between positions, sequences and
  * heads ([0], [1], [2]); the innermost dimension is contiguous. q, k and v may
  * be views (of one fused projection, say) and may have a stride of 0 (a
- * position, sequence or head shared by all); o's elements must be distinct. */
+ * position, sequence or head shared by all); o's elements must be distinct and
+ * not among the inputs'. */
 typedef struct {
   int32_t heads;       /* H >= 1 */
   int32_t key_dim;     /* 1..256 */
@@ -316,8 +317,8 @@ FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, c
  * A q, k or v that is not finite at a used position makes outputs of its
  * sequence and head non-finite from that position on, and may do so up to 127
  * positions before it. n = 0 copies the state; n <= 2^30.
- * Errors: FI_E_INVALID (NULL, sizes, strides, alignment, workspace too small),
- * FI_E_CUDA. */
+ * Errors: FI_E_INVALID (NULL, sizes, strides, alignment, o == an input, workspace
+ * too small), FI_E_CUDA. */
 FI_API fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
                                     const float* log_decay, const int32_t* lengths, const float* state_in,
                                     float* state_out, void* o, void* workspace, uint64_t workspace_bytes, void* stream);

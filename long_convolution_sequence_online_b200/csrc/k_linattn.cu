@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   using vec = typename std::conditional<V == 4, float4, typename std::conditional<V == 2, float2, float>::type>::type;
   __shared__ float qs[256], ks[256];
   __shared__ float part[8][32 * V];
-  pdl_launch_dependents();
   pdl_wait_primary();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H;

@@ -4,12 +4,12 @@
 //
 // One CTA runs the chunks of a segment of one (sequence, head) in order. Per
 // chunk, with Q, K, V the 128-row tiles and S the state before it:
-//     scores = Q K^T            -> P = scores * g^{i-j} for j <= i (bf16, in place)
+//     scores = Q K^T            -> P = scale scores * g^{i-j} for j <= i (bf16, in place)
 //     inter  = Q S              (S rounded to bf16 as an operand)
 //     intra  = P V              (P read from tensor memory)
 //     KV     = K^T (w V)        w_j = g^{m-1-j}, w V as three bf16 parts
 //     S     <- g^m S + KV       (fp32, in registers)
-//     o      = scale (g^{i+1} inter + intra)
+//     o      = scale g^{i+1} inter + intra
 // Roundings below fp32: the result, P, and S where it enters Q S. P and S are
 // rounded once each to the results' own type, so each adds an error of the size
 // of the result's own rounding. The state itself must stay an fp32 sum, so w V
@@ -21,7 +21,7 @@
 // DV / 4) block of every matrix, one phase after another; one warp issues the
 // MMAs, one the TMA copies. Per chunk c the workers form the first half of w V,
 // the outputs of chunk c - 1, the second half of w V, P, and the state; the MMAs
-// run in the order KV (first half), Q K^T, KV (second half), Q S, P V. Each phase
+// run in the order KV (first half), Q K^T, Q S, KV (second half), P V. Each phase
 // of the workers then overlaps MMAs that do not need it, and an arrival on
 // w_ready tells the issuer that everything before it in the workers' order is done
 // as well. CTAs are persistent: the copies run ahead into the next task. (Warps
@@ -122,10 +122,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   constexpr int CW = DV / 4;             // a warp's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: unless outputs pass through V's tile
-  __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs_done, p_ready, o_done, o_staged, drained;
+  __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs_done, p_ready, o_done, o_read, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
-  __shared__ float GD[63];               // GD[31 + i] = g^i, i = 0 .. 31 (masked below)
+  __shared__ float GD[63];               // GD[31 + i] = scale g^i, i = 0 .. 31 (masked below)
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   unsigned char* ks = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
@@ -133,7 +133,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   unsigned char* vs = qs + (OUT ? NKQ * L::kTileK : 0);
   unsigned char* sop = vs + NV * L::kTileV;
   unsigned char* wv = sop + L::kState;
-  pdl_launch_dependents();
+  if constexpr (!OUT) pdl_launch_dependents();   // the launch of the outputs, which waits for this one's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tasks = s.B * s.H * p.G;
   const size_t slot = (size_t)s.dk * s.dv;
@@ -154,6 +154,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     bar_init(&qs_done, 1);
     bar_init(&p_ready, kWorkers);
     bar_init(&o_done, 1);
+    bar_init(&o_read, kWorkers);
     bar_init(&o_staged, kWorkers);
     bar_init(&drained, 1);
     abort_s = 0;
@@ -256,7 +257,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       need(&o_done, j & 1);
       fence_after();
       const int64_t t = k.t0 + (int64_t)c * kCh + row;
-      const float f_inter = s.scale * G[row + 1], f_intra = s.scale;
+      const float f_inter = s.scale * G[row + 1];   // P carries the scale
       const bool tile = STAGED && vec_out && !(k.ragged && c == k.nch - 1);
       unsigned char* dst = vs + (j % NV) * L::kTileV + row * 128;
       T* op = (T*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + col0;
@@ -266,11 +267,16 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         tmem_ld16(lanes + C::inter + col0 + d, r);
         tmem_ld16(lanes + C::intra + col0 + d, q);
         ld_wait();
+        if (d + 16 >= CW) {                        // all read: the next products may take their place
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&o_read);
+        }
         if constexpr (PARTS == 3) {
           if (t >= k.end) continue;
           float w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = fmaf(f_inter, __uint_as_float(r[e]), f_intra * __uint_as_float(q[e]));
+          for (int e = 0; e < 16; ++e) w[e] = fmaf(f_inter, __uint_as_float(r[e]), __uint_as_float(q[e]));
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             if (vec_out && col0 + d + e + 4 <= s.dv) {
@@ -286,8 +292,8 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          w[e] = pack2(fmaf(f_inter, __uint_as_float(r[2 * e]), f_intra * __uint_as_float(q[2 * e])),
-                       fmaf(f_inter, __uint_as_float(r[2 * e + 1]), f_intra * __uint_as_float(q[2 * e + 1])));
+          w[e] = pack2(fmaf(f_inter, __uint_as_float(r[2 * e]), __uint_as_float(q[2 * e])),
+                       fmaf(f_inter, __uint_as_float(r[2 * e + 1]), __uint_as_float(q[2 * e + 1])));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int col = col0 + d + 8 * u;
@@ -306,7 +312,6 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           }
         }
       }
-      fence_before();
       if constexpr (STAGED) {
         fence_async();
         __syncwarp();
@@ -324,7 +329,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       sync();                                      // the task before is done with the tables and the stage
       if (tid <= kCh) G[tid] = la_pow(ld2, tid);
       if (tid >= 160 && tid < 192) GR[tid - 160] = la_pow(ld2, 191 - tid);
-      if (tid >= 192 && tid < 192 + 63) GD[tid - 192] = la_pow(ld2, max(0, tid - 192 - 31));
+      if (tid >= 192 && tid < 192 + 63) GD[tid - 192] = s.scale * la_pow(ld2, max(0, tid - 192 - 31));
 #pragma unroll
       for (int e = 0; e < CW; ++e) st[e] = 0.f;
       const float* src = !OUT ? nullptr : p.G > 1 ? ws : s_in;
@@ -427,7 +432,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
               tmem_ld16(lanes + C::scores + 32 * grp + x, r);
               ld_wait();
               if (grp < quarter) {
-                const float gi = G[row - 32 * grp - 31];
+                const float gi = s.scale * G[row - 32 * grp - 31];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                   const float4 g4 = *reinterpret_cast<const float4*>(&GR[x + e]);
@@ -544,16 +549,12 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
             commit(&qk_done);
           }
           __syncwarp();
-        }
-        alive = wait(&w_ready[1], it & 1);
-        if (!alive) break;
-        fence_after();
-        if (issuer) {
-          kv_half(ka, 1);
-          if constexpr (!OUT) commit(&w_free[1]);
-          commit(&kv_done[it & 1]);
-          commit(&k_empty[sk]);
-          if constexpr (OUT) {
+          // the state before was published ahead of w_ready; its product replaces
+          // outputs that have been read
+          alive = it == 0 || wait(&o_read, (it - 1) & 1);
+          if (!alive) break;
+          fence_after();
+          if (issuer) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const uint32_t qp = NC > 1 ? kPairA >> 2 * c & 3 : 0, sp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
@@ -564,7 +565,18 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
             }
             commit(&qs_done);
             commit(&q_empty[sk]);
-          } else {
+          }
+          __syncwarp();
+        }
+        alive = wait(&w_ready[1], it & 1);
+        if (!alive) break;
+        fence_after();
+        if (issuer) {
+          kv_half(ka, 1);
+          if constexpr (!OUT) commit(&w_free[1]);
+          commit(&kv_done[it & 1]);
+          commit(&k_empty[sk]);
+          if constexpr (!OUT) {
             commit(&v_empty[sv]);
           }
         }
@@ -593,7 +605,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // shared and tensor memory are released only once the MMAs issued are done
     if (issuer) commit(&drained);
     __syncwarp();
-    bar_wait(&drained, 0, kDefaultWaitLimit);
+    bar_wait(&drained, 0, kDrainLimit);
   } else {
     // ------------------------------------------------------------ TMA
     // Loads of chunk `it` go out as soon as the tiles' last readers are done, over
@@ -680,10 +692,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // no copy of this CTA may still be in flight when it ends
     if (issuer) bulk_wait();
     __syncwarp();
-    for (int x = max(0, wv_.j - NV); x < wv_.j; ++x) bar_wait(&v_full[x % NV], (x / NV) & 1, kDefaultWaitLimit);
+    for (int x = max(0, wv_.j - NV); x < wv_.j; ++x) bar_wait(&v_full[x % NV], (x / NV) & 1, kDrainLimit);
     for (int x = max(0, wk.j - NKQ); x < wk.j; ++x) {
-      bar_wait(&k_full[x % NKQ], (x / NKQ) & 1, kDefaultWaitLimit);
-      if constexpr (OUT) bar_wait(&q_full[x % NKQ], (x / NKQ) & 1, kDefaultWaitLimit);
+      bar_wait(&k_full[x % NKQ], (x / NKQ) & 1, kDrainLimit);
+      if constexpr (OUT) bar_wait(&q_full[x % NKQ], (x / NKQ) & 1, kDrainLimit);
     }
   }
   fence_before();
@@ -725,7 +737,7 @@ struct LaOperands {
 };
 template <typename T>
 __global__ void __launch_bounds__(256) k_linattn_layout(LaOperands ops, int B, int H, int64_t rows) {
-  pdl_launch_dependents();
+  pdl_launch_dependents();                 // the attention itself, which waits for this launch's end
   pdl_wait_primary();
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < ops.end[2]; u += (int64_t)gridDim.x * 256) {
     const int i = u < ops.end[0] ? 0 : u < ops.end[1] ? 1 : 2;

@@ -49,7 +49,6 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   __shared__ int abort_s;
   unsigned char* ring = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
   const int rank = split > 1 ? (int)cluster_rank() : 0;
   const int row0 = (int)(blockIdx.x / split) * kBM;
   const int blocks = (s.K + kBK - 1) / kBK;
@@ -96,7 +95,7 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
     }
     if (!alive && lane == 0) give_up();
     // no copy of this CTA may still be in flight when its memory is reused
-    for (int j = i > ST ? i - ST : 0; j < i; ++j) bar_wait(&full[j % ST], (j / ST) & 1, kDefaultWaitLimit);
+    for (int j = i > ST ? i - ST : 0; j < i; ++j) bar_wait(&full[j % ST], (j / ST) & 1, kDrainLimit);
   } else if (warp == 1) {
     const bool issuer = elect_one();
     constexpr uint32_t id = idesc(kBM, NT);
@@ -155,7 +154,7 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   if (split > 1) cluster_sync();
   else __syncthreads();
   // Four rows of W and one row of x at a time; every CTA's sums are asked for
-  // before the first is used (one at a time, 64 rows took 9.1 us instead of FEW_US).
+  // before the first is used (one at a time, 64 rows of 2048 -> 2048 took 9.1 us instead of 7.1).
   const int quads = kBM / 4 / split;                       // of this CTA to finish
   const int r = (rank * quads + tid % quads) * 4, c = row0 + r;
   if (c < s.N) {
@@ -213,7 +212,6 @@ template <typename T, int ACT, bool VEC, int RW>
 __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __restrict__ x, const T* __restrict__ w,
                                                     const T* __restrict__ bias, const T* residual, T* y) {
   __shared__ __align__(16) float xs[kWarpRows][kRowsK];
-  pdl_launch_dependents();
   pdl_wait_primary();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = (blockIdx.x * 8 + warp) * RW;

@@ -20,8 +20,9 @@
 // bits), and the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 are added up (the
 // rest is below 2^-24). The tensor core does not round its sums to nearest: left
 // in one accumulator, such products at a contraction of 2048 were 1.4e-5 off in
-// the 2-norm, 1.3e-7 with each block of 64 in an accumulator of its own (smallest
-// products first) and the blocks added up in the epilogue warps' registers.
+// the 2-norm; with two blocks of 64 to an accumulator (smallest products of a block
+// first), added up in the epilogue warps' registers, they are 7e-7 off, cuBLAS's fp32
+// product 8e-7.
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -38,12 +39,12 @@ constexpr int kLinThreads = 32 * (kEpiWarps + 2);
 
 __device__ int g_linear_error;   // a bounded wait gave up since the last check
 
+// fp32: blocks that share an accumulator before the epilogue warps add them up.
+constexpr int kSumBlocks = 2;
 // Stage of the ring: `units` x (x tile 128 x 128 bytes, half of a W tile BN / 2 x
 // 128 bytes). The units are the parts of fp32 values, or two blocks of the
 // contraction: a stage's waits and signals take 350 to 450 cycles whatever its
 // size, more than the 264 that the MMAs of one block take at BN = 128.
-// fp32: blocks that share an accumulator before the epilogue warps add them up.
-constexpr int kSumBlocks = 2;
 template <int PARTS>
 constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
 template <int BN, int PARTS>
@@ -182,7 +183,6 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   float* staging = reinterpret_cast<float*>(ring + (size_t)ST * SB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &abort_s;
-  pdl_launch_dependents();
   const int rank = (int)cluster_rank();
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   if (warp == 0) tmem_alloc2(&tmem_s, acc_cols<BN>());
@@ -332,7 +332,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       }
       if (!alive && lane == 0) give_up();
       // shared and tensor memory are released only once the last MMAs are done
-      if (kbs > 0) bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDefaultWaitLimit);
+      if (kbs > 0) bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDrainLimit);
     }
     __syncwarp();
   } else {
@@ -364,7 +364,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     }
     if (!alive && lane == 0) give_up();
     // no copy of this CTA may still be in flight when it ends: each stage's last use is done
-    for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDefaultWaitLimit);
+    for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDrainLimit);
   }
   fence_before();
   cluster_sync_relaxed();                          // neither CTA ends while the other may still signal it
@@ -383,7 +383,7 @@ struct LinOperand {
 };
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand b, int K, int Kp, int64_t units_a, int64_t units) {
-  pdl_launch_dependents();
+  pdl_launch_dependents();                 // the product, which waits for this launch's end
   pdl_wait_primary();
   const int per = Kp / 8;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {

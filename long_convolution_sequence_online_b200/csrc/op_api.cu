@@ -135,6 +135,7 @@ fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void
   if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(log_decay, 4) ||
       !aligned(lengths, 4) || !aligned(state_in, 4) || !aligned(state_out, 4))
     return invalid("a pointer is not aligned to its element size");
+  if (n > 0 && (o == q || o == k || o == v)) return invalid("o must not be an input");
   s.n = n;
   int sms = 0;
   cudaError_t e = device_sms(&sms);
@@ -157,6 +158,7 @@ fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const voi
   if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(log_decay, 4) ||
       !aligned(state, 4))
     return invalid("a pointer is not aligned to its element size");
+  if (o == q || o == k || o == v) return invalid("o must not be an input");
   s.n = 1;
   int sms = 0;
   cudaError_t e = device_sms(&sms);

@@ -9,6 +9,12 @@
 
 namespace fi {
 
+// The operators' launches allow programmatic stream serialization and wait for the
+// launch before them ahead of their first read or write of global memory. Only
+// those that another launch of the same call follows let that one start early: a
+// later launch of the library's (the chunk kernel, say) reads what it takes for
+// long finished before it waits, and that may be an operator's result.
+
 // Allows a kernel `bytes` of dynamic shared memory, once per device (a kernel's
 // need is a constant of its instantiation).
 template <auto Kern>

@@ -36,10 +36,14 @@ __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(saddr(bar)), "r"(parity) : "memory");
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(saddr(bar)), "r"(parity), "r"(1000u) : "memory");
   return ok != 0;
 }
+// Checks (of at most about a microsecond) after which a wait for copies or products
+// that are under way gives up, at the end of a kernel: they take microseconds.
+constexpr int kDrainLimit = 1 << 16;
+
 // Bounded waits of a whole warp (or of a single thread: the first form), which give
 // up after `limit` checks; the second also once another role of the CTA has given
 // up. A phase that is complete already, the usual case in a pipeline, is seen by
