@@ -100,6 +100,11 @@ LA_CASES = [
     (2500, 2, 1, 64, 64, False, [2500, 1301], True),
     (150, 1, 2, 200, 256, False, None, True),      # dimensions above 128
     (400, 1, 1, 256, 130, False, None, False),
+    (1500, 2, 1, 64, 128, True, [1500, 640], True),
+    (1100, 1, 2, 128, 64, False, None, True),
+    (900, 3, 1, 24, 100, True, [900, 128, 700], True),
+    (640, 1, 1, 40, 40, False, None, True),        # whole chunks only
+    (260, 160, 1, 16, 16, False, None, False),     # more heads than SMs: a CTA takes several
 ]
 
 
@@ -228,6 +233,49 @@ def test_prefill_not_finite_values(fi, dtype):
     assert torch.isfinite(S[0]).all() and torch.isfinite(S[1, 1]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefill_lengths_are_clamped(fi, dtype):
+    n = 140
+    q, k, v, ld, s0 = _la_inputs(n, 3, 1, 64, 64, dtype, 61)
+    outs = []
+    for lens in ([-7, 10 ** 6, 90], [0, n, 90]):
+        o, S = torch.zeros(n, 3, 1, 64, dtype=DT[dtype], device="cuda"), torch.empty_like(s0)
+        fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, lengths=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        outs.append((o, S))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.equal(outs[0][1][0], s0[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_prefill_positions_far_apart(fi, shift, dtype):
+    # element offsets beyond 2^31, at 16-byte boundaries and not
+    n, H, d = 280, 2, 32
+    ld = (1 << 23) + 8
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def far():
+        t = torch.empty(n * ld + 8, dtype=DT[dtype], device="cuda")[shift:].as_strided((n, 1, H, d), (ld, ld, d, 1))
+        t.copy_(_rand(g, n, 1, H, d))
+        return t
+
+    q, k, v, o = far(), far(), far(), far()
+    ld_ = torch.log(torch.tensor([0.9, 0.99], device="cuda"))
+    S = torch.empty(1, H, d, d, device="cuda")
+    fi.linattn_prefill(q, k, v, ld_, o, state_out=S)
+    torch.cuda.synchronize()
+    _check_la(o, S, q, k, v, ld_, 1.0, None, None, dtype)
+    B = n                                          # the positions as sequences: one step for each
+    qs, ks, vs, os = (t.transpose(0, 1)[0] for t in (q, k, v, o))
+    Ss = torch.zeros(B, H, d, d, device="cuda")
+    fi.linattn_step(qs, ks, vs, ld_, Ss, os)
+    torch.cuda.synchronize()
+    want = np.einsum("bhd,bhd->bh", _f64(qs), _f64(ks))[..., None] * _f64(vs)
+    A = np.einsum("bhd,bhd->bh", np.abs(_f64(qs)), np.abs(_f64(ks)))[..., None] * np.abs(_f64(vs))
+    assert np.all(np.abs(_f64(os) - want) <= (d + 16) * U32 * A + (U16 * np.abs(want) if dtype == "bf16" else 0))
+
+
 STEP_CASES = [(1, 1, 64, 64), (2, 3, 128, 128), (5, 9, 56, 104), (3, 2, 1, 1), (2, 2, 33, 47), (1, 2, 256, 256),
               (4, 1, 200, 130), (64, 16, 128, 128), (1, 12, 64, 64), (70, 2, 32, 200)]
 
@@ -324,6 +372,15 @@ LIN_CASES = [
     (300, 864, 865, "none", True, True),
     (513, 33, 2000, "none", True, False),
     (1000, 200, 130, "gelu", True, True),
+    (1777, 96, 1728, "tanh", True, True),          # one round of tiles
+    (2304, 64, 4096, "none", False, True),         # several rounds
+    (4100, 72, 2049, "relu", True, False),
+    (3, 100, 5000, "none", True, True),
+    (8, 1030, 5001, "relu", False, True),
+    (9, 1000, 300, "silu", True, False),
+    (31, 700, 200, "none", True, True),
+    (40, 8200, 100, "none", False, False),
+    (128, 512, 384, "tanh", False, True),
 ]
 
 
@@ -400,6 +457,26 @@ def test_linear_no_rows(fi):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 40, 200])
+def test_linear_rows_far_apart(fi, n, dtype):
+    # element offsets beyond 2^31 in x, w, residual and y
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dt = DT[dtype]
+    ld, nin, nout = (1 << 24) + 8, 72, 130
+    far = max(n, nout)
+
+    def rows(count, cols, scale=1.0):
+        t = torch.empty(far * ld, dtype=dt, device="cuda").as_strided((count, cols), (ld, 1))
+        t.copy_(_rand(g, count, cols, scale=scale))
+        return t
+
+    x, w, r, y = rows(n, nin), rows(nout, nin, nin ** -0.5), rows(n, nout), rows(n, nout)
+    fi.linear(x, w, y, residual=r, act="relu")
+    torch.cuda.synchronize()
+    _check_linear(y, x, w, None, r, "relu", dtype)
+
+
 # ------------------------------------------------------------------ refusals of the binding
 
 def test_binding_refusals(fi):
@@ -471,6 +548,94 @@ def test_captured_graph_replays_with_new_inputs(fi, dtype):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_two_graphs_with_scratch_at_once(fi):
+    # two captured graphs whose calls need scratch (fp32 operands), replayed on two
+    # streams at the same time, give what they give one after the other
+    g = torch.Generator(device="cuda").manual_seed(4)
+    graphs, outs, runs = [], [], []          # a graph's tensors live as long as it does
+    for i in range(2):
+        x, w, y = _rand(g, 700, 500), _rand(g, 300, 500, scale=0.05), torch.empty(700, 300, device="cuda")
+        q, k, v, ld, s0 = _la_inputs(1500, 1, 2, 64, 64, "f32", 90 + i)
+        o, S = torch.empty_like(v), torch.empty_like(s0)
+
+        def run(x=x, w=w, y=y, q=q, k=k, v=v, ld=ld, s0=s0, o=o, S=S):
+            fi.linear(x, w, y, act="gelu")
+            fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S)
+
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graphs.append(graph)
+        runs.append(run)
+        outs.append((y, o, S))
+    want = []
+    for graph, out in zip(graphs, outs):
+        graph.replay()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for out in outs:
+            for t in out:
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            for s, t in zip(a, b):
+                assert torch.equal(s, t)
+    fi.op_sync()
+
+
+def test_a_context_reads_what_an_operator_has_just_written(fi):
+    # the noise of a generation comes from a linear layer launched right before it; the
+    # generation's first kernel reads noise before it waits for the launch ahead of it
+    g = torch.Generator(device="cuda").manual_seed(12)
+    M, D, L, B, n = 2, 64, 256, 16, 256
+    h = torch.randn(M, D, L, generator=g, device="cuda") * torch.exp(-0.2 * torch.arange(L, device="cuda"))
+    x, w = _rand(g, n * B, 2048), _rand(g, D, 2048, scale=0.02)
+    x0 = _rand(g, B, D)
+    ys = []
+    for wait in (True, False, False):
+        ctx = fi.Context(h, B, "f32")
+        eps, y = torch.zeros(n, B, D, device="cuda"), torch.empty(n, B, D, device="cuda")
+        torch.cuda.synchronize()
+        fi.linear(x, w, eps.view(n * B, D))
+        if wait:
+            torch.cuda.synchronize()
+        ctx.generate(n, x0, eps, y, 0.1)
+        ctx.sync()
+        ctx.close()
+        ys.append(y)
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+def test_scratch_that_is_too_small_is_refused(fi):
+    import ctypes
+    x = torch.empty(300, 64, device="cuda")
+    cfg = fi.LinearConfig(64, 300, fi.FI_F32, 0, 64, 64, 300, 300)
+    y = torch.empty(300, 300, device="cuda")
+    need = ctypes.c_uint64()
+    at, p = ctypes.addressof(cfg), x.data_ptr()
+    assert fi.lib.fi_linear_workspace(at, 300, p, p, ctypes.byref(need)) == fi.FI_OK and need.value > 0
+    ws = torch.empty(need.value + 256, dtype=torch.uint8, device="cuda")
+    for ptr, size in ((None, need.value), (ws.data_ptr(), need.value - 1), (ws.data_ptr() + 16, need.value)):
+        assert fi.lib.fi_linear(at, 300, p, p, None, None, y.data_ptr(), ptr, size, None) == fi.FI_E_INVALID
+        assert "workspace" in fi.lib.fi_last_error().decode()
+    la = fi.LinattnConfig(1, 64, 64, 1, fi.FI_F32, 1.0)
+    for name in ("q_stride", "k_stride", "v_stride", "o_stride"):
+        getattr(la, name)[:] = (64, 64, 64)
+    assert fi.lib.fi_linattn_workspace(ctypes.addressof(la), 300, p, p, p, ctypes.byref(need)) == fi.FI_OK and need.value > 0
+    ld = torch.zeros(1, device="cuda")
+    assert fi.lib.fi_linattn_prefill(ctypes.addressof(la), 300, p, p, p, ld.data_ptr(), None, None, None, y.data_ptr(),
+                                     ws.data_ptr(), need.value - 1, None) == fi.FI_E_INVALID
+    assert "workspace" in fi.lib.fi_last_error().decode()
 
 
 def test_calls_on_two_streams_at_once(fi):

@@ -180,6 +180,37 @@ def test_linear_refuses_nulls_alignment_and_aliases():
     assert L.fi_linear(at, 0, x, w, b, r, y, None, 0, None) == fi.FI_OK      # no rows: nothing to do
 
 
+def test_linear_scratch_is_known_without_a_device():
+    fi = _fi()
+    need = ctypes.c_uint64(7)
+    at = ctypes.c_void_p
+    aligned, odd = at(4096), at(4098)
+    bf = _lin(fi, in_features=64, ldx=64, ldw=64, dtype=fi.FI_BF16)
+    ask = lambda cfg, n, x, w: (fi.lib.fi_linear_workspace(ctypes.addressof(cfg), n, x, w, ctypes.byref(need)), need.value)   # noqa: E731
+    assert ask(bf, 300, aligned, aligned) == (fi.FI_OK, 0)
+    assert ask(bf, 300, odd, aligned) == (fi.FI_OK, 300 * 64 * 2)           # x alone
+    assert ask(bf, 300, aligned, odd) == (fi.FI_OK, 16 * 64 * 2)            # w alone
+    assert ask(bf, 1, odd, odd) == (fi.FI_OK, 0)                            # one row reads them as they stand
+    f32 = _lin(fi, in_features=60, ldx=60, ldw=60)
+    assert ask(f32, 300, aligned, aligned) == (fi.FI_OK, -(-3 * 300 * 64 * 2 // 256) * 256 + 3 * 16 * 64 * 2)
+    assert ask(f32, 0, aligned, aligned) == (fi.FI_OK, 0)
+    assert fi.lib.fi_linear_workspace(ctypes.addressof(f32), 300, aligned, aligned, None) == fi.FI_E_INVALID
+    assert fi.lib.fi_linear(ctypes.addressof(f32), 300, at(1 << 20), at(1 << 21), None, None, at(1 << 22), None, 0, None) == fi.FI_E_INVALID
+    assert "workspace" in fi.lib.fi_last_error().decode()
+
+
+def test_linattn_refuses_outputs_among_inputs():
+    fi = _fi()
+    cfg = _la(fi)
+    at = ctypes.addressof(cfg)
+    p = [ctypes.c_void_p(1 << (12 + i)) for i in range(5)]
+    for i in range(3):
+        assert fi.lib.fi_linattn_prefill(at, 5, p[0], p[1], p[2], p[3], None, None, None, p[i], None, 0, None) == fi.FI_E_INVALID
+        assert "o must not" in fi.lib.fi_last_error().decode()
+        assert fi.lib.fi_linattn_step(at, p[0], p[1], p[2], p[3], p[4], p[i], None) == fi.FI_E_INVALID
+        assert "o must not" in fi.lib.fi_last_error().decode()
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     fi = _fi()
