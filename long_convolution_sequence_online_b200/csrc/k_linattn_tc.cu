@@ -4,7 +4,7 @@
 //
 // One CTA runs the chunks of a segment of one (sequence, head) in order. Per
 // chunk, with Q, K, V the 128-row tiles and S the state before it:
-//     scores = Q K^T            -> P = scale scores * g^{i-j} for j <= i (bf16, in place)
+//     scores = Q K^T            -> P = scale scores * g^{i-j} for j <= i (bf16, over them)
 //     inter  = Q S              (S rounded to bf16 as an operand)
 //     intra  = P V              (P read from tensor memory)
 //     KV     = K^T (w V)        w_j = g^{m-1-j}, w V as three bf16 parts
@@ -455,10 +455,14 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
               else split3(f[e], f[e + 1], out[0][(x + e) / 2], out[PARTS / 2][(x + e) / 2], out[PARTS - 1][(x + e) / 2]);
             }
           }
-          // P takes the place of scores that the other warps of these rows read
-          if constexpr (PARTS == 1) asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+          // one part: over this block's own scores (the product takes 16 columns of P at a
+          // time from anywhere), so no warp waits for the others' reads
+          if constexpr (PARTS == 1) {
+            tmem_st16(lanes + C::p + 32 * grp, out[0]);
+          } else {
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) tmem_st16(lanes + C::p + 64 * part + 16 * grp, out[part]);
+            for (int part = 0; part < PARTS; ++part) tmem_st16(lanes + C::p + 64 * part + 16 * grp, out[part]);
+          }
           st_wait();
           fence_before();
           __syncwarp();
@@ -591,7 +595,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
               const uint32_t pp = NC > 1 ? kPairA >> 2 * c & 3 : 0, vp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
 #pragma unroll
               for (int x = 0; x < kCh / 16; ++x)
-                mma_ta(tmem + C::intra, tmem + C::p + 64 * pp + 8 * x, desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
+                mma_ta(tmem + C::intra, tmem + C::p + (PARTS == 1 ? 32 * (x / 2) + 8 * (x % 2) : 64 * pp + 8 * x), desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
                        id_pv, c > 0 || x > 0);
             }
             commit(&o_done);
