@@ -49,14 +49,14 @@ template <int PARTS>
 constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
 template <int BN, int PARTS>
 constexpr int stage_bytes() { return PARTS * kStageBlocks<PARTS> * (kBM + BN / 2) * 128; }
-// VEC kernels need no staging and have room for more: fp32 3 stages instead of 2.
-template <int BN, int PARTS, bool VEC>
-constexpr int num_stages() { return (VEC ? 229376 : 196608) / stage_bytes<BN, PARTS>(); }
-constexpr int kStagingCols = 16, kStagingLd = kStagingCols + 1;
-constexpr int kStagingBytes = kEpiWarps * 32 * kStagingLd * 4;
-template <int BN, int PARTS, bool VEC>
+template <int BN, int PARTS>
+constexpr int num_stages() { return 196608 / stage_bytes<BN, PARTS>(); }
+// bytes of an epilogue warp's stage (Staged below): 32 rows of 32 results and 16 bytes, 32 biases
+template <int PARTS>
+constexpr int staging_bytes() { return 32 * (32 * (PARTS == 3 ? 4 : 2) + 16) + 128; }
+template <int BN, int PARTS>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)num_stages<BN, PARTS, VEC>() * stage_bytes<BN, PARTS>() + (VEC ? 0 : kStagingBytes);
+  return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kEpiWarps * staging_bytes<PARTS>();
 }
 template <int BN>
 constexpr uint32_t acc_cols() { return BN <= 128 ? 256 : 512; }   // two accumulators
@@ -81,98 +81,189 @@ __device__ __forceinline__ float activate(float u) {
   else return linear_act<ACT>(u);
 }
 
-// act(acc + bias) + residual of 32 columns of a row per lane, to y: the lane
-// finishes and stores its row's columns, 16 bytes at a time.
-template <typename T, int ACT>
-__device__ __forceinline__ void store_vec(const LinShape& s, float (&v)[32], const T* bias, const T* residual, T* y,
-                                          int64_t row, int c0) {
-  constexpr int E = 16 / sizeof(T);
-  auto add = [&](const uint4& b, int u) {
-    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+// act(acc + bias) + residual of 32 columns, a row per lane, go to y by way of shared
+// memory, so that a warp's accesses to memory run along the rows (a row per lane costs a lookup per lane and access: 8192 x 768 -> 2048 bf16 25.4
+// us, along the rows 21.4). Rows may start anywhere (not ALIGNED) and end inside the
+// chunk: each is moved up in shared memory by the elements `a` that its address in
+// memory is past a 16-byte boundary, so that memory is still read and written in whole
+// units of 16 bytes; its 32 elements then start with E - a single ones, end with a, and
+// have units between (a = 0: units alone). A lane's rows lie 8 or E apart and so share
+// their a, which keeps addresses out of the loops: with two warps per scheduler it is
+// instructions that bound this. (8192 x 768 -> 767 bf16 + GELU + residual: 23.6 us, 36.0
+// with addresses formed per access; 1777 x 865 -> 1727 + tanh + residual: 20.7, 27.3 an
+// element at a time.)
+template <typename T, bool ALIGNED>
+struct StagedSide {                                        // y or the residual: the warp's 32 rows
+  static constexpr int E = 16 / sizeof(T), U = 32 / E;     // elements of a unit, units of a chunk
+  static constexpr int H = E / 4;                          // single elements of a lane and row
+  static constexpr int kWords = 32 * sizeof(T) / 4, kRow = 32 * sizeof(T) + 16;
+  T* p;
+  int64_t ld;
+  T *unit_p, *single_p[H];
+  int unit_s, single_s[H], row_a;                          // places in the stage; a of the lane's own row
+  int units, singles;                                      // the lane's first row, or 32: it has no such
+
+  static __device__ __forceinline__ int past(const T* q) { return ALIGNED ? 0 : (int)((uintptr_t)q / sizeof(T)) & (E - 1); }
+  __device__ __forceinline__ void init(T* first, int64_t stride, int lane) {
+    p = first;
+    ld = stride;
+    row_a = past(p + lane * ld);
+    int r = lane / U, a = past(p + r * ld), c = (E - a) % E + E * (lane % U);
+    unit_p = p + r * ld + c;
+    unit_s = r * kRow + (c + a) * (int)sizeof(T);
+    units = lane % U < U - 1 || a == 0 ? r : 32;
+    r = lane % 8;
+    a = past(p + r * ld);
+    singles = a != 0 ? r : 32;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (sizeof(T) == 2) {
-        v[u * 8 + 2 * e] += lo_f(w[e]);
-        v[u * 8 + 2 * e + 1] += hi_f(w[e]);
-      } else {
-        v[u * 4 + e] += __uint_as_float(w[e]);
+    for (int h = 0; h < H; ++h) {
+      const int e = lane / 8 + 4 * h;
+      c = e < E - a ? e : 32 - E + e;
+      single_p[h] = p + r * ld + c;
+      single_s[h] = r * kRow + (c + a) * (int)sizeof(T);
+    }
+  }
+  __device__ __forceinline__ unsigned char* at(unsigned char* stg, int r, int c) const {
+    return stg + r * kRow + (c + past(p + r * ld)) * (int)sizeof(T);
+  }
+};
+
+template <typename T, bool ALIGNED>
+struct Staged {
+  using S = StagedSide<T, ALIGNED>;
+  static constexpr int E = S::E, U = S::U, H = S::H, kWords = S::kWords, kRow = S::kRow;
+  S y, res;
+  uint4 unit[U];                                           // a lane's share of a residual on its way
+  T single[4 * H];
+
+  __device__ __forceinline__ void fetch(int c, int rows) {   // the columns c .. c + 31 are there
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (res.units + E * i < rows) unit[i] = *reinterpret_cast<const uint4*>(res.unit_p + c + i * (E * res.ld));
+#pragma unroll
+    for (int i = 0; i < 4 && !ALIGNED; ++i)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (res.singles + 8 * i < rows) single[i * H + h] = res.single_p[h][c + i * (8 * res.ld)];
+  }
+
+  // v = act(v + bias) + residual of a row per lane, to y's columns c on. rows, cols:
+  // how many there are. With 32 columns the residual has been fetched, and next()
+  // fetches the next chunk's.
+  template <int ACT, typename Next>
+  __device__ __forceinline__ void store(float (&v)[32], int c, int rows, int cols, const T* bias, bool residual, Next next,
+                                        unsigned char* stg, int lane) {
+    const bool whole = cols >= 32;
+    float* bs = reinterpret_cast<float*>(stg + 32 * kRow);
+    bs[lane] = bias && lane < cols ? op_load(bias + lane) : 0.f;
+    if (residual) {
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (res.units + E * i < rows) *reinterpret_cast<uint4*>(stg + res.unit_s + i * (E * kRow)) = unit[i];
+#pragma unroll
+        for (int i = 0; i < 4 && !ALIGNED; ++i)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (res.singles + 8 * i < rows) *reinterpret_cast<T*>(stg + res.single_s[h] + i * (8 * kRow)) = single[i * H + h];
+        next();
+      } else if (lane < cols) {
+#pragma unroll 16
+        for (int r = 0; r < rows; ++r) *reinterpret_cast<T*>(res.at(stg, r, lane)) = res.p[r * res.ld + c + lane];
       }
     }
-  };
-  if (bias) {
-#pragma unroll
-    for (int u = 0; u < 32 / E; ++u) add(__ldg(reinterpret_cast<const uint4*>(bias + c0) + u), u);
-  }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = activate<T, ACT>(v[e]);
-  if (row >= s.n) return;
-  if (residual) {
-    const T* rp = residual + row * s.ldr + c0;
-#pragma unroll
-    for (int u = 0; u < 32 / E; ++u) add(*(reinterpret_cast<const uint4*>(rp) + u), u);
-  }
-  T* yp = y + row * s.ldy + c0;
-#pragma unroll
-  for (int u = 0; u < 32 / E; ++u) {
-    uint4 o;
-    if constexpr (sizeof(T) == 2)
-      o = make_uint4(pack2(v[u * 8], v[u * 8 + 1]), pack2(v[u * 8 + 2], v[u * 8 + 3]),
-                     pack2(v[u * 8 + 4], v[u * 8 + 5]), pack2(v[u * 8 + 6], v[u * 8 + 7]));
-    else
-      o = make_uint4(__float_as_uint(v[u * 4]), __float_as_uint(v[u * 4 + 1]), __float_as_uint(v[u * 4 + 2]),
-                     __float_as_uint(v[u * 4 + 3]));
-    *(reinterpret_cast<uint4*>(yp) + u) = o;
-  }
-}
-
-// The same where columns end inside the chunk or rows start at no 16-byte boundary:
-// the sums pass through shared memory and a lane finishes a column's rows (column
-// c0 + lane % 16 or + 16, rows lane / 16, + 2, ...), so that loads and stores run
-// along the columns.
-template <typename T, int ACT>
-__device__ __forceinline__ void store_apart(const LinShape& s, const float (&v)[32], const T* bias, const T* residual, T* y,
-                                            int64_t row0, int c0, float* stg, int lane) {
-  const int rows = (int)min((int64_t)32, s.n - row0), cl = lane & 15, r0 = lane >> 4;
-  float res[2][16], bv[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {            // everything that comes from memory first
-    const int c = c0 + 16 * h + cl;
-    bv[h] = bias && c < s.N ? op_load(bias + c) : 0.f;
-    const T* rp = residual + (row0 + r0) * s.ldr + c;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      res[h][r] = residual && c < s.N && r0 + 2 * r < rows ? op_load(rp) : 0.f;
-      rp += 2 * s.ldr;
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int e = 0; e < kStagingCols; ++e) stg[lane * kStagingLd + e] = v[16 * h + e];
-    const int c = c0 + 16 * h + cl;
-    T* yp = y + (row0 + r0) * s.ldy + c;
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      if (c < s.N && r0 + 2 * r < rows) op_store(yp, activate<T, ACT>(stg[(r0 + 2 * r) * kStagingLd + cl] + bv[h]) + res[h][r]);
-      yp += 2 * s.ldy;
+    for (int e = 0; e < 32; e += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(bs + e);
+      v[e] = activate<T, ACT>(v[e] + b.x);
+      v[e + 1] = activate<T, ACT>(v[e + 1] + b.y);
+      v[e + 2] = activate<T, ACT>(v[e + 2] + b.z);
+      v[e + 3] = activate<T, ACT>(v[e + 3] + b.w);
+    }
+    // a row is moved by the bits of its a, words of 4 bytes first
+    uint32_t w[kWords + 4];
+    unsigned char* mine = stg + lane * kRow;
+    if (residual) {
+#pragma unroll
+      for (int k = 0; k < kWords + 4; k += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(mine + 4 * k);
+        w[k] = q.x; w[k + 1] = q.y; w[k + 2] = q.z; w[k + 3] = q.w;
+      }
+      const int by = res.row_a * (int)sizeof(T) / 4;
+#pragma unroll
+      for (int k = 0; k < kWords + 2; ++k) w[k] = by & 2 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < kWords + 1; ++k) w[k] = by & 1 ? w[k + 1] : w[k];
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t sel = res.row_a & 1 ? 0x5432 : 0x3210;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          const uint32_t x = __byte_perm(w[k], w[k + 1], sel);
+          v[2 * k] += lo_f(x);
+          v[2 * k + 1] += hi_f(x);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) v[k] += __uint_as_float(w[k]);
+      }
+      __syncwarp();
+    }
+    const int by = y.row_a * (int)sizeof(T) / 4;
+#pragma unroll
+    for (int k = 0; k < kWords + 4; ++k) w[k] = 0;
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t sel = y.row_a & 1 ? 0x5432 : 0x7654;
+      uint32_t before = 0;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t x = pack2(v[2 * k], v[2 * k + 1]);
+        w[k] = __byte_perm(before, x, sel);
+        before = x;
+      }
+      w[kWords] = before >> 16;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) w[k] = __float_as_uint(v[k]);
+    }
+#pragma unroll
+    for (int k = kWords + 1; k > 0; --k) w[k] = by & 1 ? w[k - 1] : w[k];
+#pragma unroll
+    for (int k = kWords + 3; k > 1; --k) w[k] = by & 2 ? w[k - 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < kWords + 4; k += 4)
+      *reinterpret_cast<uint4*>(mine + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+    __syncwarp();
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (y.units + E * i < rows)
+          *reinterpret_cast<uint4*>(y.unit_p + c + i * (E * y.ld)) =
+              *reinterpret_cast<const uint4*>(stg + y.unit_s + i * (E * kRow));
+#pragma unroll
+      for (int i = 0; i < 4 && !ALIGNED; ++i)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          if (y.singles + 8 * i < rows) y.single_p[h][c + i * (8 * y.ld)] = *reinterpret_cast<const T*>(stg + y.single_s[h] + i * (8 * kRow));
+    } else if (lane < cols) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) y.p[r * y.ld + c + lane] = *reinterpret_cast<const T*>(y.at(stg, r, lane));
     }
     __syncwarp();
   }
-}
+};
 
 // BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32; part p of a matrix is its rows
-// p n .. (p + 1) n). VEC: rows of y, bias and residual at 16-byte boundaries and
-// whole chunks of 32 columns only. An epilogue warp drains tensor-memory lanes 32 (w % 4) .. + 31,
-// column half w / 4.
-template <int BN, int PARTS, bool VEC, typename T, int ACT>
+// p n .. (p + 1) n). ALIGNED: rows of y and residual at 16-byte boundaries. An epilogue
+// warp drains tensor-memory lanes 32 (w % 4) .. + 31, column half w / 4.
+template <int BN, int PARTS, bool ALIGNED, typename T, int ACT>
 __global__ void __launch_bounds__(kLinThreads, 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
             const T* __restrict__ bias, const T* residual, T* y,
             int wait_limit) {
   constexpr int BW = BN / 2;                       // W rows in this CTA's stages
   constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
-  constexpr int ST = num_stages<BN, PARTS, VEC>(), SB = stage_bytes<BN, PARTS>();
+  constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
   constexpr int XB = kBM * 128, WB = BW * 128;
   constexpr int TM = 2 * kBM;                      // rows of a tile
   extern __shared__ unsigned char raw_smem[];
@@ -180,7 +271,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   unsigned char* ring = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
-  float* staging = reinterpret_cast<float*>(ring + (size_t)ST * SB);
+  unsigned char* staging = ring + (size_t)ST * SB;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &abort_s;
   const int rank = (int)cluster_rank();
@@ -213,7 +304,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = warp >> 2;
     constexpr int CW = BN / 2;                     // columns of this warp
-    float* stg = staging + warp * 32 * kStagingLd;
+    unsigned char* stg = staging + warp * staging_bytes<PARTS>();
     uint32_t unit = 0;                             // accumulators drained
     bool alive = true;
     for (int t = first; t < g.tiles && alive; t += stride) {
@@ -228,11 +319,19 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         const int bytes = min(CW, s.N - col0) * (int)sizeof(T);
         for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + o));
       }
-      auto store = [&](float (&v)[32], int c) {
-        if (row0 >= s.n || col0 + c >= s.N) return;
-        if constexpr (VEC) store_vec<T, ACT>(s, v, bias, residual, y, row0 + lane, col0 + c);
-        else store_apart<T, ACT>(s, v, bias, residual, y, row0, col0 + c, stg, lane);
+      const int rows = (int)min((int64_t)32, s.n - row0);   // may be negative
+      Staged<T, ALIGNED> staged;
+      staged.y.init(y + row0 * s.ldy + col0, s.ldy, lane);
+      if (residual) staged.res.init(const_cast<T*>(residual) + row0 * s.ldr + col0, s.ldr, lane);
+      auto fetch = [&](int c) {
+        if (residual && c < CW && rows > 0 && col0 + c + 32 <= s.N) staged.fetch(c, rows);
       };
+      auto store = [&](float (&v)[32], int c) {
+        if (rows <= 0 || col0 + c >= s.N) return;
+        staged.template store<ACT>(v, c, rows, s.N - col0 - c, bias ? bias + col0 + c : nullptr, residual != nullptr,
+                                   [&] { fetch(c + 32); }, stg, lane);
+      };
+      fetch(0);
       if constexpr (PARTS == 1) {
         alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
         if (!alive) break;
@@ -419,12 +518,12 @@ __global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand 
   }
 }
 
-template <int BN, int PARTS, bool VEC, typename T, int ACT>
-cudaError_t run_vec(const LinCall& c) {
+template <int BN, int PARTS, bool ALIGNED, typename T, int ACT>
+cudaError_t run_rows(const LinCall& c) {
   const LinShape& s = c.s;
-  constexpr auto kern = k_linear_tc<BN, PARTS, VEC, T, ACT>;
+  constexpr auto kern = k_linear_tc<BN, PARTS, ALIGNED, T, ACT>;
   constexpr int TM = 2 * kBM;
-  constexpr size_t smem = smem_bytes<BN, PARTS, VEC>();
+  constexpr size_t smem = smem_bytes<BN, PARTS>();
   cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   CUtensorMap xmap, wmap;
@@ -456,9 +555,9 @@ cudaError_t run_vec(const LinCall& c) {
 template <int BN, int PARTS, typename T, int ACT>
 cudaError_t run(const LinCall& c) {
   const LinShape& s = c.s;
-  const bool vec = s.N % 32 == 0 && linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) && ((uintptr_t)c.bias & 15) == 0 &&
-                   (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
-  return vec ? run_vec<BN, PARTS, true, T, ACT>(c) : run_vec<BN, PARTS, false, T, ACT>(c);
+  const bool aligned = linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) &&
+                       (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
+  return aligned ? run_rows<BN, PARTS, true, T, ACT>(c) : run_rows<BN, PARTS, false, T, ACT>(c);
 }
 
 template <int BN, int PARTS, typename T>
