@@ -27,14 +27,6 @@ constexpr size_t few_smem() { return 1024 + (size_t)few_stages<NT, PARTS>() * fe
 // rounded to nearest; the accumulators are added up afterwards).
 constexpr int kSumBlocks = 2;
 
-__device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
-  uint32_t at;
-  float4 v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-  return v;
-}
-
 // Cluster of `split` CTAs: the same 128 rows of W, consecutive parts of the
 // contraction. Each leaves its sums [NT][128] in shared memory; each then adds up
 // 128 / split rows of all of them (in rank order) and finishes those outputs.
@@ -166,7 +158,7 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
       float4 v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (q < split) v[q] = split == 1 ? *reinterpret_cast<const float4*>(part + t * kBM + r) : ld_cluster4(part + t * kBM + r, q);
+        if (q < split) v[q] = split == 1 ? *reinterpret_cast<const float4*>(part + t * kBM + r) : ld_cluster4(cluster_addr(part + t * kBM + r, q));
       float u[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
       for (int q = 1; q < 8; ++q)

@@ -256,11 +256,10 @@ struct Staged {
 // BN: columns of a tile. PARTS: 1 (bf16) or 3 (fp32; part p of a matrix is its rows
 // p n .. (p + 1) n). ALIGNED: rows of y and residual at 16-byte boundaries. An epilogue
 // warp drains tensor-memory lanes 32 (w % 4) .. + 31, column half w / 4.
-template <int BN, int PARTS, bool ALIGNED, typename T, int ACT>
+template <int BN, int PARTS, bool ALIGNED, bool SPLIT, typename T, int ACT>
 __global__ void __launch_bounds__(kLinThreads, 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-            const T* __restrict__ bias, const T* residual, T* y,
-            int wait_limit) {
+            const T* __restrict__ bias, const T* residual, T* y, int log_split, int wait_limit) {
   constexpr int BW = BN / 2;                       // W rows in this CTA's stages
   constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
   constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
@@ -272,10 +271,15 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   __shared__ int abort_s;
   unsigned char* ring = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
   unsigned char* staging = ring + (size_t)ST * SB;
+  float* sums = reinterpret_cast<float*>(ring);    // [BN][kBM], once no stage is used any more
+  static_assert(!SPLIT || BN * kBM * 4 <= ST * SB, "the ring holds the sums");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &abort_s;
-  const int rank = (int)cluster_rank();
-  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  // a cluster is `split` pairs, which share a tile's contraction
+  const int crank = (int)cluster_rank(), rank = crank & 1, part = crank >> 1;
+  const uint16_t pair = (uint16_t)(3 << (crank & ~1));
+  if constexpr (!SPLIT) log_split = 0;
+  const int split = 1 << log_split, first = blockIdx.x >> (log_split + 1), stride = gridDim.x >> (log_split + 1);
   if (warp == 0) tmem_alloc2(&tmem_s, acc_cols<BN>());
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
@@ -288,13 +292,16 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     }
     abort_s = 0;
     bar_init_fence();
+    tma_prefetch(&xmap);
+    tma_prefetch(&wmap);
   }
   fence_before();
   cluster_sync();
   fence_after();
   pdl_wait_primary();                              // from here on inputs are read and y is written
   const uint32_t tmem = tmem_s;
-  const int nk = (s.K + KS * kBK - 1) / (KS * kBK);   // stages per tile
+  const int stages = (s.K + KS * kBK - 1) / (KS * kBK);   // of a tile; this pair's: k0 .. k1
+  const int k0 = (int)((uint32_t)(stages * part) >> log_split), k1 = (int)((uint32_t)(stages * (part + 1)) >> log_split);
   auto give_up = [&]() {
     *abort_flag = 1;
     atomicExch(&g_linear_error, 1);
@@ -314,7 +321,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       const int col0 = n * BN + half * CW;
       const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + half * CW;
       // the tile's residual on its way into L2 while the tile is multiplied: a lane per row
-      if (residual && row0 + lane < s.n) {
+      if (!SPLIT && residual && row0 + lane < s.n) {
         const char* rp = reinterpret_cast<const char*>(residual + (row0 + lane) * s.ldr + col0);
         const int bytes = min(CW, s.N - col0) * (int)sizeof(T);
         for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + o));
@@ -327,11 +334,16 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         if (residual && c < CW && rows > 0 && col0 + c + 32 <= s.N) staged.fetch(c, rows);
       };
       auto store = [&](float (&v)[32], int c) {
-        if (rows <= 0 || col0 + c >= s.N) return;
-        staged.template store<ACT>(v, c, rows, s.N - col0 - c, bias ? bias + col0 + c : nullptr, residual != nullptr,
-                                   [&] { fetch(c + 32); }, stg, lane);
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sums[(half * CW + c + e) * kBM + 32 * q + lane] = v[e];
+        } else {
+          if (rows <= 0 || col0 + c >= s.N) return;
+          staged.template store<ACT>(v, c, rows, s.N - col0 - c, bias ? bias + col0 + c : nullptr, residual != nullptr,
+                                     [&] { fetch(c + 32); }, stg, lane);
+        }
       };
-      fetch(0);
+      if constexpr (!SPLIT) fetch(0);
       if constexpr (PARTS == 1) {
         alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
         if (!alive) break;
@@ -359,7 +371,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         float acc[CW];
 #pragma unroll
         for (int e = 0; e < CW; ++e) acc[e] = 0.f;
-        for (int kb = 0; kb < nk; kb += kSumBlocks, ++unit) {
+        for (int kb = k0; kb < k1; kb += kSumBlocks, ++unit) {
           alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
@@ -394,16 +406,17 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       uint32_t kbs = 0, unit = 0;
       bool alive = true;
       for (int t = first; t < g.tiles && alive; t += stride) {
-        for (int kb = 0; kb < nk; ++kb, ++kbs) {
+        for (int kb = k0; kb < k1; ++kb, ++kbs) {
           const int st = kbs % ST;
-          if (PARTS > 1 ? kb % kSumBlocks == 0 : kb == 0)
+          const bool start = PARTS > 1 ? (kb - k0) % kSumBlocks == 0 : kb == k0;   // of an accumulator
+          if (start)
             alive = unit < 2 || warp_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
           alive = alive && warp_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
           const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + UNITS * XB;
           const uint32_t d = tmem + (unit & 1) * BN;
-          const bool last = kb == nk - 1 || (PARTS > 1 && kb % kSumBlocks == kSumBlocks - 1);
+          const bool last = kb == k1 - 1 || (PARTS > 1 && (kb - k0) % kSumBlocks == kSumBlocks - 1);
           if (issuer) {
             if constexpr (PARTS == 1) {
               const int steps = min(KS * kBK / 16, (s.K - kb * KS * kBK + 15) / 16);   // of 16
@@ -411,7 +424,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
               for (int k = 0; k < KS * kBK / 16; ++k) {
                 if (k >= steps) break;
                 const uint32_t xo = (k / 4) * XB + (k % 4) * 32, wo = (k / 4) * WB + (k % 4) * 32;
-                mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, kb > 0 || k > 0);
+                mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, !start || k > 0);
               }
             } else {
               constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
@@ -419,11 +432,10 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
               for (int p = 0; p < 6; ++p)
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id,
-                       kb % kSumBlocks > 0 || p > 0 || k > 0);
+                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, !start || p > 0 || k > 0);
             }
-            commit2(&empty_bar[st]);
-            if (last) commit2(&acc_full[unit & 1]);
+            commit2(&empty_bar[st], pair);
+            if (last) commit2(&acc_full[unit & 1], pair);
           }
           __syncwarp();
           if (last) ++unit;
@@ -442,7 +454,7 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     for (int t = first; t < g.tiles && alive; t += stride) {
       int m, n;
       tile_at(g, t, m, n);
-      for (int kb = 0; kb < nk; ++kb, ++kbs) {
+      for (int kb = k0; kb < k1; ++kb, ++kbs) {
         const int st = kbs % ST, k = kb * KS * kBK;
         alive = kbs < ST || warp_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag);
         if (!alive) break;
@@ -465,8 +477,42 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     // no copy of this CTA may still be in flight when it ends: each stage's last use is done
     for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDrainLimit);
   }
+  if constexpr (SPLIT) {
+    // every pair left its sums in shared memory, where no stage is used any more; each
+    // finishes BN / split columns, in the order of the pairs
+    const int q = warp & 3, half = warp >> 2, width = BN >> log_split, c0 = part * width + 32 * half;
+    int m, n;
+    tile_at(g, first, m, n);
+    const int64_t row0 = (int64_t)m * TM + rank * kBM + 32 * q;
+    const int col0 = n * BN + c0, rows = (int)min((int64_t)32, s.n - row0);
+    const bool work = warp < kEpiWarps && 32 * half < width && rows > 0 && col0 < s.N;
+    Staged<T, ALIGNED> staged;
+    if (work) {
+      staged.y.init(y + row0 * s.ldy + col0, s.ldy, lane);
+      if (residual) staged.res.init(const_cast<T*>(residual) + row0 * s.ldr + col0, s.ldr, lane);
+      if (residual && col0 + 32 <= s.N) staged.fetch(0, rows);
+    }
+    fence_before();
+    cluster_sync();
+    fence_after();
+    if (work) {
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0.f;
+      for (int i = 0; i < split; ++i) {
+        const uint32_t from = cluster_addr(sums + c0 * kBM + 32 * q + lane, 2 * i + rank);
+        float u[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) u[e] = ld_cluster(from + e * (kBM * 4));
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += u[e];
+      }
+      staged.template store<ACT>(v, 0, rows, s.N - col0, bias ? bias + col0 : nullptr, residual != nullptr, [] {},
+                                 staging + warp * staging_bytes<PARTS>(), lane);
+    }
+  }
   fence_before();
-  cluster_sync_relaxed();                          // neither CTA ends while the other may still signal it
+  cluster_sync_relaxed();                          // no CTA ends while another may still signal it or read its sums
   fence_after();
   if (warp == 0) tmem_free2(tmem, acc_cols<BN>());
 }
@@ -518,11 +564,30 @@ __global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand 
   }
 }
 
-template <int BN, int PARTS, bool ALIGNED, typename T, int ACT>
-cudaError_t run_rows(const LinCall& c) {
+// Pairs that share a tile's contraction, log2, where tiles leave most SMs idle: worth
+// its 1 us of exchange from a contraction of about 1500 in bf16 and 256 in fp32 (300 x
+// 512 -> 512 bf16: 6.3 us, split by two 7.2; 600 x 4096 -> 256: 16.6, by four 10.5, fp32
+// 69.7 and 27.0). Clusters of 8 CTAs do not fill every group of SMs: 16 tiles by four
+// need two rounds (160 x 2048 -> 2048 fp32: 36.6 us, by two 27.3).
+int linear_log_split(const LinShape& s, int tiles, int num_sms) {
+  const int stages = (s.K + kBK - 1) / kBK / (s.bf16 ? kStageBlocks<1> : kStageBlocks<3>);
+  if (8 * tiles <= num_sms * 3 / 4 && stages >= (s.bf16 ? 16 : 8)) return 2;
+  return 4 * tiles <= num_sms * 9 / 10 && stages >= (s.bf16 ? 12 : 4);
+}
+
+LinTiles tiles_of(const LinShape& s, int bn) {
+  LinTiles g{};
+  g.mt = (int)(((int64_t)s.n + 2 * kBM - 1) / (2 * kBM));
+  g.nt = (s.N + bn - 1) / bn;
+  g.group = g.mt < 8 ? g.mt : 8;
+  g.tiles = g.mt * g.nt;
+  return g;
+}
+
+template <int BN, int PARTS, bool ALIGNED, bool SPLIT, typename T, int ACT>
+cudaError_t run_rows(const LinCall& c, int log_split) {
   const LinShape& s = c.s;
-  constexpr auto kern = k_linear_tc<BN, PARTS, ALIGNED, T, ACT>;
-  constexpr int TM = 2 * kBM;
+  constexpr auto kern = k_linear_tc<BN, PARTS, ALIGNED, SPLIT, T, ACT>;
   constexpr size_t smem = smem_bytes<BN, PARTS>();
   cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
@@ -530,17 +595,13 @@ cudaError_t run_rows(const LinCall& c) {
   if (!linear_map(&xmap, c.x, (int64_t)PARTS * s.n, s.K, s.ldx, kBM) ||
       !linear_map(&wmap, c.w, (int64_t)PARTS * s.N, s.K, s.ldw, BN / 2))
     return cudaErrorInvalidValue;
-  LinTiles g{};
-  g.mt = (int)(((int64_t)s.n + TM - 1) / TM);
-  g.nt = (s.N + BN - 1) / BN;
-  g.group = g.mt < 8 ? g.mt : 8;
-  g.tiles = g.mt * g.nt;
-  const int pairs = g.tiles < c.num_sms / 2 ? g.tiles : c.num_sms / 2;
+  const LinTiles g = tiles_of(s, BN);
+  const int split = 1 << log_split, pairs = SPLIT ? g.tiles * split : g.tiles < c.num_sms / 2 ? g.tiles : c.num_sms / 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
@@ -549,15 +610,22 @@ cudaError_t run_rows(const LinCall& c) {
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, (int)kDefaultWaitLimit);
+  return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, log_split,
+                            (int)kDefaultWaitLimit);
 }
 
 template <int BN, int PARTS, typename T, int ACT>
 cudaError_t run(const LinCall& c) {
   const LinShape& s = c.s;
+  if constexpr (BN == 128) {
+    // a warp stores 32 columns once: no kernels of their own for aligned rows
+    if (const int log_split = linear_log_split(s, tiles_of(s, BN).tiles, c.num_sms))
+      return run_rows<BN, PARTS, false, true, T, ACT>(c, log_split);
+  }
   const bool aligned = linear_aligned16(c.y, s.ldy, s.n, sizeof(T)) &&
                        (!c.residual || linear_aligned16(c.residual, s.ldr, s.n, sizeof(T)));
-  return aligned ? run_rows<BN, PARTS, true, T, ACT>(c) : run_rows<BN, PARTS, false, T, ACT>(c);
+  return aligned ? run_rows<BN, PARTS, true, false, T, ACT>(c, 0)
+                 : run_rows<BN, PARTS, false, false, T, ACT>(c, 0);
 }
 
 template <int BN, int PARTS, typename T>

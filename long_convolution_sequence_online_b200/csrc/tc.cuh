@@ -117,6 +117,22 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Another CTA's copy of a place in shared memory.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
 constexpr uint32_t kLeaderMask = 0xFEFFFFFFu;
 __device__ __forceinline__ void tmem_alloc2(uint32_t* out, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(out)), "r"(cols) : "memory");
@@ -131,11 +147,11 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
 }
-// Arrives on the barrier of both CTAs once the MMAs issued so far are done.
-__device__ __forceinline__ void commit2(uint64_t* bar) {
+// Arrives on the barrier of both CTAs (`pair`: a bit for each) once the MMAs issued so far are done.
+__device__ __forceinline__ void commit2(uint64_t* bar, uint16_t pair) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(saddr(bar)), "h"((uint16_t)3) : "memory");
+      ::"r"(saddr(bar)), "h"(pair) : "memory");
 }
 // Into this CTA's shared memory, counted on the leader's barrier.
 __device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {

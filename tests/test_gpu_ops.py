@@ -706,3 +706,57 @@ def test_a_layer_of_a_hybrid_stack(fi, dtype):
     _check_linear(flat(a), flat(o), wo, None, flat(x), "none", dtype)
     _check_linear(flat(hid), flat(a), w1, b1, None, "gelu", dtype)
     _check_linear(flat(y), flat(hid), w2, b2, flat(a), "none", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nin,nout", [(200, 2048, 128), (300, 2048, 769), (513, 1537, 200), (257, 4100, 33), (129, 256, 2100),
+                                        (1000, 1600, 384)])
+@pytest.mark.parametrize("act,bias,residual", [("none", False, False), ("tanh", True, True)])
+def test_linear_shared_contraction(fi, n, nin, nout, act, bias, residual, dtype):
+    # few tiles and a long contraction: several pairs of CTAs work on a tile
+    g = torch.Generator(device="cuda").manual_seed(n + nin)
+    dt = DT[dtype]
+    x, w = _rand(g, n, nin, dtype=dt), _rand(g, nout, nin, dtype=dt, scale=nin ** -0.5)
+    b = _rand(g, nout, dtype=dt) if bias else None
+    r = _rand(g, n, nout, dtype=dt) if residual else None
+    y = torch.full((n + 1, nout), float("nan"), dtype=dt, device="cuda")
+    fi.linear(x, w, y[:n], bias=b, residual=r, act=act)
+    again = torch.empty(n, nout, dtype=dt, device="cuda")
+    fi.linear(x, w, again, bias=b, residual=r, act=act)
+    fi.op_sync()
+    _check_linear(y[:n], x, w, b, r, act, dtype)
+    assert torch.equal(again, y[:n])
+    assert y[n].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nin,nout", [(300, 512, 300), (300, 2048, 300), (2000, 96, 225)])
+@pytest.mark.parametrize("sy,sr,dy,dr", [(0, 0, 8, 8), (1, 0, 3, 0), (0, 3, 0, 1), (5, 2, 2, 7), (7, 7, 1, 1), (6, 1, 8, 5)])
+def test_linear_rows_at_any_alignment(fi, n, nin, nout, sy, sr, dy, dr, dtype):
+    # y and the residual start sy, sr elements past a 16-byte boundary, their rows are
+    # dy, dr elements longer than a row; what lies between the rows stays as it was
+    g = torch.Generator(device="cuda").manual_seed(100 * sy + sr)
+    dt = DT[dtype]
+    x, w = _rand(g, n, nin, dtype=dt), _rand(g, nout, nin, dtype=dt, scale=nin ** -0.5)
+    b = _rand(g, nout, dtype=dt)
+
+    def view(shift, more):
+        base = torch.full((n * (nout + more) + 16,), 7.0, dtype=dt, device="cuda")
+        return base, base[shift:shift + n * (nout + more)].view(n, nout + more)[:, :nout]
+
+    ybase, y = view(sy, dy)
+    rbase, r = view(sr, dr)
+    r.copy_(_rand(g, n, nout, dtype=dt))
+    fi.linear(x, w, y, bias=b, residual=r, act="silu")
+    fi.op_sync()
+    _check_linear(y, x, w, b, r, "silu", dtype)
+    y.fill_(7.0)
+    assert (ybase == 7.0).all()
+    # in place
+    want = torch.empty(n, nout, dtype=dt, device="cuda")
+    fi.linear(x, w, want, bias=b, residual=r, act="silu")
+    fi.linear(x, w, r, bias=b, residual=r, act="silu")
+    fi.op_sync()
+    assert torch.equal(r, want)
+    r.fill_(7.0)
+    assert (rbase == 7.0).all()
