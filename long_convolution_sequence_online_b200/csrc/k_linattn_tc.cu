@@ -48,13 +48,13 @@ constexpr int kLaTcThreads = 32 * (kTmaWarp + 1);
 
 __device__ int g_linattn_error;          // a bounded wait gave up since the last check
 
-// DK, DV: key and value dimensions padded to 64 or 128. V is always double
+// DK, DV: key and value dimensions padded to 64 or 128. V is double
 // buffered (the next chunk's w V starts first), K and Q where there is room.
 // The launch that forms states only has room for two halves of w V.
 // PARTS: bf16 parts of an input, 1 or 3 (fp32).
 template <int DK, int DV, bool OUT, int PARTS>
 struct LaSmem {
-  static constexpr int kSlotsKQ = PARTS == 3 || (DK == 128 && DV == 128) ? 1 : 2, kSlotsV = PARTS == 3 ? 1 : 2;
+  static constexpr int kSlotsKQ = PARTS == 3 || (DK == 128 && DV == 128) ? 1 : 2, kSlotsV = PARTS == 3 && OUT ? 1 : 2;
   static constexpr int kHalves = OUT ? 1 : 2;
   static constexpr int kPlaneK = kCh * 2 * DK, kPlaneV = kCh * 2 * DV;   // a part of a tile
   static constexpr int kTileK = PARTS * kPlaneK, kTileV = PARTS * kPlaneV;
@@ -728,7 +728,8 @@ bool map_heads(CUtensorMap* map, const void* x, const int64_t (&st)[3], const La
 }
 
 // Inputs that no tensor map describes, and fp32 ones, as bf16 parts [part][n][B][H][d
-// rounded up to 8]: 8 elements per thread.
+// rounded up to 8]: 8 elements per thread. I: what counts them (64-bit divisions cost
+// more than the memory accesses).
 struct LaOperand {
   const void* src;
   __nv_bfloat16* dst;
@@ -739,20 +740,20 @@ struct LaOperands {
   LaOperand x[3];
   int64_t end[3];        // units of 8 elements up to and with each
 };
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(256) k_linattn_layout(LaOperands ops, int B, int H, int64_t rows) {
   pdl_launch_dependents();                 // the attention itself, which waits for this launch's end
   pdl_wait_primary();
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < ops.end[2]; u += (int64_t)gridDim.x * 256) {
     const int i = u < ops.end[0] ? 0 : u < ops.end[1] ? 1 : 2;
     const LaOperand& o = ops.x[i];
-    const int64_t v = i ? u - ops.end[i - 1] : u;
-    const int per = (o.d + 7) / 8;
-    const int64_t r = v / per;             // (position, sequence, head)
-    const int k = (int)(v - r * per) * 8, h = (int)(r % H), b = (int)(r / H % B);
-    const int64_t t = r / H / B;
-    const T* p = (const T*)o.src + t * o.st[0] + b * o.st[1] + h * o.st[2] + k;
-    __nv_bfloat16* d = o.dst + r * (8 * per) + k;
+    const I v = (I)(i ? u - ops.end[i - 1] : u), per = (I)((o.d + 7) / 8);
+    const I r = v / per;                   // (position, sequence, head)
+    const I tb = r / (I)H, t = tb / (I)B;
+    const int64_t h = r - tb * (I)H, b = tb - t * (I)B;
+    const int k = (int)(v - r * per) * 8;
+    const T* p = (const T*)o.src + (int64_t)t * o.st[0] + b * o.st[1] + h * o.st[2] + k;
+    __nv_bfloat16* d = o.dst + (int64_t)r * (8 * (int)per) + k;
     if constexpr (sizeof(T) == 2) {
       uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(256) k_linattn_layout(LaOperands ops, int B, i
       for (int e = 0; e < 4; ++e) split3(f[2 * e], f[2 * e + 1], q[0][e], q[1][e], q[2][e]);
 #pragma unroll
       for (int x = 0; x < 3; ++x)
-        *reinterpret_cast<uint4*>(d + x * rows * (8 * per)) = make_uint4(q[x][0], q[x][1], q[x][2], q[x][3]);
+        *reinterpret_cast<uint4*>(d + x * rows * (8 * (int)per)) = make_uint4(q[x][0], q[x][1], q[x][2], q[x][3]);
     }
   }
 }
@@ -902,8 +903,12 @@ cudaError_t launch_linattn_tc(const LaShape& shape, const LaPlan& p, const LaPtr
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = s.bf16 ? cudaLaunchKernelEx(&cfg, k_linattn_layout<__nv_bfloat16>, ops, s.B, s.H, rows)
-                                 : cudaLaunchKernelEx(&cfg, k_linattn_layout<float>, ops, s.B, s.H, rows);
+    const bool narrow = units <= UINT32_MAX;
+    const cudaError_t e =
+        s.bf16 ? cudaLaunchKernelEx(&cfg, narrow ? k_linattn_layout<__nv_bfloat16, uint32_t> : k_linattn_layout<__nv_bfloat16, uint64_t>,
+                                    ops, s.B, s.H, rows)
+               : cudaLaunchKernelEx(&cfg, narrow ? k_linattn_layout<float, uint32_t> : k_linattn_layout<float, uint64_t>, ops, s.B,
+                                    s.H, rows);
     if (e != cudaSuccess) return e;
   }
   if (!s.bf16) return run<64, 64, 3>(s, p, a, num_sms, st);

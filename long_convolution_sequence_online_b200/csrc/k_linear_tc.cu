@@ -519,23 +519,24 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
 
 // An operand that TMA cannot take (fp32, or rows at no 16-byte boundary) as
 // `parts` bf16 matrices of rows of Kp = K rounded up to 8 elements, the rest zero:
-// 8 elements per thread, read once, written once.
+// 8 elements per thread, read once, written once. I: what counts them.
 struct LinOperand {
   const void* src;
   __nv_bfloat16* dst;
   int64_t rows, ld;
   int vec;               // rows start at 16-byte boundaries
 };
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(256) k_linear_layout(LinOperand a, LinOperand b, int K, int Kp, int64_t units_a, int64_t units) {
   pdl_launch_dependents();                 // the product, which waits for this launch's end
   pdl_wait_primary();
-  const int per = Kp / 8;
+  const I per = (I)(Kp / 8);
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
     const bool first = u < units_a;
     const LinOperand& o = first ? a : b;
-    const int64_t v = first ? u : u - units_a, row = v / per;
-    const int k = (int)(v - row * per) * 8;
+    const I v = (I)(first ? u : u - units_a), r = v / per;
+    const int k = (int)(v - r * per) * 8;
+    const int64_t row = (int64_t)r;
     const T* p = (const T*)o.src + row * o.ld + k;
     __nv_bfloat16* d = o.dst + row * Kp + k;
     if constexpr (sizeof(T) == 2) {
@@ -721,8 +722,12 @@ cudaError_t launch_linear(const LinShape& shape, const void* x, const void* w, c
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = s.bf16 ? cudaLaunchKernelEx(&cfg, k_linear_layout<__nv_bfloat16>, a, b, s.K, Kp, ua, units)
-                                 : cudaLaunchKernelEx(&cfg, k_linear_layout<float>, a, b, s.K, Kp, ua, units);
+    const bool narrow = units <= UINT32_MAX;
+    const cudaError_t e =
+        s.bf16 ? cudaLaunchKernelEx(&cfg, narrow ? k_linear_layout<__nv_bfloat16, uint32_t> : k_linear_layout<__nv_bfloat16, uint64_t>,
+                                    a, b, s.K, Kp, ua, units)
+               : cudaLaunchKernelEx(&cfg, narrow ? k_linear_layout<float, uint32_t> : k_linear_layout<float, uint64_t>, a, b, s.K, Kp,
+                                    ua, units);
     if (e != cudaSuccess) return e;
   }
   if (linear_few_fits(s, num_sms)) return launch_linear_few(c);
