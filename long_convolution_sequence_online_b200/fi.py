@@ -292,12 +292,13 @@ def _op_stream(stream, dev):
 
 
 def _scratch(need, like, stream, st):
-    """Scratch of one call: the allocator hands its memory out again once the call's stream has passed it."""
+    """Scratch of one call, from the memory of the call's stream: whatever used it before, and whatever
+    is given it next, runs on that stream as well."""
     import torch
-    ws = torch.empty(need, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(st, device=like.device) if st else torch.cuda.default_stream(like.device))
-    return ws
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(st, device=like.device) if st else torch.cuda.default_stream(like.device)):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
 def _check_tensors(tensors, dtype):

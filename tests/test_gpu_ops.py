@@ -760,3 +760,33 @@ def test_linear_rows_at_any_alignment(fi, n, nin, nout, sy, sr, dy, dr, dtype):
     assert torch.equal(r, want)
     r.fill_(7.0)
     assert (rbase == 7.0).all()
+
+
+@pytest.mark.parametrize("op", ["linear", "prefill"])
+def test_scratch_of_a_call_on_another_stream(fi, op):
+    # memory that work still waiting on the current stream uses is not scratch of a call
+    # that goes ahead on another one
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w, y = _rand(g, 1024, 512), _rand(g, 512, 512), torch.empty(1024, 512, device="cuda")
+    q, k, v = (_rand(g, 512, 4, 4, 64) for _ in range(3))
+    o, ld = torch.empty_like(v), torch.full((4,), -0.1, device="cuda")
+    other = torch.cuda.Stream()
+
+    def call(stream):
+        if op == "linear":
+            fi.linear(x, w, y, stream=stream)
+        else:
+            fi.linattn_prefill(q, k, v, ld, o, stream=stream)
+
+    call(other.cuda_stream)                 # the kernels are loaded
+    torch.cuda.synchronize()
+    sizes = [need for _, need, _ in fi._configs.values() if need > 0]
+    torch.cuda.empty_cache()
+    held = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)           # some 10 ms
+    kept = [h.clone() for h in held]
+    del held
+    call(other.cuda_stream)
+    torch.cuda.synchronize()
+    assert all((h == 7).all() for h in kept)
