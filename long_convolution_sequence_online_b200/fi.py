@@ -283,6 +283,12 @@ def _keep(key, cfg, need=0):
     return got
 
 
+def _check_sizes(*shapes):
+    """The C structures hold sizes in 32 bits; larger ones would pass as their remainder."""
+    if any(n > 2 ** 31 - 1 for shape in shapes for n in shape):
+        raise ValueError("a dimension is larger than 2^31 - 1")
+
+
 def _op_stream(stream, dev):
     """The stream of a call whose tensors are on CUDA device `dev`, which must be the current one."""
     import torch
@@ -322,6 +328,7 @@ def _linattn_config(key, q, k, v, log_decay, o, states, lengths, scale, n):
     lead, want = ("", 3) if n is None else ("[n]", 4)
     if q.dim() != want or k.shape != q.shape or o.shape != v.shape or v.dim() != want or v.shape[:-1] != q.shape[:-1]:
         raise ValueError(f"expected q, k {lead}[B][H][key_dim] and v, o {lead}[B][H][value_dim]")
+    _check_sizes(q.shape, v.shape)
     if not (k.dtype == v.dtype == o.dtype == q.dtype):
         raise ValueError("q, k, v and o must have one dtype")
     if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (q, k, v, o)):
@@ -356,7 +363,7 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
     key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
            o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), _look(log_decay), _look(state_in),
            _look(state_out), _look(lengths), scale, pq & 15, pk & 15, pv & 15)
-    at, need, _ = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state_in, state_out), lengths, scale,
+    at, need, _cfg = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state_in, state_out), lengths, scale,
                                                        int(q.shape[0]))
     st = _op_stream(stream, key[12])
     ws = _scratch(need, q, stream, st) if need else None
@@ -376,7 +383,7 @@ def linattn_step(q, k, v, log_decay, state, o, scale: float = 1.0, stream=None):
            o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), state.shape, state.stride(),
            state.dtype, state.get_device(), log_decay.shape, log_decay.stride(), log_decay.dtype, log_decay.get_device(),
            scale)
-    at = (_configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state,), None, scale, None))[0]
+    at, _, _cfg = _configs.get(key) or _linattn_config(key, q, k, v, log_decay, o, (state,), None, scale, None)   # held by _cfg
     s = lib.fi_linattn_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
                             o.data_ptr(), _op_stream(stream, key[12]))
     if s:
@@ -387,6 +394,7 @@ def _linear_config(key, x, w, y, bias, residual, act):
     code = _check_tensors((x, w, y, bias, residual), x.dtype)
     if x.dim() != 2 or w.dim() != 2 or y.dim() != 2 or x.shape[1] != w.shape[1] or tuple(y.shape) != (x.shape[0], w.shape[0]):
         raise ValueError("expected x [n][in], w [out][in] and y [n][out]")
+    _check_sizes(x.shape, w.shape)
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
     if any(t is not None and t.dtype != x.dtype for t in (w, y, bias, residual)):
@@ -417,7 +425,7 @@ def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
     px, pw = x.data_ptr(), w.data_ptr()
     key = (x.shape, w.shape, y.shape, x.stride(), w.stride(), y.stride(), x.dtype, w.dtype, y.dtype, x.get_device(),
            w.get_device(), y.get_device(), _look(bias), _look(residual), act, px & 15, pw & 15)
-    at, need, _ = _configs.get(key) or _linear_config(key, x, w, y, bias, residual, act)
+    at, need, _cfg = _configs.get(key) or _linear_config(key, x, w, y, bias, residual, act)
     st = _op_stream(stream, key[9])
     ws = _scratch(need, x, stream, st) if need else None
     s = lib.fi_linear(at, x.shape[0], px, pw, None if bias is None else bias.data_ptr(),

@@ -790,3 +790,23 @@ def test_scratch_of_a_call_on_another_stream(fi, op):
     call(other.cuda_stream)
     torch.cuda.synchronize()
     assert all((h == 7).all() for h in kept)
+
+
+def test_sizes_beyond_32_bits_are_refused(fi):
+    # shapes of which only one element exists: 2^32 + 5 would pass as 5
+    big = 2 ** 32 + 5
+    one = torch.zeros(1, 1, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        fi.linear(one.expand(big, 1), one.expand(1, 1), one.expand(big, 1))
+    with pytest.raises(ValueError, match="2\\^31"):
+        fi.linear(one.expand(1, big), one.expand(1, big), one)
+    with pytest.raises(ValueError, match="2\\^31"):
+        fi.linear(one, one.expand(big, 1), one.expand(1, big))
+    x = torch.zeros(1, 1, 1, 1, device="cuda")
+    ld, S = torch.zeros(1, device="cuda"), torch.zeros(1, 1, 1, 1, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        t = x.expand(big, 1, 1, 1)
+        fi.linattn_prefill(t, t, t, ld, t)
+    with pytest.raises(ValueError, match="2\\^31"):
+        t = x[0].expand(big, 1, 1)
+        fi.linattn_step(t, t, t, ld, S, t)
