@@ -8,9 +8,9 @@
 // Every power of g has an exponent >= 0, so nothing overflows whatever the decay.
 //
 // The chunked form here takes the shapes whose tiles do not fit the tensor cores' kernel
-// (k_linattn_tc.cu: above 128 dimensions, fp32 above 64). Bound by shared-memory reads of its
-// 4 x 4 outer products with one CTA per SM: 4 x 2048 positions, 8 heads of 256, fp32 1.66 ms,
-// 16 of 128 0.97 ms (11 to 12 TFLOP/s).
+// (k_linattn_tc.cu): bf16 above 128 dimensions, more than 2^29 fp32 positions. Bound by
+// shared-memory reads of its 4 x 4 outer products with one CTA per SM: 4 x 2048 positions, 8
+// heads of 256, bf16 1.61 ms (12 TFLOP/s).
 #include "op_internal.cuh"
 
 namespace fi {
@@ -350,15 +350,17 @@ static LaPlan la_plan(const LaShape& s, int num_sms) {
 size_t linattn_prefill_workspace(const LaShape& s, const LaPtrs& a, int num_sms) {
   if (s.n == 0) return 0;
   if (!linattn_tc_fits(s)) return la_workspace_bytes(s, la_plan(s, num_sms));
-  return la_workspace_bytes(s, linattn_tc_plan(s, num_sms)) + linattn_tc_layout_bytes(s, a);
+  const LaShape b = linattn_tc_block(s);
+  return la_workspace_bytes(b, linattn_tc_plan(b, num_sms)) + linattn_tc_layout_bytes(s, a);
 }
 
 cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& ptrs, void* workspace, int num_sms, cudaStream_t st) {
   LaPtrs a = ptrs;
   a.ws = (float*)workspace;
   if (linattn_tc_fits(s)) {
-    const LaPlan p = linattn_tc_plan(s, num_sms);
-    return launch_linattn_tc(s, p, a, (unsigned char*)workspace + la_workspace_bytes(s, p), num_sms, st);
+    const LaShape b = linattn_tc_block(s);
+    const LaPlan p = linattn_tc_plan(b, num_sms);
+    return launch_linattn_tc(s, p, a, (unsigned char*)workspace + la_workspace_bytes(b, p), num_sms, st);
   }
   const LaPlan p = la_plan(s, num_sms);
   return s.bf16 ? prefill_dk<__nv_bfloat16>(s, p, a, st) : prefill_dk<float>(s, p, a, st);

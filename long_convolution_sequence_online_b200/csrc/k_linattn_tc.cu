@@ -35,6 +35,12 @@
 // sequence of 16K 112 us (states 40, outputs 72; 2.4 TB/s), 32 of 2K 288 us (3.9 TB/s, 1000 W).
 // fp32, 12 heads of 64, 8K: 106 us (layout 27, states 26, outputs 55), waiting on
 // products and single-buffered tiles.
+//
+// fp32 inputs come as three bf16 parts each and every product as six products of parts;
+// their tiles fit up to 64 dimensions. Above, blocks of 64 value dimensions are tasks of
+// their own, and blocks of key dimensions launches of their own, of which the later
+// ones add to the outputs (q . k is the sum over them). Scores are formed once per
+// block: 4 x 2048 positions, 16 heads of 128, 0.49 ms; in fp32 arithmetic (k_linattn.cu) 0.97.
 #include <type_traits>
 
 #include "op_internal.cuh"
@@ -91,17 +97,22 @@ struct LaCols {
 // (0,2) (0,1) (0,0).
 constexpr uint32_t kPairA = 0x052, kPairB = 0x118, kSingleB = 0x006;
 
-// What a CTA does for one (sequence, head) and segment.
+// What a CTA does for one (sequence, head), segment and, fp32, block of 64 value
+// dimensions (v0 ..); `slot` counts the former without the segments.
 struct LaTask {
-  int bh, b, h, seg, len, end, nch;
+  int slot, bh, b, h, v0, dv, seg, len, end, nch;
   int64_t t0;
   bool ragged;    // the last chunk ends inside a longer batch: what stands behind is cleared in the tiles
 };
 template <bool OUT, int PARTS>
 __device__ __forceinline__ LaTask la_task(const LaShape& s, const LaPlan& p, const LaPtrs& a, int i) {
   LaTask t;
-  t.bh = i % (s.B * s.H);                // segments of a head far apart: the early ones end first
-  t.seg = i / (s.B * s.H);
+  const int blocks = PARTS == 3 ? (s.dv + 63) / 64 : 1, slots = s.B * s.H * blocks;
+  t.slot = i % slots;                    // segments of a head far apart: the early ones end first
+  t.bh = PARTS == 3 ? t.slot / blocks : t.slot;
+  t.v0 = PARTS == 3 ? (t.slot - t.bh * blocks) * 64 : 0;
+  t.dv = PARTS == 3 ? min(64, s.dv - t.v0) : s.dv;
+  t.seg = i / slots;
   t.b = t.bh / s.H;
   t.h = t.bh - t.b * s.H;
   t.len = la_length(a.lengths, t.b, s.n);
@@ -115,7 +126,8 @@ __device__ __forceinline__ LaTask la_task(const LaShape& s, const LaPlan& p, con
   return t;
 }
 
-template <int DK, int DV, bool OUT, int PARTS>
+// ADD: outputs are added to o (a further block of key dimensions).
+template <int DK, int DV, bool OUT, int PARTS, bool ADD>
 __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -141,8 +153,9 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   unsigned char* wv = sop + L::kState;
   if constexpr (!OUT) pdl_launch_dependents();   // the launch of the outputs, which waits for this one's end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tasks = s.B * s.H * p.G;
-  const size_t slot = (size_t)s.dk * s.dv;
+  const int tasks = s.B * s.H * (PARTS == 3 ? (s.dv + 63) / 64 : 1) * p.G;
+  const int ws_ld = PARTS == 3 ? min(64, s.dv) : s.dv;     // the scratch's states: dk x ws_ld
+  const size_t slot = (size_t)s.dk * ws_ld;
   if (warp == 0) tmem_alloc(&tmem_s, 512);
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
@@ -266,7 +279,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       const float f_inter = s.scale * G[row + 1];   // P carries the scale
       const bool tile = STAGED && vec_out && !(k.ragged && c == k.nch - 1);
       unsigned char* dst = vs + (j % NV) * L::kTileV + row * 128;
-      T* op = (T*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + col0;
+      T* op = (T*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + k.v0 + col0;
 #pragma unroll
       for (int d = 0; d < CW; d += 16) {
         uint32_t r[16], q[16];
@@ -285,12 +298,17 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           for (int e = 0; e < 16; ++e) w[e] = fmaf(f_inter, __uint_as_float(r[e]), __uint_as_float(q[e]));
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            if (vec_out && col0 + d + e + 4 <= s.dv) {
-              *reinterpret_cast<float4*>(op + d + e) = make_float4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            if (vec_out && col0 + d + e + 4 <= k.dv) {
+              float4 v = make_float4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+              if constexpr (ADD) {
+                const float4 u = *reinterpret_cast<const float4*>(op + d + e);
+                v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+              }
+              *reinterpret_cast<float4*>(op + d + e) = v;
             } else {
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                if (col0 + d + e + x < s.dv) op_store(op + d + e + x, w[e + x]);
+                if (col0 + d + e + x < k.dv) op_store(op + d + e + x, ADD ? op_load(op + d + e + x) + w[e + x] : w[e + x]);
             }
           }
           continue;
@@ -307,12 +325,12 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           if (tile) {
             *reinterpret_cast<uint4*>(dst + (col >> 6) * (kCh * 128) + ((((col & 63) >> 3) ^ (row & 7)) << 4)) = v;
           } else if (t < k.end) {
-            if (vec_out && col + 8 <= s.dv) {
+            if (vec_out && col + 8 <= k.dv) {
               *reinterpret_cast<uint4*>(op + d + 8 * u) = v;
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (col + e < s.dv)
+                if (col + e < k.dv)
                   reinterpret_cast<unsigned short*>(op)[d + 8 * u + e] = (unsigned short)(w[4 * u + e / 2] >> (16 * (e & 1)));
             }
           }
@@ -326,10 +344,11 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     };
     for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
       const LaTask k = la_task<OUT, PARTS>(s, p, a, i);
-      float* ws = a.ws ? a.ws + (size_t)k.bh * p.G * slot : nullptr;
-      const float* s_in = a.state_in ? a.state_in + (size_t)k.bh * slot : nullptr;
+      float* ws = a.ws ? a.ws + (size_t)k.slot * p.G * slot : nullptr;
+      const float* s_in = a.state_in ? a.state_in + k.bh * s.state_slot + k.v0 : nullptr;
       if (!OUT && k.seg == 0 && s_in)
-        for (size_t e = tid; e < slot; e += 32 * kWorkers) ws[e] = s_in[e];
+        for (int r = warp; r < s.dk; r += kWorkers)
+          for (int c = lane; c < k.dv; c += 32) ws[r * ws_ld + c] = s_in[(size_t)r * s.state_ld + c];
       if (k.nch == 0 && !(OUT && k.seg == 0 && k.len == 0)) continue;
       const float ld2 = la_log2_decay(__ldg(a.log_decay + k.h));
       sync();                                      // the task before is done with the tables and the stage
@@ -339,6 +358,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
       for (int e = 0; e < CW; ++e) st[e] = 0.f;
       const float* src = !OUT ? nullptr : p.G > 1 ? ws : s_in;
+      const int src_ld = p.G > 1 ? ws_ld : s.state_ld;
       const int g0 = s_in ? 0 : 1;
       constexpr int PER = DV / 8;                  // float4s of half a row of the state
       if (src && g0 <= k.seg) {
@@ -350,10 +370,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
             for (int u = 0; u < 128 * PER / (32 * kWorkers); ++u) {
               const int e = tid + u * (32 * kWorkers), r = e / PER, c = hc * (DV / 2) + 4 * (e % PER);
               float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (r < s.dk && c < s.dv)
+              if (r < s.dk && c < k.dv)
                 for (int g = g0; g <= k.seg; ++g) {
                   const float f = la_pow(ld2, (g == 0 ? k.seg : k.seg - g) * p.seg);
-                  const float4 v = *reinterpret_cast<const float4*>(src + (size_t)g * slot + (size_t)r * s.dv + c);
+                  const float4 v = *reinterpret_cast<const float4*>(src + (size_t)g * slot + (size_t)r * src_ld + c);
                   x.x = fmaf(f, v.x, x.x);
                   x.y = fmaf(f, v.y, x.y);
                   x.z = fmaf(f, v.z, x.z);
@@ -374,10 +394,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         } else if (row < s.dk) {
           for (int g = g0; g <= k.seg; ++g) {
             const float f = la_pow(ld2, (g == 0 ? k.seg : k.seg - g) * p.seg);
-            const float* sp = src + (size_t)g * slot + (size_t)row * s.dv + col0;
+            const float* sp = src + (size_t)g * slot + (size_t)row * src_ld + col0;
 #pragma unroll
             for (int e = 0; e < CW; ++e)
-              if (col0 + e < s.dv) st[e] = fmaf(f, sp[e], st[e]);
+              if (col0 + e < k.dv) st[e] = fmaf(f, sp[e], st[e]);
           }
         }
       }
@@ -483,8 +503,9 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       if (OUT && k.nch > 0) outputs(k, k.nch - 1, it - 1);
       if (!OUT) update(k.nch - 1, it - 1);
       float* dst = nullptr;
+      const int dst_ld = OUT ? s.state_ld : ws_ld;
       if constexpr (!OUT) dst = ws + (size_t)(k.seg + 1) * slot;
-      else if (a.state_out && k.end == k.len) dst = a.state_out + (size_t)k.bh * slot;   // this segment holds the last position
+      else if (a.state_out && k.end == k.len) dst = a.state_out + k.bh * s.state_slot + k.v0;   // this segment holds the last position
       if (!dst) continue;
       if (vec_state) {
         for (int hc = 0; hc < 2; ++hc) {
@@ -498,14 +519,14 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
           for (int u = 0; u < 128 * PER / (32 * kWorkers); ++u) {
             const int e = tid + u * (32 * kWorkers), r = e / PER, c = hc * (DV / 2) + 4 * (e % PER);
-            if (r < s.dk && c < s.dv)
-              *reinterpret_cast<float4*>(dst + (size_t)r * s.dv + c) = *reinterpret_cast<const float4*>(stage + r * L::kLd + 4 * (e % PER));
+            if (r < s.dk && c < k.dv)
+              *reinterpret_cast<float4*>(dst + (size_t)r * dst_ld + c) = *reinterpret_cast<const float4*>(stage + r * L::kLd + 4 * (e % PER));
           }
         }
       } else if (row < s.dk) {
 #pragma unroll
         for (int e = 0; e < CW; ++e)
-          if (col0 + e < s.dv) dst[(size_t)row * s.dv + col0 + e] = st[e];
+          if (col0 + e < k.dv) dst[(size_t)row * dst_ld + col0 + e] = st[e];
       }
     }
   } else if (warp == kMmaWarp) {
@@ -641,24 +662,24 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     Walk wk{(int)blockIdx.x, 0, 0, la_task<OUT, PARTS>(s, p, a, min((int)blockIdx.x, tasks - 1))};
     settle(wk);
     Walk wv_ = wk, wo = wk;
-    auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, const Walk& w, int zb, int zh) {
+    auto load = [&](unsigned char* dst, int D, const CUtensorMap& map, uint64_t* bar, const Walk& w, int x0, int zb, int zh) {
       if (issuer) {
         bar_expect(bar, PARTS * D * 2 * kCh);
         for (int part = 0; part < PARTS; ++part)
           for (int d = 0; d < D; d += 64)
-            tma_4d(dst + (part * D + d) / 64 * (kCh * 128), &map, bar, d, part * s.n + (int)w.k.t0 + w.c * kCh, zb, zh);
+            tma_4d(dst + (part * D + d) / 64 * (kCh * 128), &map, bar, x0 + d, part * s.n + (int)w.k.t0 + w.c * kCh, zb, zh);
       }
       __syncwarp();
     };
     auto load_v = [&]() {
-      load(vs + (wv_.j % NV) * L::kTileV, DV, vmap, &v_full[wv_.j % NV], wv_, wv_.k.b * mul.vb, wv_.k.h * mul.vh);
+      load(vs + (wv_.j % NV) * L::kTileV, DV, vmap, &v_full[wv_.j % NV], wv_, wv_.k.v0, wv_.k.b * mul.vb, wv_.k.h * mul.vh);
       next(wv_);
     };
     auto load_k = [&]() {
-      load(ks + (wk.j % NKQ) * L::kTileK, DK, kmap, &k_full[wk.j % NKQ], wk, wk.k.b * mul.kb, wk.k.h * mul.kh);
+      load(ks + (wk.j % NKQ) * L::kTileK, DK, kmap, &k_full[wk.j % NKQ], wk, 0, wk.k.b * mul.kb, wk.k.h * mul.kh);
     };
     auto load_q = [&]() {
-      load(qs + (wk.j % NKQ) * L::kTileK, DK, qmap, &q_full[wk.j % NKQ], wk, wk.k.b * mul.qb, wk.k.h * mul.qh);
+      load(qs + (wk.j % NKQ) * L::kTileK, DK, qmap, &q_full[wk.j % NKQ], wk, 0, wk.k.b * mul.qb, wk.k.h * mul.qh);
     };
     for (int c = 0; c < NV; ++c) {
       if (wv_.i < tasks) load_v();
@@ -796,7 +817,7 @@ bool aligned_heads(const void* x, const int64_t (&st)[3], const LaShape& s) {
   return true;
 }
 
-template <int DK, int DV, int PARTS>
+template <int DK, int DV, int PARTS, bool ADD = false>
 cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms, cudaStream_t st) {
   CUtensorMap qm, km, vm, om{};
   LaMul mul{};
@@ -806,12 +827,12 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
     return cudaErrorInvalidValue;
   const int vec_out = PARTS == 1 ? mappable(a.o, s.os, s) && map_heads(&om, a.o, s.os, s, 1, s.dv, &ob, &oh)
                                  : aligned_heads(a.o, s.os, s);
-  const int vec_state = s.dv % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
+  const int vec_state = s.dv % 4 == 0 && s.state_ld % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int tasks = s.B * s.H * p.G;
+  const int tasks = s.B * s.H * (PARTS == 3 ? (s.dv + 63) / 64 : 1) * p.G;
   cfg.gridDim = dim3((unsigned)(tasks < num_sms ? tasks : num_sms));
   cfg.blockDim = dim3(kLaTcThreads);
   cfg.stream = st;
@@ -819,13 +840,13 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.G > 1) {
-    constexpr auto kern = k_linattn_tc<DK, DV, false, PARTS>;
+    constexpr auto kern = k_linattn_tc<DK, DV, false, PARTS, false>;
     cfg.dynamicSmemBytes = LaSmem<DK, DV, false, PARTS>::bytes;
     if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
     if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
-  constexpr auto kern = k_linattn_tc<DK, DV, true, PARTS>;
+  constexpr auto kern = k_linattn_tc<DK, DV, true, PARTS, ADD>;
   cfg.dynamicSmemBytes = LaSmem<DK, DV, true, PARTS>::bytes;
   if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit);
@@ -838,8 +859,19 @@ size_t operand_bytes(const LaShape& s, int d) {
 }  // namespace
 
 bool linattn_tc_fits(const LaShape& s) {
-  // the three parts of an fp32 position index stay below 2^31; its tiles fit shared memory up to 64 dimensions
-  return s.n > 0 && (s.bf16 ? s.dk <= 128 && s.dv <= 128 : s.dk <= 64 && s.dv <= 64 && s.n <= (1 << 29));
+  // the three parts of an fp32 position index stay below 2^31
+  return s.n > 0 && (s.bf16 ? s.dk <= 128 && s.dv <= 128 : s.n <= (1 << 29));
+}
+
+// What fp32 launches work on: tiles fit shared memory up to 64 dimensions, blocks of value
+// dimensions are like heads of their own, those of key dimensions follow one another.
+LaShape linattn_tc_block(const LaShape& s) {
+  LaShape b = s;
+  if (s.bf16) return b;
+  b.H *= (s.dv + 63) / 64;
+  b.dk = s.dk < 64 ? s.dk : 64;
+  b.dv = s.dv < 64 ? s.dv : 64;
+  return b;
 }
 
 size_t linattn_tc_layout_bytes(const LaShape& s, const LaPtrs& a) {
@@ -917,7 +949,24 @@ cudaError_t launch_linattn_tc(const LaShape& shape, const LaPlan& p, const LaPtr
                                     s.H, rows);
     if (e != cudaSuccess) return e;
   }
-  if (!s.bf16) return run<64, 64, 3>(s, p, a, num_sms, st);
+  s.state_slot = (int64_t)s.dk * s.dv;
+  s.state_ld = s.dv;
+  if (!s.bf16) {
+    // q . k is the sum over blocks of key dimensions, and so are the outputs (each block after
+    // the first adds to them); the state's blocks are apart
+    for (int k0 = 0; k0 < s.dk; k0 += 64) {
+      LaShape t = s;
+      LaPtrs b = a;
+      t.dk = s.dk - k0 < 64 ? s.dk - k0 : 64;
+      b.q = (const __nv_bfloat16*)a.q + k0;
+      b.k = (const __nv_bfloat16*)a.k + k0;
+      if (a.state_in) b.state_in = a.state_in + (size_t)k0 * s.dv;
+      if (a.state_out) b.state_out = a.state_out + (size_t)k0 * s.dv;
+      const cudaError_t e = k0 == 0 ? run<64, 64, 3>(t, p, b, num_sms, st) : run<64, 64, 3, true>(t, p, b, num_sms, st);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
   if (s.dk <= 64) return s.dv <= 64 ? run<64, 64, 1>(s, p, a, num_sms, st) : run<64, 128, 1>(s, p, a, num_sms, st);
   return s.dv <= 64 ? run<128, 64, 1>(s, p, a, num_sms, st) : run<128, 128, 1>(s, p, a, num_sms, st);
 }

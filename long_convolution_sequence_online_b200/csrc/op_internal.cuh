@@ -38,6 +38,10 @@ struct LaShape {
   int bf16;
   float scale;
   int64_t qs[3], ks[3], vs[3], os[3];
+  // Tensor-core form of a block of key dimensions: where the states' blocks lie (elements
+  // between (sequence, head)s, between rows).
+  int64_t state_slot;
+  int state_ld;
 };
 
 // A prompt is cut into G segments of seg positions (a multiple of the chunk)
@@ -65,11 +69,13 @@ struct LaPtrs {
 // Scratch of a prompt: the segments' states, then inputs that are laid out first.
 size_t linattn_prefill_workspace(const LaShape& s, const LaPtrs& a, int num_sms);
 cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& a, void* workspace, int num_sms, cudaStream_t st);
-// Tensor-core form (k_linattn_tc.cu): dimensions up to 128, fp32 up to 64. `layout`:
-// scratch for inputs that no tensor map describes, and all fp32 ones.
+// Tensor-core form (k_linattn_tc.cu): bf16 dimensions up to 128, fp32 in blocks of 64
+// (linattn_tc_block: the heads and dimensions that a launch works on, for the plan and its
+// scratch). `layout`: scratch for inputs that no tensor map describes, and all fp32 ones.
 bool linattn_tc_fits(const LaShape& s);
+LaShape linattn_tc_block(const LaShape& s);
 size_t linattn_tc_layout_bytes(const LaShape& s, const LaPtrs& a);
-LaPlan linattn_tc_plan(const LaShape& s, int num_sms);
+LaPlan linattn_tc_plan(const LaShape& block, int num_sms);
 cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a, void* layout, int num_sms, cudaStream_t st);
 // Whether a bounded wait gave up in these kernels since the last check
 // (synchronises the stream; the flag is cleared).

@@ -810,3 +810,36 @@ def test_sizes_beyond_32_bits_are_refused(fi):
     with pytest.raises(ValueError, match="2\\^31"):
         t = x[0].expand(big, 1, 1)
         fi.linattn_step(t, t, t, ld, S, t)
+
+
+@pytest.mark.parametrize("n,B,H,dk,dv,fused,lens,carried", [
+    (300, 2, 2, 65, 129, False, [300, 131], True),       # blocks of one dimension, odd rows of the state
+    (1000, 1, 2, 130, 70, True, None, True),             # several segments
+    (1300, 2, 1, 256, 256, False, [1300, 0], True),
+    (129, 3, 1, 100, 40, True, [1, 129, 128], False),
+    (700, 1, 1, 40, 200, False, None, True),
+    (150, 90, 1, 72, 130, False, None, False),           # more blocks than SMs
+])
+def test_prefill_fp32_in_blocks_of_dimensions(fi, n, B, H, dk, dv, fused, lens, carried):
+    q, k, v, ld, s0 = _la_inputs(n, B, H, dk, dv, "f32", n + dv, fused)
+    lengths = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if lens is not None:
+        for b, m in enumerate(lens):
+            for t in (q, k, v):
+                t[m:, b] = math.nan
+    base = torch.full((n, B, H, dv + 3), 7.0, device="cuda")
+    o = base[..., 1:dv + 1]                               # rows at no 16-byte boundary
+    state = s0.clone() if carried else torch.full_like(s0, math.nan)
+    fi.linattn_prefill(q, k, v, ld, o, state_in=state if carried else None, state_out=state, lengths=lengths, scale=dk ** -0.5)
+    again, S = torch.full((n, B, H, dv), 7.0, device="cuda"), torch.empty_like(s0)
+    fi.linattn_prefill(q, k, v, ld, again, state_in=s0 if carried else None, state_out=S, lengths=lengths, scale=dk ** -0.5)
+    fi.op_sync()
+    assert torch.equal(o, again) and torch.equal(state, S)
+    assert (base[..., 0] == 7.0).all() and (base[..., dv + 1:] == 7.0).all()
+    if lens is not None:
+        for b, m in enumerate(lens):
+            assert (o[m:, b] == 7.0).all()
+            o[m:, b] = 0
+            for t in (q, k, v):
+                t[m:, b] = 0
+    _check_la(o, state, q, k, v, ld, dk ** -0.5, s0 if carried else None, lens, "f32")
