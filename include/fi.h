@@ -316,7 +316,7 @@ FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, c
  *            captured graphs among them, need a workspace each.
  * A q, k or v that is not finite at a used position makes outputs of its
  * sequence and head non-finite from that position on, and may do so up to 127
- * positions before it. n = 0 copies the state; n <= 2^30.
+ * positions before it. n = 0 copies the state; n <= 2^29.
  * Errors: FI_E_INVALID (NULL, sizes, strides, alignment, o == an input, workspace
  * too small), FI_E_CUDA. */
 FI_API fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,

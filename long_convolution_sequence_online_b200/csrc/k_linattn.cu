@@ -8,9 +8,8 @@
 // Every power of g has an exponent >= 0, so nothing overflows whatever the decay.
 //
 // The chunked form here takes the shapes whose tiles do not fit the tensor cores' kernel
-// (k_linattn_tc.cu): bf16 above 128 dimensions, more than 2^29 fp32 positions. Bound by
-// shared-memory reads of its 4 x 4 outer products with one CTA per SM: 4 x 2048 positions, 8
-// heads of 256, bf16 1.61 ms (12 TFLOP/s).
+// (k_linattn_tc.cu): bf16 above 128 dimensions. Bound by shared-memory reads of its 4 x 4
+// outer products with one CTA per SM: 4 x 2048 positions, 8 heads of 256 1.6 ms (12 TFLOP/s).
 #include "op_internal.cuh"
 
 namespace fi {
@@ -356,14 +355,19 @@ size_t linattn_prefill_workspace(const LaShape& s, const LaPtrs& a, int num_sms)
 
 cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& ptrs, void* workspace, int num_sms, cudaStream_t st) {
   LaPtrs a = ptrs;
+  if (s.n == 0) {                          // the state before is the state after
+    const size_t bytes = (size_t)s.B * s.H * s.dk * s.dv * sizeof(float);
+    if (!a.state_out || a.state_out == a.state_in) return cudaSuccess;
+    return a.state_in ? cudaMemcpyAsync(a.state_out, a.state_in, bytes, cudaMemcpyDeviceToDevice, st)
+                      : cudaMemsetAsync(a.state_out, 0, bytes, st);
+  }
   a.ws = (float*)workspace;
   if (linattn_tc_fits(s)) {
     const LaShape b = linattn_tc_block(s);
     const LaPlan p = linattn_tc_plan(b, num_sms);
     return launch_linattn_tc(s, p, a, (unsigned char*)workspace + la_workspace_bytes(b, p), num_sms, st);
   }
-  const LaPlan p = la_plan(s, num_sms);
-  return s.bf16 ? prefill_dk<__nv_bfloat16>(s, p, a, st) : prefill_dk<float>(s, p, a, st);
+  return prefill_dk<__nv_bfloat16>(s, la_plan(s, num_sms), a, st);
 }
 
 cudaError_t launch_linattn_step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay,

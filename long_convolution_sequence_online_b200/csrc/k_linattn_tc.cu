@@ -859,8 +859,7 @@ size_t operand_bytes(const LaShape& s, int d) {
 }  // namespace
 
 bool linattn_tc_fits(const LaShape& s) {
-  // the three parts of an fp32 position index stay below 2^31
-  return s.n > 0 && (s.bf16 ? s.dk <= 128 && s.dv <= 128 : s.n <= (1 << 29));
+  return !s.bf16 || (s.dk <= 128 && s.dv <= 128);
 }
 
 // What fp32 launches work on: tiles fit shared memory up to 64 dimensions, blocks of value

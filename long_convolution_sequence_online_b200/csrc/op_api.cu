@@ -35,7 +35,7 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // Grids index sequences x heads in one dimension.
 constexpr int64_t kMaxRows = 65535;
-constexpr int32_t kMaxPositions = 1 << 30;
+constexpr int32_t kMaxPositions = 1 << 29;        // the three parts of fp32 rows are indexed below 2^31
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxLd = (int64_t)1 << 38;      // below a tensor map's 2^40 bytes
 
@@ -59,11 +59,11 @@ fi_status check_linattn(const fi_linattn_config* c, int64_t positions, LaShape* 
   // passes over the whole extent below it
   struct Dim { int64_t stride, count; } d[3] = {{c->o_stride[0], positions}, {c->o_stride[1], c->batch}, {c->o_stride[2], c->heads}};
   std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  int64_t extent = c->value_dim;
+  __int128 extent = c->value_dim;
   for (const Dim& x : d) {
     if (x.count <= 1) continue;
     if (x.stride < extent) return invalid("o_stride: rows of o overlap");
-    extent = x.stride * (x.count - 1) + extent;
+    extent += (__int128)x.stride * (x.count - 1);
   }
   *s = LaShape{};
   s->H = c->heads;
@@ -83,7 +83,7 @@ fi_status check_linattn(const fi_linattn_config* c, int64_t positions, LaShape* 
 
 fi_status check_linear(const fi_linear_config* c, int32_t n, bool residual, LinShape* s) {
   if (!c) return invalid("cfg is NULL");
-  if (n < 0 || n > kMaxPositions / 2) return invalid("n must be in [0, 2^29]");
+  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^29]");
   if (c->in_features < 1 || c->in_features > (1 << 20)) return invalid("in_features must be in [1, 2^20]");
   if (c->out_features < 1 || c->out_features > (1 << 20)) return invalid("out_features must be in [1, 2^20]");
   if (c->dtype != FI_F32 && c->dtype != FI_BF16) return invalid("dtype must be FI_F32 or FI_BF16");
@@ -109,7 +109,7 @@ fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, const vo
                                uint64_t* bytes) {
   if (!bytes) return invalid("bytes is NULL");
   *bytes = 0;
-  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^30]");
+  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^29]");
   LaShape s;
   const fi_status r = check_linattn(cfg, n, &s);
   if (r != FI_OK) return r;
@@ -126,7 +126,7 @@ fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, const vo
 fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
                              const float* log_decay, const int32_t* lengths, const float* state_in, float* state_out,
                              void* o, void* workspace, uint64_t workspace_bytes, void* stream) {
-  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^30]");
+  if (n < 0 || n > kMaxPositions) return invalid("n must be in [0, 2^29]");
   LaShape s;
   const fi_status r = check_linattn(cfg, n, &s);
   if (r != FI_OK) return r;
