@@ -47,17 +47,32 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   const int row0 = (int)(blockIdx.x / split) * kBM;
   const int blocks = (s.K + kBK - 1) / kBK;
   const int b0 = (int)((int64_t)blocks * rank / split), b1 = (int)((int64_t)blocks * (rank + 1) / split);
-  if (warp == 0) tmem_alloc(&tmem_s, cols);
-  if (tid == 32) {
-    for (int i = 0; i < ST; ++i) {
-      bar_init(&full[i], 1);
-      bar_init(&empty[i], 1);
+  auto load = [&](int i) {                // stage of block b0 + i, by one thread
+    unsigned char* dst = ring + i % ST * SB;
+    bar_expect(&full[i % ST], SB);
+    for (int part = 0; part < PARTS; ++part) {
+      tma_2d(dst + part * WB, &wmap, &full[i % ST], (b0 + i) * kBK, part * s.N + row0);
+      tma_2d(dst + PARTS * WB + part * XB, &xmap, &full[i % ST], (b0 + i) * kBK, part * s.n);
     }
-    bar_init(&done, 1);
-    abort_s = 0;
-    bar_init_fence();
-    tma_prefetch(&xmap);
-    tma_prefetch(&wmap);
+  };
+  const int ahead = min(ST, b1 - b0);     // the first copies go out before the other warps are ready
+  if (warp == 0) {
+    if (elect_one()) {
+      tma_prefetch(&xmap);
+      tma_prefetch(&wmap);
+      for (int i = 0; i < ST; ++i) {
+        bar_init(&full[i], 1);
+        bar_init(&empty[i], 1);
+      }
+      bar_init(&done, 1);
+      abort_s = 0;
+      bar_init_fence();
+      pdl_wait_primary();
+      for (int i = 0; i < ahead; ++i) load(i);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    tmem_alloc(&tmem_s, cols);
   }
   fence_before();
   __syncthreads();
@@ -72,19 +87,11 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   if (warp == 0) {
     const bool issuer = elect_one();
     bool alive = true;
-    int i = 0;
+    int i = ahead;
     for (; i < b1 - b0; ++i) {
-      const int st = i % ST;
-      alive = i < ST || warp_wait(&empty[st], (i / ST - 1) & 1, wait_limit, abort_flag);
+      alive = warp_wait(&empty[i % ST], (i / ST - 1) & 1, wait_limit, abort_flag);
       if (!alive) break;
-      if (issuer) {
-        unsigned char* dst = ring + st * SB;
-        bar_expect(&full[st], SB);
-        for (int part = 0; part < PARTS; ++part) {
-          tma_2d(dst + part * WB, &wmap, &full[st], (b0 + i) * kBK, part * s.N + row0);
-          tma_2d(dst + PARTS * WB + part * XB, &xmap, &full[st], (b0 + i) * kBK, part * s.n);
-        }
-      }
+      if (issuer) load(i);
       __syncwarp();
     }
     if (!alive && lane == 0) give_up();
@@ -194,7 +201,7 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
   if (split > 1) cluster_sync_relaxed();                   // others may still read this CTA's sums
   else __syncthreads();
   fence_after();
-  if (warp == 0) tmem_free(tmem, cols);
+  if (warp == 1) tmem_free(tmem, cols);
 }
 
 // At most kWarpRows rows of x, operands as they stand: a warp per RW rows of W, its
