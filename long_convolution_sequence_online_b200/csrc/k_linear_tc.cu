@@ -14,9 +14,9 @@
 //
 // Bound: the tensor pipe. 16384 x 2048 -> 8192 bf16 + GELU 439 to 460 us (1.2 PFLOP/s
 // under the power cap, where the library's product alone takes 400 to 415), 8192 x 2048 ->
-// 2048 49 us (46); fp32 8192 x 768 -> 768 + GELU 57 us, 10 of them laying out, the
-// product at 59 % of the tensor pipe (192 tiles are 2.6 rounds). Small products are
-// bound by latency, 6 to 7 us up to a contraction of 1000.
+// 2048 49 us (46); fp32 8192 x 768 -> 768 + GELU 59 us, 10 of them laying out (192 tiles
+// are 2.6 rounds of the pairs), 4096 x 2048 -> 2048 170 us. Small products are bound by
+// latency, 6 to 7 us up to a contraction of 1000.
 //
 // Operands come by TMA, which wants bf16 rows that start at 16-byte boundaries.
 // Others are laid out so first, by a launch of their own into scratch (on chip,
@@ -28,9 +28,9 @@
 // bits), and the products x0w0 + x0w1 + x1w0 + x1w1 + x0w2 + x2w0 are added up (the
 // rest is below 2^-24). The tensor core does not round its sums to nearest: left
 // in one accumulator, such products at a contraction of 2048 were 1.4e-5 off in
-// the 2-norm; with two blocks of 64 to an accumulator (smallest products of a block
-// first), added up in the epilogue warps' registers, they are 7e-7 off, cuBLAS's fp32
-// product 8e-7.
+// the 2-norm, with two blocks of 64 to an accumulator 6e-7; with one, smallest products
+// first, added up in the epilogue warps' registers, they are 1e-7 off, the library's
+// fp32 product 8e-7.
 #include "op_internal.cuh"
 #include "tc.cuh"
 
@@ -47,27 +47,30 @@ constexpr int kLinThreads = 32 * (kEpiWarps + 2);
 
 __device__ int g_linear_error;   // a bounded wait gave up since the last check
 
-// fp32: blocks that share an accumulator before the epilogue warps add them up.
-constexpr int kSumBlocks = 2;
-// Stage of the ring: `units` x (x tile 128 x 128 bytes, half of a W tile BN / 2 x
-// 128 bytes). The units are the parts of fp32 values, or two blocks of the
-// contraction: a stage's waits and signals take 350 to 450 cycles whatever its
-// size, more than the 264 that the MMAs of one block take at BN = 128.
+// Stage of the ring: an x tile 128 x 128 bytes and half of a W tile, BN / 2 x 128 bytes. bf16:
+// of two blocks of the contraction (a stage's waits and signals take 350 to 450 cycles
+// whatever its size, more than the 264 that the MMAs of one block take at BN = 128). fp32: of
+// one part of a block's values, the smallest part first, as the products let go of them:
+// with whole blocks only two fit, and the copies of one had to be there within the MMAs of the
+// other.
 template <int PARTS>
 constexpr int kStageBlocks = PARTS == 3 ? 1 : 2;
 template <int BN, int PARTS>
-constexpr int stage_bytes() { return PARTS * kStageBlocks<PARTS> * (kBM + BN / 2) * 128; }
+constexpr int stage_bytes() { return kStageBlocks<PARTS> * (kBM + BN / 2) * 128; }
+// bytes of an epilogue warp's stage (Staged below): 32 rows of 64 bytes and 16 more, 32 biases
+constexpr int kStagingBytes = 32 * (64 + 16) + 128;
 template <int BN, int PARTS>
-constexpr int num_stages() { return 196608 / stage_bytes<BN, PARTS>(); }
-// bytes of an epilogue warp's stage (Staged below): 32 rows of 32 results and 16 bytes, 32 biases
-template <int PARTS>
-constexpr int staging_bytes() { return 32 * (32 * (PARTS == 3 ? 4 : 2) + 16) + 128; }
+constexpr int num_stages() { return (232448 - 1024 - kEpiWarps * kStagingBytes) / stage_bytes<BN, PARTS>(); }
 template <int BN, int PARTS>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kEpiWarps * staging_bytes<PARTS>();
+  return 1024 + (size_t)num_stages<BN, PARTS>() * stage_bytes<BN, PARTS>() + kEpiWarps * kStagingBytes;
 }
-template <int BN>
-constexpr uint32_t acc_cols() { return BN <= 128 ? 256 : 512; }   // two accumulators
+// Accumulators: two; fp32, which changes them at every block, four, so that an epilogue
+// has four blocks' time.
+template <int PARTS>
+constexpr int kAccs = PARTS == 3 ? 4 : 2;
+template <int BN, int PARTS>
+constexpr uint32_t acc_cols() { return kAccs<PARTS> * BN <= 256 ? 256 : 512; }
 
 struct LinTiles {
   int mt, nt, group;   // row tiles, column tiles, row tiles per group
@@ -89,22 +92,23 @@ __device__ __forceinline__ float activate(float u) {
   else return linear_act<ACT>(u);
 }
 
-// act(acc + bias) + residual of 32 columns, a row per lane, go to y by way of shared
+// act(acc + bias) + residual of 64 bytes of columns, a row per lane, go to y by way of shared
 // memory, so that a warp's accesses to memory run along the rows (a row per lane costs a lookup per lane and access: 8192 x 768 -> 2048 bf16 25.4
 // us, along the rows 21.4). Rows may start anywhere (not ALIGNED) and end inside the
 // chunk: each is moved up in shared memory by the elements `a` that its address in
 // memory is past a 16-byte boundary, so that memory is still read and written in whole
-// units of 16 bytes; its 32 elements then start with E - a single ones, end with a, and
-// have units between (a = 0: units alone). A lane's rows lie 8 or E apart and so share
+// units of 16 bytes; its elements then start with E - a single ones, end with a, and
+// have units between (a = 0: units alone). A lane's rows lie 8 apart and so share
 // their a, which keeps addresses out of the loops: with two warps per scheduler it is
 // instructions that bound this. (8192 x 768 -> 767 bf16 + GELU + residual: 23.6 us, 36.0
 // with addresses formed per access; 1777 x 865 -> 1727 + tanh + residual: 20.7, 27.3 an
 // element at a time.)
 template <typename T, bool ALIGNED>
 struct StagedSide {                                        // y or the residual: the warp's 32 rows
-  static constexpr int E = 16 / sizeof(T), U = 32 / E;     // elements of a unit, units of a chunk
+  static constexpr int C = 64 / sizeof(T);                 // columns of a chunk
+  static constexpr int E = 16 / sizeof(T), U = C / E;      // elements of a unit, units of a chunk
   static constexpr int H = E / 4;                          // single elements of a lane and row
-  static constexpr int kWords = 32 * sizeof(T) / 4, kRow = 32 * sizeof(T) + 16;
+  static constexpr int kWords = 16, kRow = 64 + 16;
   T* p;
   int64_t ld;
   T *unit_p, *single_p[H];
@@ -126,7 +130,7 @@ struct StagedSide {                                        // y or the residual:
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const int e = lane / 8 + 4 * h;
-      c = e < E - a ? e : 32 - E + e;
+      c = e < E - a ? e : C - E + e;
       single_p[h] = p + r * ld + c;
       single_s[h] = r * kRow + (c + a) * (int)sizeof(T);
     }
@@ -139,15 +143,15 @@ struct StagedSide {                                        // y or the residual:
 template <typename T, bool ALIGNED>
 struct Staged {
   using S = StagedSide<T, ALIGNED>;
-  static constexpr int E = S::E, U = S::U, H = S::H, kWords = S::kWords, kRow = S::kRow;
+  static constexpr int C = S::C, E = S::E, U = S::U, H = S::H, kWords = S::kWords, kRow = S::kRow;
   S y, res;
   uint4 unit[U];                                           // a lane's share of a residual on its way
   T single[4 * H];
 
-  __device__ __forceinline__ void fetch(int c, int rows) {   // the columns c .. c + 31 are there
+  __device__ __forceinline__ void fetch(int c, int rows) {   // the columns c .. c + C - 1 are there
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (res.units + E * i < rows) unit[i] = *reinterpret_cast<const uint4*>(res.unit_p + c + i * (E * res.ld));
+      if (res.units + 8 * i < rows) unit[i] = *reinterpret_cast<const uint4*>(res.unit_p + c + i * (8 * res.ld));
 #pragma unroll
     for (int i = 0; i < 4 && !ALIGNED; ++i)
 #pragma unroll
@@ -156,33 +160,33 @@ struct Staged {
   }
 
   // v = act(v + bias) + residual of a row per lane, to y's columns c on. rows, cols:
-  // how many there are. With 32 columns the residual has been fetched, and next()
+  // how many there are. With all C the residual has been fetched, and next()
   // fetches the next chunk's.
   template <int ACT, typename Next>
-  __device__ __forceinline__ void store(float (&v)[32], int c, int rows, int cols, const T* bias, bool residual, Next next,
+  __device__ __forceinline__ void store(float (&v)[C], int c, int rows, int cols, const T* bias, bool residual, Next next,
                                         unsigned char* stg, int lane) {
-    const bool whole = cols >= 32;
+    const bool whole = cols >= C;
     float* bs = reinterpret_cast<float*>(stg + 32 * kRow);
-    bs[lane] = bias && lane < cols ? op_load(bias + lane) : 0.f;
+    bs[lane] = bias && lane < C && lane < cols ? op_load(bias + lane) : 0.f;
     if (residual) {
       if (whole) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-          if (res.units + E * i < rows) *reinterpret_cast<uint4*>(stg + res.unit_s + i * (E * kRow)) = unit[i];
+          if (res.units + 8 * i < rows) *reinterpret_cast<uint4*>(stg + res.unit_s + i * (8 * kRow)) = unit[i];
 #pragma unroll
         for (int i = 0; i < 4 && !ALIGNED; ++i)
 #pragma unroll
           for (int h = 0; h < H; ++h)
             if (res.singles + 8 * i < rows) *reinterpret_cast<T*>(stg + res.single_s[h] + i * (8 * kRow)) = single[i * H + h];
         next();
-      } else if (lane < cols) {
+      } else if (lane < cols) {                            // fewer than C
 #pragma unroll 16
         for (int r = 0; r < rows; ++r) *reinterpret_cast<T*>(res.at(stg, r, lane)) = res.p[r * res.ld + c + lane];
       }
     }
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
+    for (int e = 0; e < C; e += 4) {
       const float4 b = *reinterpret_cast<const float4*>(bs + e);
       v[e] = activate<T, ACT>(v[e] + b.x);
       v[e + 1] = activate<T, ACT>(v[e + 1] + b.y);
@@ -245,9 +249,9 @@ struct Staged {
     if (whole) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (y.units + E * i < rows)
-          *reinterpret_cast<uint4*>(y.unit_p + c + i * (E * y.ld)) =
-              *reinterpret_cast<const uint4*>(stg + y.unit_s + i * (E * kRow));
+        if (y.units + 8 * i < rows)
+          *reinterpret_cast<uint4*>(y.unit_p + c + i * (8 * y.ld)) =
+              *reinterpret_cast<const uint4*>(stg + y.unit_s + i * (8 * kRow));
 #pragma unroll
       for (int i = 0; i < 4 && !ALIGNED; ++i)
 #pragma unroll
@@ -269,12 +273,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
             const T* __restrict__ bias, const T* residual, T* y, int log_split, int wait_limit) {
   constexpr int BW = BN / 2;                       // W rows in this CTA's stages
-  constexpr int KS = kStageBlocks<PARTS>, UNITS = PARTS * KS;
+  constexpr int KS = kStageBlocks<PARTS>, NA = kAccs<PARTS>;
   constexpr int ST = num_stages<BN, PARTS>(), SB = stage_bytes<BN, PARTS>();
   constexpr int XB = kBM * 128, WB = BW * 128;
   constexpr int TM = 2 * kBM;                      // rows of a tile
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t full_bar[ST], empty_bar[ST], acc_full[2], acc_empty[2];
+  __shared__ uint64_t full_bar[ST], empty_bar[ST], acc_full[NA], acc_empty[NA];
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
   unsigned char* ring = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
@@ -288,13 +292,13 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   const uint16_t pair = (uint16_t)(3 << (crank & ~1));
   if constexpr (!SPLIT) log_split = 0;
   const int split = 1 << log_split, first = blockIdx.x >> (log_split + 1), stride = gridDim.x >> (log_split + 1);
-  if (warp == 0) tmem_alloc2(&tmem_s, acc_cols<BN>());
+  if (warp == 0) tmem_alloc2(&tmem_s, acc_cols<BN, PARTS>());
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
       bar_init(&full_bar[i], 1);
       bar_init(&empty_bar[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NA; ++i) {
       bar_init(&acc_full[i], 1);
       bar_init(&acc_empty[i], 2 * kEpiWarps);
     }
@@ -318,8 +322,8 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
   if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = warp >> 2;
-    constexpr int CW = BN / 2;                     // columns of this warp
-    unsigned char* stg = staging + warp * staging_bytes<PARTS>();
+    constexpr int CW = BN / 2, SC = Staged<T, ALIGNED>::C;   // columns of this warp, of a chunk
+    unsigned char* stg = staging + warp * kStagingBytes;
     uint32_t unit = 0;                             // accumulators drained
     bool alive = true;
     for (int t = first; t < g.tiles && alive; t += stride) {
@@ -339,31 +343,31 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       staged.y.init(y + row0 * s.ldy + col0, s.ldy, lane);
       if (residual) staged.res.init(const_cast<T*>(residual) + row0 * s.ldr + col0, s.ldr, lane);
       auto fetch = [&](int c) {
-        if (residual && c < CW && rows > 0 && col0 + c + 32 <= s.N) staged.fetch(c, rows);
+        if (residual && c < CW && rows > 0 && col0 + c + SC <= s.N) staged.fetch(c, rows);
       };
-      auto store = [&](float (&v)[32], int c) {
+      auto store = [&](float (&v)[SC], int c) {
         if constexpr (SPLIT) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sums[(half * CW + c + e) * kBM + 32 * q + lane] = v[e];
+          for (int e = 0; e < SC; ++e) sums[(half * CW + c + e) * kBM + 32 * q + lane] = v[e];
         } else {
           if (rows <= 0 || col0 + c >= s.N) return;
           staged.template store<ACT>(v, c, rows, s.N - col0 - c, bias ? bias + col0 + c : nullptr, residual != nullptr,
-                                     [&] { fetch(c + 32); }, stg, lane);
+                                     [&] { fetch(c + SC); }, stg, lane);
         }
       };
       if constexpr (!SPLIT) fetch(0);
       if constexpr (PARTS == 1) {
-        alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
+        alive = warp_wait(&acc_full[unit % NA], (unit / NA) & 1, wait_limit, abort_flag);
         if (!alive) break;
         fence_after();
         auto load = [&](int c, float (&v)[32]) {
           uint32_t r[32];
-          tmem_ld32(at + (unit & 1) * BN + c, r);
+          tmem_ld32(at + (unit % NA) * BN + c, r);
           ld_wait();
           if (c + 32 >= CW) {                      // all columns read: the MMA may overwrite them
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_leader(&acc_empty[unit & 1]);
+            if (lane == 0) bar_arrive_leader(&acc_empty[unit % NA]);
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
@@ -379,28 +383,28 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
         float acc[CW];
 #pragma unroll
         for (int e = 0; e < CW; ++e) acc[e] = 0.f;
-        for (int kb = k0; kb < k1; kb += kSumBlocks, ++unit) {
-          alive = warp_wait(&acc_full[unit & 1], (unit >> 1) & 1, wait_limit, abort_flag);
+        for (int kb = k0; kb < k1; ++kb, ++unit) {
+          alive = warp_wait(&acc_full[unit % NA], (unit / NA) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
 #pragma unroll
           for (int c = 0; c < CW; c += 16) {
             uint32_t r[16];
-            tmem_ld16(at + (unit & 1) * BN + c, r);
+            tmem_ld16(at + (unit % NA) * BN + c, r);
             ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[c + e] += __uint_as_float(r[e]);
           }
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive_leader(&acc_empty[unit & 1]);
+          if (lane == 0) bar_arrive_leader(&acc_empty[unit % NA]);
         }
         if (!alive) break;
 #pragma unroll
-        for (int c = 0; c < CW; c += 32) {
-          float v[32];
+        for (int c = 0; c < CW; c += SC) {
+          float v[SC];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = acc[c + e];
+          for (int e = 0; e < SC; ++e) v[e] = acc[c + e];
           store(v, c);
         }
       }
@@ -414,19 +418,20 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
       uint32_t kbs = 0, unit = 0;
       bool alive = true;
       for (int t = first; t < g.tiles && alive; t += stride) {
-        for (int kb = k0; kb < k1; ++kb, ++kbs) {
-          const int st = kbs % ST;
-          const bool start = PARTS > 1 ? (kb - k0) % kSumBlocks == 0 : kb == k0;   // of an accumulator
+        for (int kb = k0; kb < k1; ++kb) {
+          const bool start = PARTS > 1 || kb == k0;              // of an accumulator
           if (start)
-            alive = unit < 2 || warp_wait(&acc_empty[unit & 1], ((unit >> 1) - 1) & 1, wait_limit, abort_flag);
-          alive = alive && warp_wait(&full_bar[st], (kbs / ST) & 1, wait_limit, abort_flag);
+            alive = unit < NA || warp_wait(&acc_empty[unit % NA], (unit / NA - 1) & 1, wait_limit, abort_flag);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+            alive = alive && warp_wait(&full_bar[(kbs + p) % ST], ((kbs + p) / ST) & 1, wait_limit, abort_flag);
           if (!alive) break;
           fence_after();
-          const uint32_t xa = saddr(ring + (size_t)st * SB), wa = xa + UNITS * XB;
-          const uint32_t d = tmem + (unit & 1) * BN;
-          const bool last = kb == k1 - 1 || (PARTS > 1 && (kb - k0) % kSumBlocks == kSumBlocks - 1);
+          const uint32_t d = tmem + (unit % NA) * BN;
+          const bool last = PARTS > 1 || kb == k1 - 1;
           if (issuer) {
             if constexpr (PARTS == 1) {
+              const uint32_t xa = saddr(ring + (size_t)(kbs % ST) * SB), wa = xa + KS * XB;
               const int steps = min(KS * kBK / 16, (s.K - kb * KS * kBK + 15) / 16);   // of 16
 #pragma unroll
               for (int k = 0; k < KS * kBK / 16; ++k) {
@@ -434,18 +439,26 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
                 const uint32_t xo = (k / 4) * XB + (k % 4) * 32, wo = (k / 4) * WB + (k % 4) * 32;
                 mma2(d, desc_k(xa + xo), desc_k(wa + wo), id, !start || k > 0);
               }
+              commit2(&empty_bar[kbs % ST], pair);
             } else {
               constexpr int px[6] = {2, 0, 1, 1, 0, 0}, pw[6] = {0, 2, 1, 0, 1, 0};   // smallest first
+              uint32_t at[3];                                    // the stage of part 2 - j follows that of 3 - j
 #pragma unroll
-              for (int p = 0; p < 6; ++p)
+              for (int j = 0; j < 3; ++j) at[2 - j] = saddr(ring + (size_t)((kbs + j) % ST) * SB);
+#pragma unroll
+              for (int p = 0; p < 6; ++p) {
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                  mma2(d, desc_k(xa + px[p] * XB + 32 * k), desc_k(wa + pw[p] * WB + 32 * k), id, !start || p > 0 || k > 0);
+                  mma2(d, desc_k(at[px[p]] + 32 * k), desc_k(at[pw[p]] + XB + 32 * k), id, p > 0 || k > 0);
+                if (p == 1) commit2(&empty_bar[kbs % ST], pair);         // part 2 is done with
+                if (p == 4) commit2(&empty_bar[(kbs + 1) % ST], pair);
+                if (p == 5) commit2(&empty_bar[(kbs + 2) % ST], pair);
+              }
             }
-            commit2(&empty_bar[st], pair);
-            if (last) commit2(&acc_full[unit & 1], pair);
+            if (last) commit2(&acc_full[unit % NA], pair);
           }
           __syncwarp();
+          kbs += PARTS;
           if (last) ++unit;
         }
       }
@@ -462,24 +475,25 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     for (int t = first; t < g.tiles && alive; t += stride) {
       int m, n;
       tile_at(g, t, m, n);
-      for (int kb = k0; kb < k1; ++kb, ++kbs) {
-        const int st = kbs % ST, k = kb * KS * kBK;
-        alive = kbs < ST || warp_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag);
-        if (!alive) break;
-        if (issuer) {
-          unsigned char* dst = ring + (size_t)st * SB;
-          const int units = PARTS == 1 ? min(KS, (s.K - k + kBK - 1) / kBK) : PARTS;
-          if (rank == 0) bar_expect(&full_bar[st], 2 * units * (XB + WB));   // both CTAs' tiles
+      for (int kb = k0; kb < k1 && alive; ++kb)
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u)
-            if (u < units) {
-              const int ku = PARTS == 1 ? k + u * kBK : k;
-              tma_2d_pair(dst + u * XB, &xmap, &full_bar[st], ku, (PARTS == 1 ? 0 : u * s.n) + m * TM + rank * kBM);
-              tma_2d_pair(dst + UNITS * XB + u * WB, &wmap, &full_bar[st], ku, (PARTS == 1 ? 0 : u * s.N) + n * BN + rank * BW);
-            }
+        for (int p = PARTS - 1; p >= 0; --p, ++kbs) {
+          const int st = kbs % ST, k = kb * KS * kBK;
+          alive = kbs < ST || warp_wait(&empty_bar[st], (kbs / ST - 1) & 1, wait_limit, abort_flag);
+          if (!alive) break;
+          if (issuer) {
+            unsigned char* dst = ring + (size_t)st * SB;
+            const int units = min(KS, (s.K - k + kBK - 1) / kBK);
+            if (rank == 0) bar_expect(&full_bar[st], 2 * units * (XB + WB));   // both CTAs' tiles
+#pragma unroll
+            for (int u = 0; u < KS; ++u)
+              if (u < units) {
+                tma_2d_pair(dst + u * XB, &xmap, &full_bar[st], k + u * kBK, p * s.n + m * TM + rank * kBM);
+                tma_2d_pair(dst + KS * XB + u * WB, &wmap, &full_bar[st], k + u * kBK, p * s.N + n * BN + rank * BW);
+              }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
     }
     if (!alive && lane == 0) give_up();
     // no copy of this CTA may still be in flight when it ends: each stage's last use is done
@@ -494,11 +508,12 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     const int64_t row0 = (int64_t)m * TM + rank * kBM + 32 * q;
     const int col0 = n * BN + c0, rows = (int)min((int64_t)32, s.n - row0);
     const bool work = warp < kEpiWarps && 32 * half < width && rows > 0 && col0 < s.N;
+    constexpr int SC = Staged<T, ALIGNED>::C;
     Staged<T, ALIGNED> staged;
     if (work) {
       staged.y.init(y + row0 * s.ldy + col0, s.ldy, lane);
       if (residual) staged.res.init(const_cast<T*>(residual) + row0 * s.ldr + col0, s.ldr, lane);
-      if (residual && col0 + 32 <= s.N) staged.fetch(0, rows);
+      if (residual && col0 + SC <= s.N) staged.fetch(0, rows);
     }
     fence_before();
     cluster_sync();
@@ -515,14 +530,24 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] += u[e];
       }
-      staged.template store<ACT>(v, 0, rows, s.N - col0, bias ? bias + col0 : nullptr, residual != nullptr, [] {},
-                                 staging + warp * staging_bytes<PARTS>(), lane);
+#pragma unroll
+      for (int c = 0; c < 32; c += SC) {
+        if (col0 + c >= s.N) break;
+        float u[SC];
+#pragma unroll
+        for (int e = 0; e < SC; ++e) u[e] = v[c + e];
+        auto next = [&] {
+          if (residual && c + SC < 32 && col0 + c + 2 * SC <= s.N) staged.fetch(c + SC, rows);
+        };
+        staged.template store<ACT>(u, c, rows, s.N - col0 - c, bias ? bias + col0 + c : nullptr, residual != nullptr, next,
+                                   staging + warp * kStagingBytes, lane);
+      }
     }
   }
   fence_before();
   cluster_sync_relaxed();                          // no CTA ends while another may still signal it or read its sums
   fence_after();
-  if (warp == 0) tmem_free2(tmem, acc_cols<BN>());
+  if (warp == 0) tmem_free2(tmem, acc_cols<BN, PARTS>());
 }
 
 // An operand that TMA cannot take (fp32, or rows at no 16-byte boundary) as
