@@ -1,5 +1,5 @@
 // Declarations of the context-free operators (linear attention, linear layer):
-// launchers in k_linattn.cu and k_linear.cu, argument checks and entry points
+// launchers in k_linattn*.cu and k_linear_*.cu, argument checks and entry points
 // in op_api.cu.
 #pragma once
 
