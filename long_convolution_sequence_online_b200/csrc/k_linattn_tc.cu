@@ -191,6 +191,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       *abort_flag = 1;
       atomicExch(&g_linattn_error, 1);
     }
+    __syncwarp();
   };
   // The arithmetic warps meet at barriers of their own, so after a wait that gave up
   // they run on to the end (no wait lasts any more, the results are not valid).
@@ -208,7 +209,10 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     const int col0 = grp * CW;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     float* stage = reinterpret_cast<float*>(wv);   // [128][kLd], when w V is not in use
-    auto sync = [] { asm volatile("bar.sync 5, %0;" ::"n"(32 * kWorkers) : "memory"); };
+    auto sync = [] {
+      __syncwarp();                                // the barrier takes whole warps; lanes may have parted before it
+      asm volatile("bar.sync 5, %0;" ::"n"(32 * kWorkers) : "memory");
+    };
     float st[CW];                                  // S, row `row`, columns col0 ..
     // S as the B operand of Q S: rows of 64 bf16 columns, 128-byte swizzle.
     auto publish = [&]() {
@@ -283,6 +287,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
       for (int d = 0; d < CW; d += 16) {
         uint32_t r[16], q[16];
+        __syncwarp();                              // lanes part below, at rows behind the end; these loads take whole warps
         tmem_ld16(lanes + C::inter + col0 + d, r);
         tmem_ld16(lanes + C::intra + col0 + d, q);
         ld_wait();

@@ -110,11 +110,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Cluster barriers. The instructions are `aligned`: a warp has to arrive as one, whatever
+// branches its lanes took before, so its lanes are brought together first.
 // Execution only: nothing written before is made visible.
 __device__ __forceinline__ void cluster_sync_relaxed() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Another CTA's copy of a place in shared memory.
