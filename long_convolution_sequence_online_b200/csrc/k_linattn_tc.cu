@@ -131,7 +131,7 @@ template <int DK, int DV, bool OUT, int PARTS, bool ADD>
 __global__ void __launch_bounds__(kLaTcThreads, 1)
 k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap qmap,
              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-             const __grid_constant__ CUtensorMap omap, LaMul mul, int vec_out, int vec_state, int wait_limit) {
+             const __grid_constant__ CUtensorMap omap, LaMul mul, int vec_out, int tile_out, int vec_state, int wait_limit) {
   using L = LaSmem<DK, DV, OUT, PARTS>;
   using C = LaCols<PARTS>;
   using T = typename std::conditional<PARTS == 3, float, __nv_bfloat16>::type;
@@ -274,14 +274,16 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // a time (more would not fit the registers beside the state, and a spill goes to
     // L2: shared memory leaves little L1). They go to V's tile, which is not read any
     // more, and from there by TMA (a lane per row, stores from registers touch 32
-    // lines each and took 2500 cycles a chunk); rows behind the end of a sequence,
-    // which a tile would overwrite, and an o that no tensor map describes, go directly.
+    // lines each and took 2500 cycles a chunk). Directly go rows behind the end of a
+    // sequence, which a tile would overwrite, an o that no tensor map describes, and one
+    // whose rows are no multiple of 16 bytes: a TMA store writes whole units of 16
+    // bytes, also over what stands behind the end of a row.
     auto outputs = [&](const LaTask& k, int c, int j) {
       need(&o_done, j & 1);
       fence_after();
       const int64_t t = k.t0 + (int64_t)c * kCh + row;
       const float f_inter = s.scale * G[row + 1];   // P carries the scale
-      const bool tile = STAGED && vec_out && !(k.ragged && c == k.nch - 1);
+      const bool tile = STAGED && tile_out && !(k.ragged && c == k.nch - 1);
       unsigned char* dst = vs + (j % NV) * L::kTileV + row * 128;
       T* op = (T*)a.o + k.b * s.os[1] + k.h * s.os[2] + t * s.os[0] + k.v0 + col0;
 #pragma unroll
@@ -710,7 +712,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       if constexpr (STAGED) {
         alive = wait(&o_staged, j & 1);
         if (!alive) break;
-        if (issuer && vec_out && !(wo.k.ragged && wo.c == wo.k.nch - 1)) {
+        if (issuer && tile_out && !(wo.k.ragged && wo.c == wo.k.nch - 1)) {
           for (int d = 0; d < DV; d += 64)
             tma_store_4d(&omap, vs + (j % NV) * L::kTileV + (d / 64) * (kCh * 128), d, (int)wo.k.t0 + wo.c * kCh, wo.k.b, wo.k.h);
           bulk_commit();
@@ -832,6 +834,7 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
     return cudaErrorInvalidValue;
   const int vec_out = PARTS == 1 ? mappable(a.o, s.os, s) && map_heads(&om, a.o, s.os, s, 1, s.dv, &ob, &oh)
                                  : aligned_heads(a.o, s.os, s);
+  const int tile_out = PARTS == 1 && vec_out && s.dv % 8 == 0;
   const int vec_state = s.dv % 4 == 0 && s.state_ld % 4 == 0 && ((uintptr_t)a.state_in & 15) == 0 && ((uintptr_t)a.state_out & 15) == 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -848,13 +851,13 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
     constexpr auto kern = k_linattn_tc<DK, DV, false, PARTS, false>;
     cfg.dynamicSmemBytes = LaSmem<DK, DV, false, PARTS>::bytes;
     if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit)) != cudaSuccess)
+    if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, (int)kDefaultWaitLimit)) != cudaSuccess)
       return e;
   }
   constexpr auto kern = k_linattn_tc<DK, DV, true, PARTS, ADD>;
   cfg.dynamicSmemBytes = LaSmem<DK, DV, true, PARTS>::bytes;
   if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, vec_state, (int)kDefaultWaitLimit);
+  return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, (int)kDefaultWaitLimit);
 }
 
 size_t operand_bytes(const LaShape& s, int d) {

@@ -76,7 +76,8 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
       ::"r"(saddr(dst)), "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// From shared memory; parts outside the tensor are not written.
+// From shared memory; parts outside the tensor are not written, in units of 16 bytes:
+// the innermost dimension has to be a multiple of them.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
                ::"l"(map), "r"(saddr(src)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");

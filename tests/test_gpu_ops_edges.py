@@ -18,7 +18,7 @@ torch = pytest.importorskip("torch")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("d,pad,shift", [(64, 8, 0), (64, 3, 1), (128, 8, 0), (100, 1, 0), (33, 2, 0)])
+@pytest.mark.parametrize("d,pad,shift", [(64, 8, 0), (64, 3, 1), (128, 8, 0), (100, 1, 0), (33, 2, 0), (33, 7, 0), (20, 4, 0)])
 def test_prefill_sequences_that_end_inside_a_warp(fi, d, pad, shift, dtype):  # noqa: F811
     # lengths at which the lanes of one warp stand on both sides of the end, at first,
     # middle and last rows of chunks; what lies between the rows of o, before the first and
@@ -43,3 +43,48 @@ def test_prefill_sequences_that_end_inside_a_warp(fi, d, pad, shift, dtype):  # 
             t[m:, b] = 0
     assert (base == 7.0).all()
     _check_la(got, S, q, k, v, ld, d ** -0.5, s0, lens, dtype)
+
+
+@pytest.mark.parametrize("n", [128, 300])
+@pytest.mark.parametrize("dk,dv,pad", [(33, 33, 7), (20, 20, 4), (100, 100, 4), (128, 121, 7), (61, 64, 8), (40, 65, 7)])
+def test_prefill_bf16_rows_padded_to_16_bytes(fi, n, dk, dv, pad):  # noqa: F811
+    # rows whose elements end inside a unit of 16 bytes at 16-byte strides: what pads the
+    # rows of o stays as it was, what pads those of q, k and v (NaN) is not used
+    B, H = 2, 2
+    g = torch.Generator(device="cuda").manual_seed(n + dk + dv)
+
+    def padded(d, fill):
+        base = torch.full((n, B, H, (d + 7) // 8 * 8), fill, dtype=torch.bfloat16, device="cuda")
+        return base, base[..., :d]
+
+    q, k, v = padded(dk, math.nan)[1], padded(dk, math.nan)[1], padded(dv, math.nan)[1]
+    for t in (q, k, v):
+        t.copy_(_rand(g, *t.shape))
+    base = torch.full((n, B, H, dv + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = base[..., :dv]
+    ld, s0 = torch.tensor([-0.1, -0.01], device="cuda"), _rand(g, B, H, dk, dv)
+    S = torch.empty_like(s0)
+    fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, scale=dk ** -0.5)
+    fi.op_sync()
+    assert (base[..., dv:] == 7.0).all()
+    _check_la(o, S, q, k, v, ld, dk ** -0.5, s0, None, "bf16")
+
+
+@pytest.mark.parametrize("n", [1, 5, 40, 100, 200, 600])
+@pytest.mark.parametrize("nin,nout", [(33, 65), (865, 129), (2001, 300)])
+def test_linear_bf16_rows_padded_to_16_bytes(fi, n, nin, nout):  # noqa: F811
+    # as above: what pads the rows of x and w (NaN) is not used
+    g = torch.Generator(device="cuda").manual_seed(n + nin)
+
+    def padded(rows, cols, scale=1.0):
+        base = torch.full((rows, (cols + 7) // 8 * 8), math.nan, dtype=torch.bfloat16, device="cuda")
+        base[:, :cols] = _rand(g, rows, cols, scale=scale)
+        return base[:, :cols]
+
+    x, w, r = padded(n, nin), padded(nout, nin, nin ** -0.5), padded(n, nout)
+    base = torch.full((n, (nout + 7) // 8 * 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = base[:, :nout]
+    fi.linear(x, w, y, residual=r, act="tanh")
+    fi.op_sync()
+    assert (base[:, nout:] == 7.0).all()
+    _check_linear(y, x, w, None, r, "tanh", "bf16")
