@@ -303,7 +303,8 @@ FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, c
 /* A prompt of n positions (chunked form: matrix products inside chunks of
  * positions, the state carried between them).
  * log_decay: device [H] fp32, natural logarithms; values above 0 are taken as 0
- *            (no decay), -infinity keeps nothing of the past.
+ *            (no decay), -infinity keeps nothing of the past: the state before is
+ *            dropped whatever it holds, infinities and NaN too.
  * lengths:   NULL, or device [B] int32: sequence b has lengths[b] positions
  *            (clamped to [0, n]); q, k and v behind them are not used, whatever
  *            they hold, and o is left as it was there.

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kLaThreads) k_linattn(LaShape s, LaPlan p, LaP
     const float* src = p.G > 1 ? ws : s_in;
     for (int g = 0; g <= seg && src; ++g) {
       // slot 0: the state before the prompt; slot g: segment g - 1's contribution
-      if (g == 0 && !s_in) continue;
+      if (g == 0 && (!s_in || (la_drops(ld2) && len > 0))) continue;
       const float f = la_pow(ld2, (g == 0 ? seg : seg - g) * p.seg);
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H;
   const int c = (blockIdx.y * 32 + lane) * V;
   const bool in = c < s.dv;
-  const float g = la_pow(la_log2_decay(__ldg(log_decay + h)), 1);
+  const float ld2 = la_log2_decay(__ldg(log_decay + h)), g = la_pow(ld2, 1);
+  const bool drops = la_drops(ld2);
   if (tid < s.dk) {
     qs[tid] = op_load(q + b * s.qs[1] + h * s.qs[2] + tid);
     ks[tid] = op_load(k + b * s.ks[1] + h * s.ks[2] + tid);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
         *reinterpret_cast<vec*>(f) = x[u];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          f[e] = fmaf(ks[d], vv[e], g * f[e]);
+          f[e] = fmaf(ks[d], vv[e], drops ? 0.f : g * f[e]);
           acc[e] = fmaf(qs[d], f[e], acc[e]);
         }
         __stcs(reinterpret_cast<vec*>(sp + (size_t)d * s.dv), *reinterpret_cast<const vec*>(f));

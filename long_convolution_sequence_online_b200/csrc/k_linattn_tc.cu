@@ -366,7 +366,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       for (int e = 0; e < CW; ++e) st[e] = 0.f;
       const float* src = !OUT ? nullptr : p.G > 1 ? ws : s_in;
       const int src_ld = p.G > 1 ? ws_ld : s.state_ld;
-      const int g0 = s_in ? 0 : 1;
+      const int g0 = s_in && !(la_drops(ld2) && k.len > 0) ? 0 : 1;   // an empty sequence passes its state on
       constexpr int PER = DV / 8;                  // float4s of half a row of the state
       if (src && g0 <= k.seg) {
         // slot 0: the state before the prompt; slot g: segment g - 1's contribution

@@ -90,6 +90,10 @@ __device__ __forceinline__ float la_log2_decay(float log_decay) {
   const float l = log_decay < -1e30f ? -1e30f : (log_decay > 0.f ? 0.f : log_decay);
   return (float)((double)l * 1.4426950408889634);
 }
+// A decay of 0 (log_decay -infinity): the state before is dropped whatever it holds,
+// where 0 times an infinity would be NaN. A power that merely underflows does not drop
+// it: an infinity there stays one.
+__device__ __forceinline__ bool la_drops(float log2_decay) { return log2_decay < -1e30f; }
 // g^lag, lag >= 0.
 __device__ __forceinline__ float la_pow(float log2_decay, int lag) { return exp2f(log2_decay * (float)lag); }
 

@@ -88,3 +88,46 @@ def test_linear_bf16_rows_padded_to_16_bytes(fi, n, nin, nout):  # noqa: F811
     fi.op_sync()
     assert (base[:, nout:] == 7.0).all()
     _check_linear(y, x, w, None, r, "tanh", "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(1, 64), (130, 64), (130, 128), (2065, 64), (2065, 128), (70, 200), (900, 200)])
+def test_a_decay_of_zero_drops_any_state(fi, n, d, dtype):  # noqa: F811
+    # infinities and NaN in the state before reach nothing where log_decay is -infinity,
+    # and do where the decay only underflows; an empty sequence passes its state on
+    H = 3
+    q, k, v, _, s0 = _la_inputs(n, 2, H, d, d, dtype, n + d)
+    ld = torch.tensor([-math.inf, -math.inf, -200.0], device="cuda")
+    s0[:, 0, 3, 5], s0[:, 0, 4, 6], s0[:, 1] = math.inf, math.nan, -math.inf
+    lengths = torch.tensor([n, 0], dtype=torch.int32, device="cuda")
+    outs = []
+    for state in (s0, torch.zeros_like(s0)):
+        o, S = torch.zeros(n, 2, H, d, dtype=DT[dtype], device="cuda"), state.clone()
+        fi.linattn_prefill(q, k, v, ld, o, state_in=S, state_out=S, lengths=lengths, scale=0.25)
+        outs.append((o, S))
+    fi.op_sync()
+    (o, S), (want_o, want_S) = outs
+    assert torch.isfinite(o).all() and torch.equal(o[:, :, :2], want_o[:, :, :2])
+    assert torch.isfinite(S[0]).all() and torch.equal(S[0, :2], want_S[0, :2])
+    assert torch.equal(S[1].nan_to_num(7.0), s0[1].nan_to_num(7.0)) and torch.equal(S[1].isnan(), s0[1].isnan())
+    s0[0, 2, 1, 1] = math.inf
+    S = s0.clone()
+    fi.linattn_prefill(q, k, v, ld, o, state_in=S, state_out=S, lengths=lengths, scale=0.25)
+    fi.op_sync()
+    assert not torch.isfinite(S[0, 2, 1, 1]) and torch.isfinite(S[0, :2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [63, 64, 66])
+def test_a_decay_of_zero_drops_any_state_in_a_step(fi, d, dtype):  # noqa: F811
+    q, k, v, _, s0 = _la_inputs(1, 2, 3, d, d, dtype, d)
+    ld = torch.tensor([-math.inf, -math.inf, -200.0], device="cuda")
+    s0[:, 0, 3, 5], s0[:, 0, 4, 6], s0[:, 1], s0[:, 2, 1, 1] = math.inf, math.nan, -math.inf, math.inf
+    outs = []
+    for state in (s0, torch.zeros_like(s0)):
+        o, S = torch.empty(2, 3, d, dtype=DT[dtype], device="cuda"), state.clone()
+        fi.linattn_step(q[0], k[0], v[0], ld, S, o)
+        outs.append((o, S))
+    fi.op_sync()
+    assert torch.equal(outs[0][0][:, :2], outs[1][0][:, :2]) and torch.equal(outs[0][1][:, :2], outs[1][1][:, :2])
+    assert not torch.isfinite(outs[0][1][:, 2, 1, 1]).any()
