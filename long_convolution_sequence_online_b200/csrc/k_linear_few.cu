@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(256) k_linear_rows(LinShape s, const T* __rest
       if (lane == t) out = v;
     }
     if (lane < s.n) {
-      float u = linear_act<ACT>(out + (bias ? op_load(bias + c) : 0.f));
+      const float in = out + (bias ? op_load(bias + c) : 0.f);
+      float u = sizeof(T) == 2 ? linear_act_bf16<ACT>(in) : linear_act<ACT>(in);   // as the other forms have it
       if (residual) u += op_load(residual + lane * s.ldr + c);
       op_store(y + lane * s.ldy + c, u);
     }

@@ -131,3 +131,28 @@ def test_a_decay_of_zero_drops_any_state_in_a_step(fi, d, dtype):  # noqa: F811
     fi.op_sync()
     assert torch.equal(outs[0][0][:, :2], outs[1][0][:, :2]) and torch.equal(outs[0][1][:, :2], outs[1][1][:, :2])
     assert not torch.isfinite(outs[0][1][:, 2, 1, 1]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,shift", [(1, 0), (1, 1), (2, 1), (8, 0), (40, 0), (130, 0), (300, 1)])
+def test_gelu_of_negative_arguments(fi, n, shift, dtype):  # noqa: F811
+    # u Phi(u) at arguments -9 .. -3 to its own size, in every form of the layer. The
+    # argument is rounded three times at most (its parts, their sum, the factor of
+    # 1 / sqrt 2) and u^2 + 1 times that reaches the result; erfcf is within 4 steps of 2^-23,
+    # the fit for bf16 results within 6.3e-7, products and sums around them within 8
+    # roundings; the result's own rounding comes last.
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dt, nin, nout = DT[dtype], 16, 400
+    w = torch.zeros(nout, nin, dtype=dt, device="cuda")
+    w[:, 3] = (-9.0 + 6.0 * torch.rand(nout, generator=g, device="cuda")).to(dt)
+    x = torch.zeros(n * nin + 8, dtype=dt, device="cuda")[shift:shift + n * nin].view(n, nin)
+    x[:, 3] = 1.0
+    x[1::2, 3] = 0.5
+    y = torch.empty(n, nout, dtype=dt, device="cuda")
+    fi.linear(x, w, y, act="gelu")
+    fi.op_sync()
+    u = _f64(x) @ _f64(w).T
+    want = u * np.array([0.5 * math.erfc(-t / math.sqrt(2.0)) for t in u.ravel()]).reshape(u.shape)
+    tol = (3 * (1 + u * u) + 8 + 8 + 11) * U32 + (U16 if dtype == "bf16" else 0)
+    err = np.abs(_f64(y) - want) / np.abs(want)
+    assert np.all(err <= tol), (err / tol).max()
