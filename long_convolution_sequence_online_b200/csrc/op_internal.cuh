@@ -178,7 +178,7 @@ __device__ __forceinline__ float linear_act_bf16(float u) {
     p = fmaf(p, t, 0.107837f);
     p = fmaf(p, t, 0.10559982f);
     const float tail = z * (p * t) * ex2_fast(z * z * -0.72134752f);
-    return u > 0.f ? u - tail : (u <= 0.f ? -tail : u);   // NaN stays
+    return u > 0.f ? u - tail : fmaf(u, 0.f, -tail);   // NaN stays, -infinity becomes it (u 0), as in u Phi(u)
   }
   if constexpr (ACT == FI_ACT_SILU) return __fdividef(u, 1.0f + __expf(-u));
   if constexpr (ACT == FI_ACT_TANH) {

@@ -156,3 +156,29 @@ def test_gelu_of_negative_arguments(fi, n, shift, dtype):  # noqa: F811
     tol = (3 * (1 + u * u) + 8 + 8 + 11) * U32 + (U16 if dtype == "bf16" else 0)
     err = np.abs(_f64(y) - want) / np.abs(want)
     assert np.all(err <= tol), (err / tol).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "gelu", "silu", "relu", "tanh"])
+@pytest.mark.parametrize("n,shift", [(1, 0), (1, 1), (2, 1), (40, 0), (130, 0), (300, 1)])
+def test_activations_of_infinities(fi, n, shift, act, dtype):  # noqa: F811
+    # bf16: what the formula gives, in every form of the layer. fp32 operands that are not
+    # finite make the argument not finite: what the formula gives of it, or of NaN.
+    dt, nin, nout = DT[dtype], 16, 40
+    x = torch.zeros(n * nin + 8, dtype=dt, device="cuda")[shift:shift + n * nin].view(n, nin)
+    x[:, 3] = 1.0
+    for value in (math.inf, -math.inf, math.nan):
+        w = torch.zeros(nout, nin, dtype=dt, device="cuda")
+        w[5, 3] = value
+        y = torch.empty(n, nout, dtype=dt, device="cuda")
+        fi.linear(x, w, y, act=act)
+        fi.op_sync()
+        want = {"none": value, "gelu": value if value > 0 else math.nan, "silu": value if value > 0 else math.nan,
+                "relu": max(value, 0.0) if value == value else math.nan, "tanh": math.copysign(1.0, value) if value == value else math.nan}[act]
+        got = y[:, 5].double()
+        same = torch.isnan(got) if math.isnan(want) else got == want
+        if dtype == "f32":
+            same = same | torch.isnan(got)
+        assert same.all(), (value, got)
+        y[:, 5] = 0
+        assert (y == 0).all()
