@@ -336,8 +336,8 @@ typedef enum { FI_ACT_NONE = 0, FI_ACT_GELU = 1, FI_ACT_SILU = 2, FI_ACT_RELU = 
 /* y = R(act(x W^T + bias) + residual) over n rows, one rounding at the end.
  * GELU is the exact form u Phi(u), as in fi_set_mlp_block. fp32 products are
  * formed from operands split into three bf16 parts (24 bits); an fp32 operand that
- * is not finite, or above 3.38e38 in magnitude, makes act's argument not finite
- * in its row (x) or column (w) of y. */
+ * is not finite makes act's argument not finite in its row (x) or column (w) of y:
+ * NaN or an infinity, depending on the sizes. */
 typedef struct {
   int32_t in_features;  /* 1..2^20 */
   int32_t out_features; /* 1..2^20 */

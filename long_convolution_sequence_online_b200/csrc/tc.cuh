@@ -236,9 +236,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
 }
 __device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-// a, b as three bf16 parts each (8 bits a part: together fp32's 24).
+// As pack2; what rounds beyond the largest finite value becomes that value.
+__device__ __forceinline__ uint32_t pack2_finite(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// a, b as three bf16 parts each (8 bits a part: together fp32's 24). The first stays
+// finite for every finite value (above 3.39e38 rounding would make it infinite); an
+// infinity leaves infinity and NaN in the others.
 __device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-  p0 = pack2(a, b);
+  p0 = pack2_finite(a, b);
   a -= lo_f(p0);
   b -= hi_f(p0);
   p1 = pack2(a, b);

@@ -421,7 +421,8 @@ def _linear_config(key, x, w, y, bias, residual, act):
 def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
     """y = act(x w^T + bias) + residual (fi_linear): x [n][in], w [out][in], y and
     residual [n][out], bias [out], all float32 or all bfloat16, rows of any stride
-    with contiguous elements. act: none, gelu, silu, relu or tanh. residual may be y."""
+    with contiguous elements. act: none, gelu, silu, relu or tanh. residual may be y.
+    A float32 operand that is not finite makes act's argument not finite (NaN or an infinity)."""
     px, pw = x.data_ptr(), w.data_ptr()
     key = (x.shape, w.shape, y.shape, x.stride(), w.stride(), y.stride(), x.dtype, w.dtype, y.dtype, x.get_device(),
            w.get_device(), y.get_device(), _look(bias), _look(residual), act, px & 15, pw & 15)

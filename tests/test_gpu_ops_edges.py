@@ -182,3 +182,34 @@ def test_activations_of_infinities(fi, n, shift, act, dtype):  # noqa: F811
         assert same.all(), (value, got)
         y[:, 5] = 0
         assert (y == 0).all()
+
+
+@pytest.mark.parametrize("n", [1, 9, 40, 130, 300])
+def test_linear_fp32_values_near_the_largest(fi, n):  # noqa: F811
+    # finite operands above 3.38e38, which round to no finite bf16 value
+    g = torch.Generator(device="cuda").manual_seed(n)
+    big = torch.finfo(torch.float32).max
+    x, w = _rand(g, n, 70), _rand(g, 50, 70)
+    x[:, ::3] = big
+    x[:, 1::3] = -3.3961775e38
+    w *= 2.0 ** -40
+    for a, b in ((x, w), (w[:1].expand(n, 70).contiguous(), x[:1].expand(50, 70).contiguous())):
+        y = torch.empty(n, 50, device="cuda")
+        fi.linear(a, b, y)
+        fi.op_sync()
+        assert torch.isfinite(y).all()
+        _check_linear(y, a, b, None, None, "none", "f32")
+
+
+@pytest.mark.parametrize("d", [64, 100])
+def test_prefill_fp32_values_near_the_largest(fi, d):  # noqa: F811
+    q, k, v, ld, s0 = _la_inputs(300, 1, 2, d, d, "f32", d)
+    q *= 2.0 ** -30
+    k *= 2.0 ** -30
+    v[::2], v[1::2] = 3.4e38, -3.3961775e38
+    s0[:] = torch.finfo(torch.float32).max
+    o, S = torch.empty_like(v), torch.empty_like(s0)
+    fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, scale=0.125)
+    fi.op_sync()
+    assert torch.isfinite(o).all()
+    _check_la(o, S, q, k, v, ld, 0.125, s0, None, "f32")
