@@ -289,11 +289,16 @@ def _check_sizes(*shapes):
         raise ValueError("a dimension is larger than 2^31 - 1")
 
 
-def _op_stream(stream, dev):
-    """The stream of a call whose tensors are on CUDA device `dev`, which must be the current one."""
+def _current(dev):
     import torch
     if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+
+
+def _op_stream(stream, dev):
+    """The stream of a call whose tensors are on CUDA device `dev`, which must be the current one."""
+    import torch
+    _current(dev)
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
@@ -308,7 +313,8 @@ def _scratch(need, like, stream, st):
 
 
 def _check_tensors(tensors, dtype):
-    """One CUDA device, and one of the library's types for those of `tensors` that are not None; its code."""
+    """One CUDA device, the current one (scratch sizes depend on it), and one of the library's types for
+    those of `tensors` that are not None; its code."""
     import torch
     if not _DTYPE_CODE:
         _DTYPE_CODE.update({torch.float32: FI_F32, torch.bfloat16: FI_BF16})
@@ -317,6 +323,7 @@ def _check_tensors(tensors, dtype):
     devices = {t.get_device() for t in tensors if t is not None}
     if len(devices) != 1 or -1 in devices:
         raise ValueError("expected CUDA tensors on one device")
+    _current(devices.pop())
     return _DTYPE_CODE[dtype]
 
 
