@@ -366,6 +366,7 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
     strides with a contiguous innermost dimension; log_decay [H] float32;
     lengths [B] int32 or None; state_in, state_out [B][H][key_dim][value_dim]
     float32, contiguous, or None (they may be the same tensor)."""
+    scale = float(scale)      # part of what is kept: by its value, whatever holds it
     pq, pk, pv = q.data_ptr(), k.data_ptr(), v.data_ptr()
     key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
            o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), _look(log_decay), _look(state_in),
@@ -386,6 +387,7 @@ def linattn_prefill(q, k, v, log_decay, o, state_in=None, state_out=None, length
 def linattn_step(q, k, v, log_decay, state, o, scale: float = 1.0, stream=None):
     """One position of every sequence (fi_linattn_step): q, k [B][H][key_dim],
     v, o [B][H][value_dim], state [B][H][key_dim][value_dim] float32, updated in place."""
+    scale = float(scale)
     key = (q.shape, k.shape, v.shape, o.shape, q.stride(), k.stride(), v.stride(), o.stride(), q.dtype, k.dtype, v.dtype,
            o.dtype, q.get_device(), k.get_device(), v.get_device(), o.get_device(), state.shape, state.stride(),
            state.dtype, state.get_device(), log_decay.shape, log_decay.stride(), log_decay.dtype, log_decay.get_device(),

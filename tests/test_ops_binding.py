@@ -89,3 +89,12 @@ def test_another_device_than_the_current_one_leaves_nothing_behind(fi, stand_in,
     assert stand_in.calls and fi._configs
     with pytest.raises(ValueError, match="not the current device"):
         call(fi, 1)
+
+
+@pytest.mark.parametrize("call", [_prompt, _step])
+def test_a_scale_that_changes_in_place_is_read_anew(fi, stand_in, call):
+    scale = torch.tensor(0.5)
+    call(fi, 0, scale=scale)
+    scale.fill_(2.0)
+    call(fi, 0, scale=scale)
+    assert stand_in.calls[0][1].scale == 0.5 and stand_in.calls[-1][1].scale == 2.0
