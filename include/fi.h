@@ -278,7 +278,7 @@ FI_API fi_status fi_op_sync(void* stream);
  * position, sequence or head shared by all); o's elements must be distinct and
  * not among the inputs'. */
 typedef struct {
-  int32_t heads;       /* H >= 1 */
+  int32_t heads;       /* H >= 1; B x H at most 2^22 */
   int32_t key_dim;     /* 1..256 */
   int32_t value_dim;   /* 1..256 */
   int32_t batch;       /* B >= 1 */

@@ -37,8 +37,8 @@ __device__ __forceinline__ void axpy4(float a, const float4& x, float (&y)[4]) {
   y[3] = fmaf(a, x.w, y[3]);
 }
 
-// Segment blockIdx.z of (sequence, head) blockIdx.y, value columns
-// [kSlice blockIdx.x, + kSlice). OUT = false: the segment's own contribution
+// Segment blockIdx.z of (sequence, head) blockIdx.x, value columns
+// [kSlice blockIdx.y, + kSlice). OUT = false: the segment's own contribution
 // to the state into slot segment + 1 (segment 0 also copies the state before
 // the prompt into slot 0). OUT = true: the outputs, and the state after the
 // last position.
@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kLaThreads) k_linattn(LaShape s, LaPlan p, LaP
   float* G = S + DKP * kSlice;             // g^0 .. g^C
   constexpr int LD = DKP + 4, LP = kC + 4, R = DKP / 64;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H;
-  const int c0 = blockIdx.x * kSlice, nc = min(kSlice, s.dv - c0);
+  const int bh = blockIdx.x, b = bh / s.H, h = bh - b * s.H;
+  const int c0 = blockIdx.y * kSlice, nc = min(kSlice, s.dv - c0);
   const int seg = blockIdx.z;
   const int len = la_length(a.lengths, b, s.n);
   const int64_t t0 = (int64_t)seg * p.seg;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
 template <typename T, int DKP>
 cudaError_t prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
   cudaError_t e;
-  const dim3 grid((unsigned)((s.dv + kSlice - 1) / kSlice), (unsigned)(s.B * s.H), (unsigned)p.G);
+  const dim3 grid((unsigned)(s.B * s.H), (unsigned)((s.dv + kSlice - 1) / kSlice), (unsigned)p.G);
   if (p.G > 1) {
     if ((e = allow_smem<k_linattn<T, DKP, false>>(la_smem<DKP>())) != cudaSuccess) return e;
     k_linattn<T, DKP, false><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);

@@ -33,8 +33,9 @@ cudaError_t device_sms(int* sms) {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Grids index sequences x heads in one dimension.
-constexpr int64_t kMaxRows = 65535;
+// Sequences x heads: with up to 4 blocks of dimensions and 64 segments each, tasks are
+// counted below 2^31.
+constexpr int64_t kMaxRows = 1 << 22;
 constexpr int32_t kMaxPositions = 1 << 29;        // the three parts of fp32 rows are indexed below 2^31
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxLd = (int64_t)1 << 38;      // below a tensor map's 2^40 bytes

@@ -213,3 +213,23 @@ def test_prefill_fp32_values_near_the_largest(fi, d):  # noqa: F811
     fi.op_sync()
     assert torch.isfinite(o).all()
     _check_la(o, S, q, k, v, ld, 0.125, s0, None, "f32")
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 8, 8), ("bf16", 8, 8), ("bf16", 1, 130), ("f32", 70, 3)])
+def test_more_than_65535_sequences_and_heads(fi, dtype, dk, dv):  # noqa: F811
+    # 4099 sequences of 16 heads: what smaller batches of them give
+    n, B, H = 3, 4099, 16
+    q, k, v, ld, s0 = _la_inputs(n, B, H, dk, dv, dtype, dk)
+    o, S = torch.empty_like(v), s0.clone()
+    fi.linattn_prefill(q, k, v, ld, o, state_in=S, state_out=S, scale=0.5)
+    o1 = torch.empty_like(o[0])
+    fi.linattn_step(q[0], k[0], v[0], ld, S, o1, scale=0.5)
+    for at in (0, 1000, 2000, 3000, 4000):
+        part = slice(at, min(at + 1000, B))
+        T, p, p1 = s0[part].clone(), torch.empty_like(v[:, part]), torch.empty_like(v[0, part])
+        fi.linattn_prefill(q[:, part], k[:, part], v[:, part], ld, p, state_in=T, state_out=T, scale=0.5)
+        fi.linattn_step(q[0, part], k[0, part], v[0, part], ld, T, p1, scale=0.5)
+        fi.op_sync()
+        assert torch.equal(p, o[:, part]) and torch.equal(p1, o1[part]) and torch.equal(T, S[part])
+    last = slice(B - 1, B)
+    _check_la(o[:, last], None, q[:, last], k[:, last], v[:, last], ld, 0.5, s0[last], None, dtype)
