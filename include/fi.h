@@ -373,6 +373,12 @@ FI_API fi_status fi_linear(const fi_linear_config* cfg, int32_t n, const void* x
  * at once, which exercises the FI_E_TIMEOUT path of fi_sync without any wait. */
 FI_API fi_status fi_debug_set_wait_limit(fi_ctx* ctx, int32_t limit);
 
+/* The same for the operators' kernels launched from now on in this process (a
+ * captured graph keeps the limit of its capture): exercises the FI_E_TIMEOUT path
+ * of fi_op_sync. Waits for copies and products under way at a kernel's end keep
+ * a limit of their own. Always FI_OK. */
+FI_API fi_status fi_debug_set_op_wait_limit(int32_t limit);
+
 /* Test hook (host only, no device work): the table of on-chip block pieces the
  * chunk kernel runs for a chunk of `chunk` positions (a power of two, 2..64):
  * retimed != 0 gives the table of a launch that covers a whole chunk (the chain

@@ -851,13 +851,13 @@ cudaError_t run(const LaShape& s, const LaPlan& p, const LaPtrs& a, int num_sms,
     constexpr auto kern = k_linattn_tc<DK, DV, false, PARTS, false>;
     cfg.dynamicSmemBytes = LaSmem<DK, DV, false, PARTS>::bytes;
     if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, (int)kDefaultWaitLimit)) != cudaSuccess)
+    if ((e = cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, op_wait_limit())) != cudaSuccess)
       return e;
   }
   constexpr auto kern = k_linattn_tc<DK, DV, true, PARTS, ADD>;
   cfg.dynamicSmemBytes = LaSmem<DK, DV, true, PARTS>::bytes;
   if ((e = allow_smem<kern>(cfg.dynamicSmemBytes)) != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, (int)kDefaultWaitLimit);
+  return cudaLaunchKernelEx(&cfg, kern, s, p, a, qm, km, vm, om, mul, vec_out, tile_out, vec_state, op_wait_limit());
 }
 
 size_t operand_bytes(const LaShape& s, int d) {

@@ -344,7 +344,7 @@ cudaError_t run_few(const LinCall& c) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, s, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, split, alloc, sum_blocks, vec,
-                            (int)kDefaultWaitLimit);
+                            op_wait_limit());
 }
 
 template <int ACT>

@@ -645,7 +645,7 @@ cudaError_t run_rows(const LinCall& c, int log_split) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, s, g, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, log_split,
-                            (int)kDefaultWaitLimit);
+                            op_wait_limit());
 }
 
 template <int BN, int PARTS, typename T, int ACT>

@@ -102,9 +102,18 @@ fi_status check_linear(const fi_linear_config* c, int32_t n, bool residual, LinS
   return FI_OK;
 }
 
+std::atomic<int> g_wait_limit{kDefaultWaitLimit};
+
 }  // namespace
 
+int fi::op_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 extern "C" {
+
+fi_status fi_debug_set_op_wait_limit(int32_t limit) {
+  g_wait_limit.store(limit < 0 ? kDefaultWaitLimit : limit, std::memory_order_relaxed);
+  return FI_OK;
+}
 
 fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, const void* q, const void* k, const void* v,
                                uint64_t* bytes) {

@@ -15,6 +15,10 @@ namespace fi {
 // later launch of the library's (the chunk kernel, say) reads what it takes for
 // long finished before it waits, and that may be an operator's result.
 
+// Checks of a barrier after which a wait in a kernel launched from now on gives up
+// (fi_debug_set_op_wait_limit).
+int op_wait_limit();
+
 // Allows a kernel `bytes` of dynamic shared memory, once per device (a kernel's
 // need is a constant of its instantiation).
 template <auto Kern>

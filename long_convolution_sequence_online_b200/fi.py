@@ -24,7 +24,7 @@ EXPORTED = ("fi_init", "fi_step", "fi_generate", "fi_generate_host", "fi_generat
             "fi_profile_read", "fi_destroy", "fi_status_str", "fi_last_error", "fi_debug_fft",
             "fi_generate_noalloc", "fi_debug_set_wait_limit", "fi_debug_chunk_schedule", "fi_prefill", "fi_profile_read_sides",
             "fi_set_mlp_block", "fi_linattn_workspace", "fi_linattn_prefill", "fi_linattn_step", "fi_linear", "fi_linear_workspace",
-            "fi_op_sync")
+            "fi_op_sync", "fi_debug_set_op_wait_limit")
 
 
 class FiError(RuntimeError):
@@ -88,6 +88,7 @@ def _load():
         "fi_linattn_prefill": [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
         "fi_linattn_step": [vp, vp, vp, vp, vp, vp, vp, vp],
         "fi_op_sync": [vp],
+        "fi_debug_set_op_wait_limit": [i32],
         "fi_linear_workspace": [vp, i32, vp, vp, ctypes.POINTER(ctypes.c_uint64)],
         "fi_linear": [vp, i32, vp, vp, vp, vp, vp, vp, ctypes.c_uint64, vp],
     }
@@ -448,6 +449,11 @@ def linear(x, w, y, bias=None, residual=None, act: str = "none", stream=None):
 def op_sync(stream=None):
     """Waits for the stream; raises FiError (FI_E_TIMEOUT) if a bounded wait in an operator's kernel gave up."""
     _check(lib.fi_op_sync(_stream(stream)), "fi_op_sync")
+
+
+def set_op_wait_limit(limit: int):
+    """Test hook: barrier checks after which a wait in an operator's kernel gives up (negative: the default)."""
+    _check(lib.fi_debug_set_op_wait_limit(limit), "fi_debug_set_op_wait_limit")
 
 
 def chunk_schedule(chunk: int, retimed: bool, coarse: bool = False):

@@ -233,3 +233,51 @@ def test_more_than_65535_sequences_and_heads(fi, dtype, dk, dv):  # noqa: F811
         assert torch.equal(p, o[:, part]) and torch.equal(p1, o1[part]) and torch.equal(T, S[part])
     last = slice(B - 1, B)
     _check_la(o[:, last], None, q[:, last], k[:, last], v[:, last], ld, 0.5, s0[last], None, dtype)
+
+
+@pytest.fixture()
+def wait_limit(fi):  # noqa: F811
+    yield fi.set_op_wait_limit
+    fi.set_op_wait_limit(-1)
+
+
+def _gives_up_and_recovers(fi, wait_limit, call, outputs, limits=(0, 1)):  # noqa: F811
+    # a wait that gives up ends the call, op_sync says so once, and what comes after is as
+    # it was before
+    call()
+    fi.op_sync()
+    want = [t.clone() for t in outputs]
+    for limit in limits:
+        wait_limit(limit)
+        call()
+        call()
+        wait_limit(-1)
+        if limit == 0:
+            with pytest.raises(fi.FiError) as e:
+                fi.op_sync()
+            assert e.value.status == fi.FI_E_TIMEOUT
+        else:                                # may have been long enough
+            try:
+                fi.op_sync()
+            except fi.FiError as e:
+                assert e.status == fi.FI_E_TIMEOUT
+        fi.op_sync()
+        for t in outputs:
+            t.zero_()
+        call()
+        fi.op_sync()
+        for t, w in zip(outputs, want):
+            assert torch.equal(t, w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nin,nout", [(20, 512, 300), (40, 2048, 2048), (64, 4096, 1000), (16, 8192, 8192), (100, 2048, 200)])
+def test_waits_that_give_up_linear_few_rows(fi, wait_limit, n, nin, nout, dtype):  # noqa: F811
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, w = _rand(g, n, nin, dtype=DT[dtype]), _rand(g, nout, nin, dtype=DT[dtype], scale=nin ** -0.5)
+    if dtype == "f32":
+        x = x[:64]                           # more rows run on tiles
+    base = torch.full((n * nout + 64,), 7.0, dtype=DT[dtype], device="cuda")
+    y = base[:x.shape[0] * nout].view(-1, nout)
+    _gives_up_and_recovers(fi, wait_limit, lambda: fi.linear(x, w, y, act="gelu"), [y])
+    assert (base[y.numel():] == 7.0).all()
