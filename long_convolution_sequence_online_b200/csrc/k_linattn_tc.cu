@@ -699,14 +699,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     for (; wo.i < tasks && alive; next(wo)) {                // what follows chunk wo.j
       const int j = wo.j;
       if (wk.i < tasks) {                                    // chunk j + NKQ
+        // both before either is asked for: the copies that are waited for at the end are
+        // those of whole chunks
         alive = wait(&k_empty[j % NKQ], (j / NKQ) & 1);
+        if constexpr (OUT) alive = alive && wait(&q_empty[j % NKQ], (j / NKQ) & 1);
         if (!alive) break;
         load_k();
-        if constexpr (OUT) {
-          alive = wait(&q_empty[j % NKQ], (j / NKQ) & 1);
-          if (!alive) break;
-          load_q();
-        }
+        if constexpr (OUT) load_q();
         next(wk);
       }
       if constexpr (STAGED) {

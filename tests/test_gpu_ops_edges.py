@@ -281,3 +281,17 @@ def test_waits_that_give_up_linear_few_rows(fi, wait_limit, n, nin, nout, dtype)
     y = base[:x.shape[0] * nout].view(-1, nout)
     _gives_up_and_recovers(fi, wait_limit, lambda: fi.linear(x, w, y, act="gelu"), [y])
     assert (base[y.numel():] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,B,H,d,ragged", [(100, 1, 2, 64, False), (2065, 1, 2, 64, False), (2065, 2, 1, 128, True),
+                                            (260, 160, 1, 40, False), (1000, 2, 3, 100, True)])
+def test_waits_that_give_up_prefill(fi, wait_limit, n, B, H, d, ragged, dtype):  # noqa: F811
+    q, k, v, ld, s0 = _la_inputs(n, B, H, d, d, dtype, n)
+    lengths = torch.tensor([n - 37 * b for b in range(B)], dtype=torch.int32, device="cuda") if ragged else None
+    base = torch.full((n * B * H * d + 64,), 7.0, dtype=DT[dtype], device="cuda")
+    o, S = base[:v.numel()].view_as(v), torch.empty_like(s0)
+    o.zero_()
+    _gives_up_and_recovers(fi, wait_limit, lambda: fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, lengths=lengths,
+                                                                      scale=d ** -0.5), [o, S])
+    assert (base[v.numel():] == 7.0).all()
