@@ -497,7 +497,19 @@ k_linear_tc(LinShape s, LinTiles g, const __grid_constant__ CUtensorMap xmap, co
     }
     if (!alive && lane == 0) give_up();
     // no copy of this CTA may still be in flight when it ends: each stage's last use is done
-    for (uint32_t i = kbs > ST ? kbs - ST : 0; i < kbs; ++i) bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDrainLimit);
+    const uint32_t oldest = kbs > ST ? kbs - ST : 0;
+    bool used = true;
+    for (uint32_t i = oldest; i < kbs && used; ++i) used = bar_wait(&empty_bar[i % ST], (i / ST) & 1, kDrainLimit, abort_flag);
+    if (!used) {
+      // The products gave up. Both CTAs' copies count on the leader's barriers, and the pair
+      // ends together: the leader waits for the stages that it asked for, the other CTA for
+      // as long as the limit allows (it may have asked for one more).
+      if (rank == 0) {
+        for (uint32_t i = oldest; i < kbs; ++i) bar_wait(&full_bar[i % ST], (i / ST) & 1, kDrainLimit);
+      } else {
+        bar_wait(&empty_bar[(kbs - 1) % ST], ((kbs - 1) / ST) & 1, kDrainLimit);
+      }
+    }
   }
   if constexpr (SPLIT) {
     // every pair left its sums in shared memory, where no stage is used any more; each

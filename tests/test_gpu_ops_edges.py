@@ -295,3 +295,16 @@ def test_waits_that_give_up_prefill(fi, wait_limit, n, B, H, d, ragged, dtype): 
     _gives_up_and_recovers(fi, wait_limit, lambda: fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, lengths=lengths,
                                                                       scale=d ** -0.5), [o, S])
     assert (base[v.numel():] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nin,nout", [(300, 64, 300), (300, 2048, 2048), (200, 2048, 128), (600, 4096, 256), (4100, 512, 2049)])
+def test_waits_that_give_up_linear_tiles(fi, wait_limit, n, nin, nout, dtype):  # noqa: F811
+    # one stage of the ring and many, tiles shared by several pairs, several tiles to a pair
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, w = _rand(g, n, nin, dtype=DT[dtype]), _rand(g, nout, nin, dtype=DT[dtype], scale=nin ** -0.5)
+    r = _rand(g, n, nout, dtype=DT[dtype])
+    base = torch.full((n * nout + 64,), 7.0, dtype=DT[dtype], device="cuda")
+    y = base[:n * nout].view(n, nout)
+    _gives_up_and_recovers(fi, wait_limit, lambda: fi.linear(x, w, y, residual=r, act="silu"), [y])
+    assert (base[n * nout:] == 7.0).all()
