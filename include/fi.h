@@ -272,7 +272,8 @@ FI_API fi_status fi_op_sync(void* stream);
 /* Linear attention with one decay per head, for sequence b, head h:
  *     S_t = g_h S_{t-1} + k_t v_t^T          (S: key_dim x value_dim, 32 bits)
  *     o_t = R(scale * q_t^T S_t)             g_h = exp(log_decay[h])
- * with R as above. Strides are in elements, between positions, sequences and
+ * with R as above, the one rounding to 16 bits: bf16 prompts may form products of
+ * operands off by 2^-16 of each besides (steps do not). Strides are in elements, between positions, sequences and
  * heads ([0], [1], [2]); the innermost dimension is contiguous. q, k and v may
  * be views (of one fused projection, say) and may have a stride of 0 (a
  * position, sequence or head shared by all); o's elements must be distinct and

@@ -4,15 +4,19 @@
 //
 // One CTA runs the chunks of a segment of one (sequence, head) in order. Per
 // chunk, with Q, K, V the 128-row tiles and S the state before it:
-//     scores = Q K^T            -> P = scale scores * g^{i-j} for j <= i (bf16, over them)
-//     inter  = Q S              (S rounded to bf16 as an operand)
-//     intra  = P V              (P read from tensor memory)
+//     scores = Q K^T            -> P = scale scores * g^{i-j} for j <= i (over them)
+//     inter  = Q S              (S as two bf16 parts)
+//     intra  = P V              (P as two bf16 parts, read from tensor memory)
 //     KV     = K^T (w V)        w_j = g^{m-1-j}, w V as three bf16 parts
 //     S     <- g^m S + KV       (fp32, in registers)
 //     o      = scale g^{i+1} inter + intra
-// Roundings below fp32: the result, P, and S where it enters Q S. P and S are
-// rounded once each to the results' own type, so each adds an error of the size
-// of the result's own rounding. The state itself must stay an fp32 sum, so w V
+// Roundings below fp32: the result, and P and S where they enter their products, to two
+// bf16 parts, 16 bits each: 2^-16 of every term at most, where the result's own rounding
+// is 2^-8 of itself. (With one part each, 32 x 2K positions of 16 heads of 128 took 301
+// us instead of 367 and 16K of one sequence 118 instead of 129, with an error of the size
+// of the result's own rounding, 0.00235 in the 2-norm instead of 0.00166, and a multiple
+// of it where the two terms cancel.) S's parts take the same place one after the other;
+// shared memory has none for both. The state itself must stay an fp32 sum, so w V
 // is not rounded: three parts hold all 24 bits of it, the products with the
 // bf16 K are exact, and every chunk's KV is accumulated on its own (the tensor
 // core's sums are not rounded to nearest) and added to S in registers.
@@ -21,7 +25,7 @@
 // DV / 4) block of every matrix, one phase after another; one warp issues the
 // MMAs, one the TMA copies. Per chunk c the workers form the first half of w V,
 // the outputs of chunk c - 1, the second half of w V, P, and the state; the MMAs
-// run in the order KV (first half), Q K^T, Q S, KV (second half), P V. Each phase
+// run in the order KV (first half), Q K^T, Q S, KV (second half), Q S (second part), P V. Each phase
 // of the workers then overlaps MMAs that do not need it, and an arrival on
 // w_ready tells the issuer that everything before it in the workers' order is done
 // as well. CTAs are persistent: the copies run ahead into the next task. (Warps
@@ -140,7 +144,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
   constexpr int CW = DV / 4;             // a warp's columns of the state and of the outputs
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];   // v_empty: unless outputs pass through V's tile
-  __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs_done, p_ready, o_done, o_read, o_staged, drained;
+  __shared__ uint64_t w_ready[2], w_free[2], qk_done, kv_done[2], qs0_done, qs_done, p_ready, o_done, o_read, o_staged, drained;
   __shared__ float G[kCh + 1];           // g^0 .. g^128
   __shared__ __align__(16) float GR[32]; // g^31 .. g^0
   __shared__ float GD[63];               // GD[31 + i] = scale g^i, i = 0 .. 31 (masked below)
@@ -170,6 +174,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       bar_init(&kv_done[i], 1);                    // by the CTA's chunk, odd and even
     }
     bar_init(&qk_done, 1);
+    bar_init(&qs0_done, 1);
     bar_init(&qs_done, 1);
     bar_init(&p_ready, kWorkers);
     bar_init(&o_done, 1);
@@ -214,16 +219,22 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       asm volatile("bar.sync 5, %0;" ::"n"(32 * kWorkers) : "memory");
     };
     float st[CW];                                  // S, row `row`, columns col0 ..
-    // S as the B operand of Q S: rows of 64 bf16 columns, 128-byte swizzle.
-    auto publish = [&]() {
+    // S as the B operand of Q S: rows of 64 bf16 columns, 128-byte swizzle. bf16: one of
+    // its two parts, which take the same place one after the other.
+    auto publish = [&](int part) {
       if (OUT && row < DK) {
 #pragma unroll
         for (int e = 0; e < CW; e += 8) {
           const int col = col0 + e, unit = (col & 63) >> 3;
           unsigned char* dst = sop + (col >> 6) * (DK * 128) + row * 128 + ((unit ^ (row & 7)) << 4);
           if constexpr (PARTS == 1) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(st[e], st[e + 1]), pack2(st[e + 2], st[e + 3]),
-                                                        pack2(st[e + 4], st[e + 5]), pack2(st[e + 6], st[e + 7]));
+            uint32_t q[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              q[x] = pack2_finite(st[e + 2 * x], st[e + 2 * x + 1]);
+              if (part == 1) q[x] = pack2(st[e + 2 * x] - lo_f(q[x]), st[e + 2 * x + 1] - hi_f(q[x]));
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
           } else {
             uint32_t q[3][4];
 #pragma unroll
@@ -235,9 +246,9 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         }
       }
     };
-    // Half of w V as three parts, m positions of the chunk in use. The arrival also
-    // hands over S (published before) and releases the tensor memory read before.
-    auto scale = [&](const unsigned char* v, int half, int m) {
+    // Half of w V as three parts, m positions of the chunk in use, then what `also` does.
+    // The arrival also hands over S (published before) and releases the tensor memory read before.
+    auto scale = [&](const unsigned char* v, int half, int m, auto also) {
       constexpr int UNITS = kWHalf * DV / 8 / (32 * kWorkers);   // 16-byte units per thread
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
@@ -265,6 +276,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         *reinterpret_cast<uint4*>(dst + L::kPart) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
         *reinterpret_cast<uint4*>(dst + 2 * L::kPart) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
       }
+      also();
       fence_async();
       fence_before();
       __syncwarp();
@@ -409,7 +421,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         }
       }
       sync();                                      // the tables are there, the stage is free
-      publish();                                   // no Q S of the task before is left: its qs_done was waited for
+      publish(0);                                  // no Q S of the task before is left: its qs_done was waited for
       // S <- g^m S + KV of the task's chunk c, the CTA's chunk j
       auto update = [&](int c, int j) {
         need(&kv_done[j & 1], (j >> 1) & 1);
@@ -442,21 +454,26 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         if constexpr (!OUT) {
           // the products of chunk c - 1 go on while w V of chunk c is formed
           if (it > 0) need(&w_free[0], (it - 1) & 1);
-          scale(v, 0, m);
+          scale(v, 0, m, [] {});
           if (it > 0) need(&w_free[1], (it - 1) & 1);
-          scale(v, 1, m);
+          scale(v, 1, m, [] {});
           if (c > 0) update(c - 1, it - 1);
           continue;
         }
-        scale(v, 0, m);
+        scale(v, 0, m, [] {});
         if (OUT && c > 0) outputs(k, c - 1, it - 1);
         need(&w_free[0], it & 1);
-        scale(v, 1, m);
+        scale(v, 1, m, [&] {
+          if constexpr (OUT && PARTS == 1) {
+            need(&qs0_done, it & 1);               // the product with S's first part
+            publish(1);
+          }
+        });
         if constexpr (OUT) {
           need(&qk_done, it & 1);
           fence_after();
           // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
-          uint32_t out[PARTS][16];
+          [[maybe_unused]] uint32_t out[PARTS][16];    // three parts of the block
 #pragma unroll
           for (int x = 0; x < 32; x += 16) {
             float f[16];
@@ -482,17 +499,23 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
               for (int e = 0; e < 16; ++e) f[e] = 0.f;
             }
+            if constexpr (PARTS == 1) {
+              // two parts of 16 positions, over their own scores (the product takes 16 positions
+              // of P at a time from anywhere), so no warp waits for the others' reads
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              if constexpr (PARTS == 1) out[0][(x + e) / 2] = pack2(f[e], f[e + 1]);
-              else split3(f[e], f[e + 1], out[0][(x + e) / 2], out[PARTS / 2][(x + e) / 2], out[PARTS - 1][(x + e) / 2]);
+              for (int e = 0; e < 8; ++e) {
+                w[e] = pack2_finite(f[2 * e], f[2 * e + 1]);
+                w[8 + e] = pack2(f[2 * e] - lo_f(w[e]), f[2 * e + 1] - hi_f(w[e]));
+              }
+              tmem_st16(lanes + C::p + 32 * grp + x, w);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 2)
+                split3(f[e], f[e + 1], out[0][(x + e) / 2], out[PARTS / 2][(x + e) / 2], out[PARTS - 1][(x + e) / 2]);
             }
           }
-          // one part: over this block's own scores (the product takes 16 columns of P at a
-          // time from anywhere), so no warp waits for the others' reads
-          if constexpr (PARTS == 1) {
-            tmem_st16(lanes + C::p + 32 * grp, out[0]);
-          } else {
+          if constexpr (PARTS == 3) {
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) tmem_st16(lanes + C::p + 64 * part + 16 * grp, out[part]);
           }
@@ -504,7 +527,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         update(c, it);
         if constexpr (OUT) {
           need(&qs_done, it & 1);                  // the state before is not read any more
-          publish();
+          publish(0);
         }
       }
       if (OUT && k.nch > 0) outputs(k, k.nch - 1, it - 1);
@@ -601,8 +624,12 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
                 mma(tmem + C::inter, desc_k(qa + qp * L::kPlaneK + (x / 4) * (kCh * 128) + (x % 4) * 32),
                     desc_mn(sa + sp * L::kStatePart + 16 * x * 128, DK * 128), id_qs, c > 0 || x > 0);
             }
-            commit(&qs_done);
-            commit(&q_empty[sk]);
+            if constexpr (PARTS == 1) {
+              commit(&qs0_done);                   // the other part follows in its place
+            } else {
+              commit(&qs_done);
+              commit(&q_empty[sk]);
+            }
           }
           __syncwarp();
         }
@@ -614,8 +641,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           if constexpr (!OUT) commit(&w_free[1]);
           commit(&kv_done[it & 1]);
           commit(&k_empty[sk]);
-          if constexpr (!OUT) {
-            commit(&v_empty[sv]);
+          if constexpr (!OUT) commit(&v_empty[sv]);
+          if constexpr (OUT && PARTS == 1) {
+#pragma unroll
+            for (int x = 0; x < DK / 16; ++x)
+              mma(tmem + C::inter, desc_k(qa + (x / 4) * (kCh * 128) + (x % 4) * 32), desc_mn(sa + 16 * x * 128, DK * 128), id_qs, 1);
+            commit(&qs_done);
+            commit(&q_empty[sk]);
           }
         }
         __syncwarp();
@@ -625,11 +657,11 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           fence_after();
           if (issuer) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const uint32_t pp = NC > 1 ? kPairA >> 2 * c & 3 : 0, vp = NC > 1 ? kPairB >> 2 * c & 3 : 0;
+            for (int c = 0; c < (PARTS == 3 ? 6 : 2); ++c) {
+              const uint32_t pp = PARTS == 3 ? kPairA >> 2 * c & 3 : 1 - c, vp = PARTS == 3 ? kPairB >> 2 * c & 3 : 0;
 #pragma unroll
               for (int x = 0; x < kCh / 16; ++x)
-                mma_ta(tmem + C::intra, tmem + C::p + (PARTS == 1 ? 32 * (x / 2) + 8 * (x % 2) : 64 * pp + 8 * x), desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
+                mma_ta(tmem + C::intra, tmem + C::p + (PARTS == 1 ? 16 * x + 8 * pp : 64 * pp + 8 * x), desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
                        id_pv, c > 0 || x > 0);
             }
             commit(&o_done);

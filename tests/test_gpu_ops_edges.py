@@ -308,3 +308,32 @@ def test_waits_that_give_up_linear_tiles(fi, wait_limit, n, nin, nout, dtype):  
     y = base[:n * nout].view(n, nout)
     _gives_up_and_recovers(fi, wait_limit, lambda: fi.linear(x, w, y, residual=r, act="silu"), [y])
     assert (base[n * nout:] == 7.0).all()
+
+
+@pytest.mark.parametrize("n,B,H,dk,dv,fused,carried", [(1, 1, 2, 64, 64, False, True), (130, 1, 2, 128, 128, True, True), (700, 2, 2, 64, 128, False, True),
+                                                       (2065, 1, 1, 128, 64, False, True), (900, 2, 3, 96, 40, True, False)])
+@pytest.mark.parametrize("cancel", [False, True])
+def test_prefill_bf16_results_are_rounded_once(fi, n, B, H, dk, dv, fused, carried, cancel):  # noqa: F811
+    # The scores and the state enter their products as two bf16 parts. Each part is off by
+    # at most 2^-8 of what it rounds, so two are by 2^-16 of it, and every term of an output
+    # has one of the two: 2^-16 of the sum of absolute values besides the rounding of
+    # the result, 2^-8 of itself. Over a whole output the roundings are
+    # spread evenly: 2^-8 / sqrt 3 of the 2-norm. With `cancel` the state before takes away
+    # most of what the first positions give.
+    q, k, v, ld, s0 = _la_inputs(n, B, H, dk, dv, "bf16", n + dk, fused)
+    if cancel:
+        ld = torch.full_like(ld, -1e-4)
+        v[1:] *= 0.01                        # the first position's k v^T is most of the state,
+        s0 = -k[0].double()[..., :, None] * v[0].double()[..., None, :]
+        s0 = s0.float() * math.exp(1e-4)     # taken away by what is carried in
+    o, S = torch.empty_like(v), torch.empty_like(s0)
+    fi.linattn_prefill(q, k, v, ld, o, state_in=s0 if carried else None, state_out=S, scale=dk ** -0.5)
+    fi.op_sync()
+    s = _f64(s0) if carried else None
+    want, _ = ops.linattn(_f64(q), _f64(k), _f64(v), _f64(ld), dk ** -0.5, s)
+    A, _ = ops.linattn(np.abs(_f64(q)), np.abs(_f64(k)), np.abs(_f64(v)), _f64(ld), dk ** -0.5, None if s is None else np.abs(s))
+    err = np.abs(_f64(o) - want)
+    tol = U16 * np.abs(want) + (2.0 ** -16 + (n + dk + 16) * U32) * A
+    assert np.all(err <= tol), (err / tol).max()
+    if not cancel and want.size >= 4096:
+        assert np.linalg.norm(err) <= U16 / math.sqrt(3.0) * np.linalg.norm(want)
