@@ -25,10 +25,13 @@ template <int NT, int PARTS>
 constexpr int few_stages() { return (PARTS == 1 ? 98304 : 221184) / few_stage<NT, PARTS>(); }
 template <int NT, int PARTS>
 constexpr size_t few_smem() { return 1024 + (size_t)few_stages<NT, PARTS>() * few_stage<NT, PARTS>(); }
-// fp32: blocks whose products share an accumulator at most (the tensor core's sums are not
-// rounded to nearest; the accumulators are added up afterwards). One where tensor
-// memory has room: 1e-7 off in the 2-norm instead of 6e-7.
-constexpr int kSumBlocks = 2;
+// fp32: every block of the contraction has an accumulator of its own, since the tensor core's
+// sums are not rounded to nearest: 1e-7 off in the 2-norm, with two blocks to an
+// accumulator 6e-7. They are added up in registers: at the end, or in a second round where
+// a CTA's blocks do not fit tensor memory (more rounds would leave the products waiting).
+constexpr int kRounds = 2;
+template <int NT, int PARTS>
+constexpr int few_accs() { return PARTS == 3 ? 512 / NT : 1 << 30; }   // blocks of a round
 
 // Cluster of `split` CTAs: the same 128 rows of W, consecutive parts of the
 // contraction. Each leaves its sums [NT][128] in shared memory; each then adds up
@@ -36,7 +39,7 @@ constexpr int kSumBlocks = 2;
 template <int NT, int PARTS, typename T, int ACT>
 __global__ void __launch_bounds__(kFewThreads)
 k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-             const T* __restrict__ bias, const T* residual, T* y, int split, int cols, int sum_blocks, int vec, int wait_limit) {
+             const T* __restrict__ bias, const T* residual, T* y, int split, int cols, int vec, int wait_limit) {
   constexpr int ST = few_stages<NT, PARTS>(), SB = few_stage<NT, PARTS>(), WB = kBM * 128, XB = NT * 128;
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t full[ST], empty[ST], done;
@@ -86,73 +89,97 @@ k_linear_few(LinShape s, const __grid_constant__ CUtensorMap xmap, const __grid_
     *abort_flag = 1;
     atomicExch(&g_few_error, 1);
   };
-  if (warp == 0) {
-    const bool issuer = elect_one();
-    bool alive = true;
-    int i = ahead;
-    for (; i < b1 - b0; ++i) {
-      alive = warp_wait(&empty[i % ST], (i / ST - 1) & 1, wait_limit, abort_flag);
-      if (!alive) break;
-      if (issuer) load(i);
-      __syncwarp();
-    }
-    if (!alive && lane == 0) give_up();
-    // no copy of this CTA may still be in flight when its memory is reused
-    for (int j = i > ST ? i - ST : 0; j < i; ++j) bar_wait(&full[j % ST], (j / ST) & 1, kDrainLimit);
-  } else if (warp == 1) {
-    const bool issuer = elect_one();
-    constexpr uint32_t id = idesc(kBM, NT);
-    bool alive = true;
-    for (int i = 0; i < b1 - b0; ++i) {
-      const int st = i % ST;
-      alive = warp_wait(&full[st], (i / ST) & 1, wait_limit, abort_flag);
-      if (!alive) break;
-      fence_after();
-      if (issuer) {
-        const uint32_t wa = saddr(ring + st * SB), xa = wa + PARTS * WB;
-        if constexpr (PARTS == 1) {
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) mma(tmem, desc_k(wa + 32 * k), desc_k(xa + 32 * k), id, i > 0 || k > 0);
-        } else {
-          constexpr int pw[6] = {2, 0, 1, 1, 0, 0}, px[6] = {0, 2, 1, 0, 1, 0};   // smallest first
-          const uint32_t d = tmem + i / sum_blocks * NT;
-#pragma unroll
-          for (int p = 0; p < 6; ++p)
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              mma(d, desc_k(wa + pw[p] * WB + 32 * k), desc_k(xa + px[p] * XB + 32 * k), id, i % sum_blocks > 0 || p > 0 || k > 0);
-        }
-        commit(&empty[st]);
-      }
-      __syncwarp();
-    }
-    if (!alive && lane == 0) give_up();
-    if (issuer) commit(&done);
-    __syncwarp();
-  }
-  // all MMAs (and with them all copies) are done: shared memory is free
-  const bool arrived = bar_wait(&done, 0, kDefaultWaitLimit);
-  if (!arrived) give_up();
-  fence_after();
-  __syncthreads();
-  float* part = reinterpret_cast<float*>(ring);           // [NT][128]
+  constexpr int CAP = few_accs<NT, PARTS>();
+  const int total = b1 - b0, rounds = PARTS == 3 ? (total + CAP - 1) / CAP : 1;
   const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16);
+  [[maybe_unused]] float sums[PARTS == 3 ? NT : 1];        // of the rounds
+#pragma unroll
+  for (float& x : sums) x = 0.f;
+  bool alive = true;
+  int i = warp == 0 ? ahead : 0;
+  for (int round = 0; round < rounds; ++round) {
+    const int end = min(total, (PARTS == 3 ? round + 1 : 1) * CAP);
+    if (warp == 0) {
+      const bool issuer = elect_one();
+      for (; alive && i < min(total, end + ST); ++i) {       // what a later round takes is on its way
+        alive = warp_wait(&empty[i % ST], (i / ST - 1) & 1, wait_limit, abort_flag);
+        if (!alive) break;
+        if (issuer) load(i);
+        __syncwarp();
+      }
+      if (!alive && lane == 0) give_up();
+      // no copy of this CTA may still be in flight when its memory is reused
+      if (round == rounds - 1)
+        for (int j = i > ST ? i - ST : 0; j < i; ++j) bar_wait(&full[j % ST], (j / ST) & 1, kDrainLimit);
+    } else if (warp == 1) {
+      const bool issuer = elect_one();
+      constexpr uint32_t id = idesc(kBM, NT);
+      for (; alive && i < end; ++i) {
+        const int st = i % ST;
+        alive = warp_wait(&full[st], (i / ST) & 1, wait_limit, abort_flag);
+        if (!alive) break;
+        fence_after();
+        if (issuer) {
+          const uint32_t wa = saddr(ring + st * SB), xa = wa + PARTS * WB;
+          if constexpr (PARTS == 1) {
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) mma(tmem, desc_k(wa + 32 * k), desc_k(xa + 32 * k), id, i > 0 || k > 0);
+          } else {
+            constexpr int pw[6] = {2, 0, 1, 1, 0, 0}, px[6] = {0, 2, 1, 0, 1, 0};   // smallest first
+            const uint32_t d = tmem + i % CAP * NT;
+#pragma unroll
+            for (int p = 0; p < 6; ++p)
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)
+                mma(d, desc_k(wa + pw[p] * WB + 32 * k), desc_k(xa + px[p] * XB + 32 * k), id, p > 0 || k > 0);
+          }
+          commit(&empty[st]);
+        }
+        __syncwarp();
+      }
+      if (!alive && lane == 0) give_up();
+      if (issuer) commit(&done);
+      __syncwarp();
+    }
+    // all MMAs of the round (after the last: with them all copies) are done: shared memory is free
+    const bool arrived = bar_wait(&done, round & 1, kDefaultWaitLimit);
+    if (!arrived) give_up();
+    __syncwarp();
+    fence_after();
+    __syncthreads();
+    if constexpr (PARTS == 3) {
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        if (c >= s.n) break;
+        for (int g = 0; g < end - round * CAP; ++g) {
+          uint32_t r[16];
+          tmem_ld16(at + g * NT + c, r);
+          ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums[c + e] += __uint_as_float(r[e]);
+        }
+      }
+      if (round < rounds - 1) {              // the next round's products take their place
+        fence_before();
+        __syncthreads();
+        fence_after();
+      }
+    }
+  }
+  float* part = reinterpret_cast<float*>(ring);           // [NT][128]
 #pragma unroll
   for (int c = 0; c < NT; c += 16) {
     if (c >= s.n) break;
-    float sum[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
-    const int sums = PARTS == 1 ? (b1 > b0) : (b1 - b0 + sum_blocks - 1) / sum_blocks;
-    for (int g = 0; g < sums; ++g) {
+    if constexpr (PARTS == 1) {
       uint32_t r[16];
-      tmem_ld16(at + g * NT + c, r);
+      tmem_ld16(at + c, r);
       ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(r[e]);
-    }
+      for (int e = 0; e < 16; ++e) part[(c + e) * kBM + tid] = __uint_as_float(r[e]);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) part[(c + e) * kBM + tid] = sum[e];
+      for (int e = 0; e < 16; ++e) part[(c + e) * kBM + tid] = sums[c + e];
+    }
   }
   if (split > 1) cluster_sync();
   else __syncthreads();
@@ -323,9 +350,8 @@ cudaError_t run_few(const LinCall& c) {
   if (!linear_map(&xmap, c.x, (int64_t)PARTS * s.n, s.K, s.ldx, NT) || !linear_map(&wmap, c.w, (int64_t)PARTS * s.N, s.K, s.ldw, kBM))
     return cudaErrorInvalidValue;
   const int split = few_split(s, c.num_sms), blocks = (s.K + kBK - 1) / kBK;
-  int cols = NT;
-  const int own = (blocks + split - 1) / split, sum_blocks = PARTS == 3 && own * NT <= 512 ? 1 : kSumBlocks;
-  if (PARTS == 3) cols *= (own + sum_blocks - 1) / sum_blocks;
+  const int own = (blocks + split - 1) / split;
+  const int cols = PARTS == 3 ? NT * (own < few_accs<NT, PARTS>() ? own : few_accs<NT, PARTS>()) : NT;
   int alloc = 32;
   while (alloc < cols) alloc *= 2;
   const int vec = s.N % 4 == 0 && (uintptr_t)c.y % 8 == 0 && s.ldy % 4 == 0 &&
@@ -343,7 +369,7 @@ cudaError_t run_few(const LinCall& c) {
   cfg.stream = c.st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, s, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, split, alloc, sum_blocks, vec,
+  return cudaLaunchKernelEx(&cfg, kern, s, xmap, wmap, (const T*)c.bias, (const T*)c.residual, (T*)c.y, split, alloc, vec,
                             op_wait_limit());
 }
 
@@ -387,9 +413,8 @@ cudaError_t run_rows(const LinCall& c) {
 bool linear_few_fits(const LinShape& s, int num_sms) {
   if (s.bf16) return s.n <= kFewRows;
   if (s.n > 64) return false;
-  // an accumulator for every two blocks of a CTA's part of the contraction
   const int blocks = (s.K + kBK - 1) / kBK, split = few_split(s, num_sms), nt = s.n <= 16 ? 16 : s.n <= 32 ? 32 : 64;
-  return ((blocks + split - 1) / split + kSumBlocks - 1) / kSumBlocks * nt <= 512;
+  return (blocks + split - 1) / split <= kRounds * (512 / nt);
 }
 
 cudaError_t launch_linear_few(const LinCall& c) {

@@ -271,7 +271,7 @@ def _gives_up_and_recovers(fi, wait_limit, call, outputs, limits=(0, 1)):  # noq
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("n,nin,nout", [(20, 512, 300), (40, 2048, 2048), (64, 4096, 1000), (16, 8192, 8192), (100, 2048, 200)])
+@pytest.mark.parametrize("n,nin,nout", [(20, 512, 300), (40, 2048, 2048), (64, 4096, 1000), (16, 8192, 8192), (100, 2048, 200), (64, 8192, 512)])
 def test_waits_that_give_up_linear_few_rows(fi, wait_limit, n, nin, nout, dtype):  # noqa: F811
     g = torch.Generator(device="cuda").manual_seed(n)
     x, w = _rand(g, n, nin, dtype=DT[dtype]), _rand(g, nout, nin, dtype=DT[dtype], scale=nin ** -0.5)
@@ -337,3 +337,24 @@ def test_prefill_bf16_results_are_rounded_once(fi, n, B, H, dk, dv, fused, carri
     assert np.all(err <= tol), (err / tol).max()
     if not cancel and want.size >= 4096:
         assert np.linalg.norm(err) <= U16 / math.sqrt(3.0) * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("n,nin,nout", [(10, 512, 300), (16, 16000, 200), (16, 2048, 8192), (30, 8192, 512), (64, 4096, 1000), (64, 4096, 8192),
+                                        (64, 8192, 512), (30, 16000, 512), (9, 30000, 130), (100, 2048, 300), (300, 4096, 512), (600, 700, 600)])
+def test_linear_fp32_error_does_not_grow_with_the_contraction(fi, n, nin, nout):  # noqa: F811
+    # Inside a block of 64 only the products of the first parts, four steps of 16, add to a
+    # sum of full size, each off by at most 2^-23 of it and 2^-24 on average (the tensor
+    # core cuts off), so a block is off by 4 x 2^-24 of itself at most on average; blocks
+    # are added up with rounding, and K / 64 <= 512 roundings of up to 2^-24 of a sum that
+    # grows like a walk are sqrt(512 / 2) x 2^-24 / sqrt 3 on average. The blocks'
+    # errors do not go one way, since blocks have either sign: over sqrt(K / 64) of them
+    # the 2-norm stays at 4 x 2^-24, together with the roundings of the sums below
+    # 4 x 2^-24 + sqrt(K / 128 / 3) 2^-24 and one for the result.
+    g = torch.Generator(device="cuda").manual_seed(nin)
+    x, w = _rand(g, n, nin), _rand(g, nout, nin, scale=nin ** -0.5)
+    y = torch.empty(n, nout, device="cuda")
+    fi.linear(x, w, y)
+    fi.op_sync()
+    want = x.double() @ w.double().T
+    rel = float((y.double() - want).norm() / want.norm())
+    assert rel <= (5 + math.sqrt(nin / 128 / 3)) * U32, rel
