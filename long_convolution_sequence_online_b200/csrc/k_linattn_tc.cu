@@ -89,12 +89,16 @@ struct LaMul {
   int qb, qh, kb, kh, vb, vh;
 };
 
-// TMEM columns: scores, P (over the scores, or three parts beside them), Q S, P V
-// and K^T (w V), the last twice in the launch that forms states only.
+// TMEM columns: scores, with two parts of P over them, fp32's third beside them, Q S, P V
+// and K^T (w V), the last twice in the launch that forms states only. fp32: P V and K^T (w V)
+// have an accumulator for each half of the chunk, 64 columns apart. The tensor core cuts
+// its sums off, so what counts is how many products add to a sum of full size: of the six
+// of parts only the last, four steps of 16 (with one accumulator, 28 of K^T (w V) and 8 of
+// P V: outputs 6.7e-7 off in the 2-norm, now 3e-7, where a plain fp32 form has 2.2e-7).
 template <int PARTS>
 struct LaCols {
-  static constexpr uint32_t scores = 0, p = PARTS == 3 ? 128 : 0, inter = PARTS == 3 ? 320 : 128,
-                            intra = PARTS == 3 ? 384 : 256, kv = PARTS == 3 ? 448 : 384;
+  static constexpr uint32_t scores = 0, p = 0, p2 = 128, inter = PARTS == 3 ? 192 : 128, intra = 256, kv = 384,
+                            half = PARTS == 3 ? 64 : 0, next_kv = PARTS == 3 ? 256 : 128;
 };
 // Which parts a product takes, smallest products first: two bits per product.
 // Three parts on both sides: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0); one against three:
@@ -305,6 +309,13 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         tmem_ld16(lanes + C::inter + col0 + d, r);
         tmem_ld16(lanes + C::intra + col0 + d, q);
         ld_wait();
+        if constexpr (PARTS == 3) {
+          uint32_t q1[16];
+          tmem_ld16(lanes + C::intra + C::half + col0 + d, q1);
+          ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) + __uint_as_float(q1[e]));
+        }
         if (d + 16 >= CW) {                        // all read: the next products may take their place
           fence_before();
           __syncwarp();
@@ -427,12 +438,19 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
         need(&kv_done[j & 1], (j >> 1) & 1);
         fence_after();
         const float gm = G[min(kCh, (int)(k.end - k.t0) - c * kCh)];
-        const uint32_t at = lanes + col0 + (OUT ? C::kv : C::kv - 128 * (j & 1));
+        const uint32_t at = lanes + col0 + (OUT ? C::kv : C::kv - C::next_kv * (j & 1));
 #pragma unroll
         for (int d = 0; d < CW; d += 16) {
           uint32_t r[16];
           tmem_ld16(at + d, r);
           ld_wait();
+          if constexpr (PARTS == 3) {
+            uint32_t r1[16];
+            tmem_ld16(at + C::half + d, r1);
+            ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + __uint_as_float(r1[e]));
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) st[d + e] = fmaf(gm, st[d + e], __uint_as_float(r[e]));
         }
@@ -473,7 +491,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
           need(&qk_done, it & 1);
           fence_after();
           // P block (quarter, grp): below the diagonal g^{i-j} = g^{i-j0-31} g^{j0+31-j}
-          [[maybe_unused]] uint32_t out[PARTS][16];    // three parts of the block
+          [[maybe_unused]] uint32_t p2[16];        // the block's third part
 #pragma unroll
           for (int x = 0; x < 32; x += 16) {
             float f[16];
@@ -499,26 +517,17 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
               for (int e = 0; e < 16; ++e) f[e] = 0.f;
             }
-            if constexpr (PARTS == 1) {
-              // two parts of 16 positions, over their own scores (the product takes 16 positions
-              // of P at a time from anywhere), so no warp waits for the others' reads
-              uint32_t w[16];
+            // two parts of 16 positions, over their own scores (the product takes 16 positions
+            // of P at a time from anywhere), so no warp waits for the others' reads
+            uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                w[e] = pack2_finite(f[2 * e], f[2 * e + 1]);
-                w[8 + e] = pack2(f[2 * e] - lo_f(w[e]), f[2 * e + 1] - hi_f(w[e]));
-              }
-              tmem_st16(lanes + C::p + 32 * grp + x, w);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; e += 2)
-                split3(f[e], f[e + 1], out[0][(x + e) / 2], out[PARTS / 2][(x + e) / 2], out[PARTS - 1][(x + e) / 2]);
+            for (int e = 0; e < 8; ++e) {
+              if constexpr (PARTS == 1) split2(f[2 * e], f[2 * e + 1], w[e], w[8 + e]);
+              else split3(f[2 * e], f[2 * e + 1], w[e], w[8 + e], p2[x / 2 + e]);
             }
+            tmem_st16(lanes + C::p + 32 * grp + x, w);
           }
-          if constexpr (PARTS == 3) {
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part) tmem_st16(lanes + C::p + 64 * part + 16 * grp, out[part]);
-          }
+          if constexpr (PARTS == 3) tmem_st16(lanes + C::p2 + 16 * grp, p2);
           st_wait();
           fence_before();
           __syncwarp();
@@ -568,14 +577,14 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     // K^T (w V) over half of the chunk, smallest parts first; rows 64..127 of a
     // 64-dimensional K repeat the first ones and are not read.
     auto kv_half = [&](uint32_t ka, int half) {
-      const uint32_t d = tmem + (OUT ? C::kv : C::kv - 128 * (it & 1)), w = wa + (L::kHalves > 1 ? half * L::kHalf : 0);
+      const uint32_t d = tmem + C::half * half + (OUT ? C::kv : C::kv - C::next_kv * (it & 1)), w = wa + (L::kHalves > 1 ? half * L::kHalf : 0);
 #pragma unroll
       for (int c = 0; c < (PARTS == 3 ? 6 : 3); ++c) {
         const uint32_t kp = PARTS == 3 ? kPairA >> 2 * c & 3 : 0, wp = (PARTS == 3 ? kPairB : kSingleB) >> 2 * c & 3;
 #pragma unroll
         for (int x = 0; x < kWHalf / 16; ++x)
           mma(d, desc_mn(ka + kp * L::kPlaneK + (half * kWHalf + 16 * x) * 128, DK == 128 ? kCh * 128 : 0),
-              desc_mn(w + wp * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, half > 0 || c > 0 || x > 0);
+              desc_mn(w + wp * L::kPart + 16 * x * 128, kWHalf * 128), id_kv, (PARTS == 1 && half > 0) || c > 0 || x > 0);
       }
     };
     constexpr int NC = PARTS == 3 ? 6 : 1;         // products of parts
@@ -661,8 +670,8 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
               const uint32_t pp = PARTS == 3 ? kPairA >> 2 * c & 3 : 1 - c, vp = PARTS == 3 ? kPairB >> 2 * c & 3 : 0;
 #pragma unroll
               for (int x = 0; x < kCh / 16; ++x)
-                mma_ta(tmem + C::intra, tmem + C::p + (PARTS == 1 ? 16 * x + 8 * pp : 64 * pp + 8 * x), desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128),
-                       id_pv, c > 0 || x > 0);
+                mma_ta(tmem + C::intra + C::half * (x / 4), tmem + (pp == 2 ? C::p2 + 8 * x : C::p + 16 * x + 8 * pp),
+                       desc_mn(va + vp * L::kPlaneV + 16 * x * 128, kCh * 128), id_pv, c > 0 || (PARTS == 3 ? x % 4 : x) > 0);
             }
             commit(&o_done);
             if constexpr (!STAGED) commit(&v_empty[sv]);

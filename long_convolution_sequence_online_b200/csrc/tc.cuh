@@ -252,6 +252,11 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& p0, uint32_t&
   p1 = pack2(a, b);
   p2 = pack2(a - lo_f(p1), b - hi_f(p1));
 }
+// The first two of them: 16 bits.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& p0, uint32_t& p1) {
+  p0 = pack2_finite(a, b);
+  p1 = pack2(a - lo_f(p0), b - hi_f(p0));
+}
 
 }  // namespace tc
 

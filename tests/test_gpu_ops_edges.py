@@ -358,3 +358,43 @@ def test_linear_fp32_error_does_not_grow_with_the_contraction(fi, n, nin, nout):
     want = x.double() @ w.double().T
     rel = float((y.double() - want).norm() / want.norm())
     assert rel <= (5 + math.sqrt(nin / 128 / 3)) * U32, rel
+
+
+def _recurrence64(q, k, v, ld, scale, s0):
+    """The recurrence position by position in float64, on the GPU: o [n][B][H][dv], S."""
+    S = torch.zeros(*q.shape[1:], v.shape[-1], dtype=torch.float64, device="cuda") if s0 is None else s0.double()
+    g = ld.double().clamp(max=0).exp()[:, None, None]
+    o = torch.empty(v.shape, dtype=torch.float64, device="cuda")
+    for t in range(q.shape[0]):
+        S = g * S + k[t].double()[..., :, None] * v[t].double()[..., None, :]
+        o[t] = scale * (q[t].double()[..., None, :] @ S)[..., 0, :]
+    return o, S
+
+
+def _off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,B,H,dk,dv", [(300, 2, 2, 64, 64), (2500, 2, 2, 64, 64), (2065, 1, 3, 100, 128), (700, 3, 2, 33, 47), (8200, 1, 2, 64, 64)])
+def test_prefill_errors_in_the_2_norm(fi, n, B, H, dk, dv, dtype):  # noqa: F811
+    # Of the products of a block of 64 only those of the first parts, four steps of 16,
+    # add to a sum of full size. The tensor core cuts sums off: 2^-24 of them on average, of
+    # sums that grow like a walk, (1 + sqrt 2 + sqrt 3 + 2) / 8 = 0.77 of the last one,
+    # 3.1 x 2^-24 a product, always towards zero. An fp32 output goes through two products, Q K^T
+    # and P V or K^T (w V) and Q S: 6.2; the powers of the decay, exponents of up to a few units
+    # rounded to 2^-24 of themselves, 2; fp32 roundings of P, S and their factors 1.5: together
+    # 9.7 x 2^-24 of its 2-norm. States go through one product: 6.6; bf16 inputs' have
+    # one accumulator for a chunk, 4 steps and 12 at full size, 8 x 2^-24 more.
+    # Losing a third part of an operand would add 1.8e-6 = 30 x 2^-24.
+    q, k, v, ld, s0 = _la_inputs(n, B, H, dk, dv, dtype, 3 * n + dk)
+    o, S = torch.empty_like(v), torch.empty_like(s0)
+    fi.linattn_prefill(q, k, v, ld, o, state_in=s0, state_out=S, scale=dk ** -0.5)
+    fi.op_sync()
+    want_o, want_S = _recurrence64(q, k, v, ld, dk ** -0.5, s0)
+    if dtype == "f32":
+        assert _off(o, want_o) <= 9.7 * U32
+        assert _off(S, want_S) <= 6.6 * U32
+    else:
+        assert _off(o, want_o) <= U16 / math.sqrt(3.0) + 2.0 ** -16
+        assert _off(S, want_S) <= 14.6 * U32
