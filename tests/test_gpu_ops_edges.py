@@ -398,3 +398,75 @@ def test_prefill_errors_in_the_2_norm(fi, n, B, H, dk, dv, dtype):  # noqa: F811
     else:
         assert _off(o, want_o) <= U16 / math.sqrt(3.0) + 2.0 ** -16
         assert _off(S, want_S) <= 14.6 * U32
+
+
+def test_calls_from_several_threads(fi):  # noqa: F811
+    # four threads, a stream and tensors each, call every operator at once, sizes that no call
+    # has had before among them; the results are those of one thread
+    import threading
+
+    def work(i, stream):
+        n = 130 + 64 * i
+        with torch.cuda.stream(stream):
+            q, k, v, ld, s0 = _la_inputs(n, 2, 2, 64, 64, "bf16" if i % 2 else "f32", i)
+            g = torch.Generator(device="cuda").manual_seed(i)
+            w, x = _rand(g, 96 + i, 128, dtype=v.dtype), _rand(g, 20 + i, 128, dtype=v.dtype)
+            outs = []
+            for _ in range(8):
+                o, S = torch.empty_like(v), s0.clone()
+                fi.linattn_prefill(q, k, v, ld, o, state_in=S, state_out=S)
+                o1 = torch.empty_like(o[0])
+                fi.linattn_step(q[0], k[0], v[0], ld, S, o1)
+                y = torch.empty(n * 2, 96 + i, dtype=v.dtype, device="cuda")
+                fi.linear(o.view(n * 2, 128), w, y, act="gelu")
+                y1 = torch.empty(20 + i, 96 + i, dtype=v.dtype, device="cuda")
+                fi.linear(x, w, y1)
+                outs.append((o, S, o1, y, y1))
+            stream.synchronize()
+        return outs
+
+    got, errors = [None] * 4, []
+    gate = threading.Barrier(4)
+
+    def body(i):
+        try:
+            stream = torch.cuda.Stream()
+            gate.wait(60)
+            got[i] = work(i, stream)
+        except Exception as e:     # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors, errors
+    torch.cuda.synchronize()
+    fi.op_sync()
+    for i in range(4):
+        want = work(i, torch.cuda.Stream())[0]
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("n,nin,nout,positive", [(300, 16384, 300, False), (40, 65536, 130, False), (520, 65536, 256, False), (300, 1 << 20, 64, False),
+                                                 (300, 1 << 18, 64, True), (16, 1 << 18, 64, True)])
+def test_linear_bf16_long_contractions(fi, n, nin, nout, positive):  # noqa: F811
+    # Products of 16 add to one accumulator (to 2 to 8, where CTAs share the contraction), each
+    # sum cut off by 2^-24 of itself on average, always towards zero: over K / 16 of
+    # them, of sums that grow like a walk, at most K / 16 x 2/3 x 2^-24 of the result; of
+    # sums that grow evenly (positive values), K / 16 / 2 x 2^-24. That and the rounding of
+    # the result, 2^-8 / sqrt 3 over a whole output.
+    g = torch.Generator(device="cuda").manual_seed(nin)
+    x, w = _rand(g, n, nin, dtype=torch.bfloat16), _rand(g, nout, nin, dtype=torch.bfloat16, scale=nin ** -0.5)
+    if positive:
+        x, w = x.abs(), w.abs()
+    y = torch.empty(n, nout, dtype=torch.bfloat16, device="cuda")
+    fi.linear(x, w, y)
+    fi.op_sync()
+    want = torch.zeros(n, nout, dtype=torch.float64, device="cuda")
+    for c in range(0, nin, 1 << 16):
+        want += x[:, c:c + (1 << 16)].double() @ w[:, c:c + (1 << 16)].double().T
+    cut = nin / 16 * (0.5 if positive else 2 / 3) * U32
+    assert _off(y, want) <= math.hypot(U16 / math.sqrt(3.0), cut)

@@ -98,3 +98,23 @@ def test_a_scale_that_changes_in_place_is_read_anew(fi, stand_in, call):
     scale.fill_(2.0)
     call(fi, 0, scale=scale)
     assert stand_in.calls[0][1].scale == 0.5 and stand_in.calls[-1][1].scale == 2.0
+
+
+def test_more_than_2_to_the_29_rows_or_positions_are_refused(fi):
+    # three parts of as many rows are indexed below 2^31
+    P, need = ctypes.c_void_p(4096), ctypes.c_uint64()
+    la = fi.LinattnConfig(1, 8, 8, 1, fi.FI_F32, 1.0)
+    for name in ("q_stride", "k_stride", "v_stride", "o_stride"):
+        getattr(la, name)[:] = (8, 8, 8)
+    lin = fi.LinearConfig(8, 8, fi.FI_F32, 0, 8, 8, 8, 8)
+    at, al, most = ctypes.addressof(la), ctypes.addressof(lin), 1 << 29
+    assert fi.lib.fi_linattn_prefill(at, most + 1, P, P, P, P, None, None, None, P, None, 0, None) == fi.FI_E_INVALID
+    assert "2^29" in fi.lib.fi_last_error().decode()
+    assert fi.lib.fi_linattn_workspace(at, most + 1, P, P, P, ctypes.byref(need)) == fi.FI_E_INVALID
+    assert "2^29" in fi.lib.fi_last_error().decode()
+    assert fi.lib.fi_linear(al, most + 1, P, P, None, None, P, None, 0, None) == fi.FI_E_INVALID
+    assert "2^29" in fi.lib.fi_last_error().decode()
+    assert fi.lib.fi_linear_workspace(al, most + 1, P, P, ctypes.byref(need)) == fi.FI_E_INVALID
+    assert "2^29" in fi.lib.fi_last_error().decode()
+    assert fi.lib.fi_linear_workspace(al, most, P, P, ctypes.byref(need)) == fi.FI_OK
+    assert need.value == 3 * 8 * 2 * most + 512        # x's parts, and w's in units of 256
