@@ -259,8 +259,9 @@ FI_API fi_status fi_generate_noalloc(const fi_config* cfg, const void* h, int32_
  * for single tokens, and the linear layer. They need no context. Each runs
  * asynchronously on `stream` (NULL = legacy default stream) on the current
  * device, which must be the device of that stream and of every pointer; keeps
- * no memory between calls (scratch, where a call needs some, is the caller's); may be called from several threads and on several
- * streams at once; and may be captured into a CUDA graph. Inputs are in
+ * no memory between calls (scratch, where a call needs some, is the caller's); may
+ * be called from several threads and on several streams at once; and may be
+ * captured into a CUDA graph. Inference only: no gradients. Inputs are in
  * cfg->dtype (FI_F32 or FI_BF16), sums and states in 32 bits. */
 
 /* Wait until every call issued on `stream` has finished. Returns FI_E_TIMEOUT if
@@ -335,7 +336,9 @@ FI_API fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, co
 typedef enum { FI_ACT_NONE = 0, FI_ACT_GELU = 1, FI_ACT_SILU = 2, FI_ACT_RELU = 3, FI_ACT_TANH = 4 } fi_act;
 
 /* y = R(act(x W^T + bias) + residual) over n rows, one rounding at the end.
- * GELU is the exact form u Phi(u), as in fi_set_mlp_block. fp32 products are
+ * GELU is the exact form u Phi(u), as in fi_set_mlp_block. bf16 products are added up
+ * by the tensor cores, which cut the sum off to 24 bits after every 16 of them: up
+ * to in_features x 2^-28 of it besides the rounding. fp32 products are
  * formed from operands split into three bf16 parts (24 bits); an fp32 operand that
  * is not finite makes act's argument not finite in its row (x) or column (w) of y:
  * NaN or an infinity, depending on the sizes. */

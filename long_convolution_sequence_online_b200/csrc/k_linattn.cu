@@ -42,8 +42,9 @@ __device__ __forceinline__ void axpy4(float a, const float4& x, float (&y)[4]) {
 // to the state into slot segment + 1 (segment 0 also copies the state before
 // the prompt into slot 0). OUT = true: the outputs, and the state after the
 // last position.
-template <typename T, int DKP, bool OUT>
+template <int DKP, bool OUT>
 __global__ void __launch_bounds__(kLaThreads) k_linattn(LaShape s, LaPlan p, LaPtrs a) {
+  using T = __nv_bfloat16;
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;                           // [C][DKP]
   float* K = Q + kC * DKP;                 // [C][DKP+4]
@@ -288,25 +289,24 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   }
 }
 
-template <typename T, int DKP>
+template <int DKP>
 cudaError_t prefill(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
   cudaError_t e;
   const dim3 grid((unsigned)(s.B * s.H), (unsigned)((s.dv + kSlice - 1) / kSlice), (unsigned)p.G);
   if (p.G > 1) {
-    if ((e = allow_smem<k_linattn<T, DKP, false>>(la_smem<DKP>())) != cudaSuccess) return e;
-    k_linattn<T, DKP, false><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
+    if ((e = allow_smem<k_linattn<DKP, false>>(la_smem<DKP>())) != cudaSuccess) return e;
+    k_linattn<DKP, false><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = allow_smem<k_linattn<T, DKP, true>>(la_smem<DKP>())) != cudaSuccess) return e;
-  k_linattn<T, DKP, true><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
+  if ((e = allow_smem<k_linattn<DKP, true>>(la_smem<DKP>())) != cudaSuccess) return e;
+  k_linattn<DKP, true><<<grid, kLaThreads, la_smem<DKP>(), st>>>(s, p, a);
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t prefill_dk(const LaShape& s, const LaPlan& p, const LaPtrs& a, cudaStream_t st) {
-  if (s.dk <= 64) return prefill<T, 64>(s, p, a, st);
-  if (s.dk <= 128) return prefill<T, 128>(s, p, a, st);
-  return prefill<T, 256>(s, p, a, st);
+  if (s.dk <= 64) return prefill<64>(s, p, a, st);
+  if (s.dk <= 128) return prefill<128>(s, p, a, st);
+  return prefill<256>(s, p, a, st);
 }
 
 template <typename T, int V>
@@ -368,12 +368,11 @@ cudaError_t launch_linattn_prefill(const LaShape& s, const LaPtrs& ptrs, void* w
     const LaPlan p = linattn_tc_plan(b, num_sms);
     return launch_linattn_tc(s, p, a, (unsigned char*)workspace + la_workspace_bytes(b, p), num_sms, st);
   }
-  return prefill_dk<__nv_bfloat16>(s, la_plan(s, num_sms), a, st);
+  return prefill_dk(s, la_plan(s, num_sms), a, st);
 }
 
 cudaError_t launch_linattn_step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay,
-                                float* state, void* o, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+                                float* state, void* o, cudaStream_t st) {
   return s.bf16 ? step_vec<__nv_bfloat16>(s, q, k, v, log_decay, state, o, st)
                 : step_vec<float>(s, q, k, v, log_decay, state, o, st);
 }

@@ -170,10 +170,7 @@ fi_status fi_linattn_step(const fi_linattn_config* cfg, const void* q, const voi
     return invalid("a pointer is not aligned to its element size");
   if (o == q || o == k || o == v) return invalid("o must not be an input");
   s.n = 1;
-  int sms = 0;
-  cudaError_t e = device_sms(&sms);
-  if (e != cudaSuccess) return cuda_fail(e, "device query");
-  e = launch_linattn_step(s, q, k, v, log_decay, state, o, sms, (cudaStream_t)stream);
+  const cudaError_t e = launch_linattn_step(s, q, k, v, log_decay, state, o, (cudaStream_t)stream);
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "linear attention step launch");
 }
 

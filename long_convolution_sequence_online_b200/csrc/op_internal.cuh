@@ -85,7 +85,7 @@ cudaError_t launch_linattn_tc(const LaShape& s, const LaPlan& p, const LaPtrs& a
 // (synchronises the stream; the flag is cleared).
 cudaError_t linattn_take_error(cudaStream_t st, int* flag);
 cudaError_t launch_linattn_step(const LaShape& s, const void* q, const void* k, const void* v, const float* log_decay,
-                                float* state, void* o, int num_sms, cudaStream_t st);
+                                float* state, void* o, cudaStream_t st);
 
 // The decay's exponent base 2 per position; log_decay above 0 counts as 0, and
 // -infinity becomes a finite value whose powers underflow to 0 (a lag of 0
