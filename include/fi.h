@@ -313,7 +313,7 @@ FI_API fi_status fi_linattn_workspace(const fi_linattn_config* cfg, int32_t n, c
  * state_in:  NULL (zeros) or device fp32 [B][H][key_dim][value_dim], the state
  *            before position 0. state_out: NULL or the same, receives the state
  *            after each sequence's last position (the state before, for an
- *            empty sequence). The two may be the same buffer.
+ *            empty sequence). The two may be the same buffer, but not overlap otherwise.
  * workspace: device, 256-byte aligned, at least fi_linattn_workspace bytes; NULL
  *            when that is 0. Calls that may overlap in time, replays of
  *            captured graphs among them, need a workspace each.
@@ -341,7 +341,8 @@ typedef enum { FI_ACT_NONE = 0, FI_ACT_GELU = 1, FI_ACT_SILU = 2, FI_ACT_RELU = 
  * to in_features x 2^-28 of it besides the rounding. fp32 products are
  * formed from operands split into three bf16 parts (24 bits); an fp32 operand that
  * is not finite makes act's argument not finite in its row (x) or column (w) of y:
- * NaN or an infinity, depending on the sizes. */
+ * NaN or an infinity, depending on the sizes. Parts below 2^-133, of operands below
+ * 2^-110, are lost. */
 typedef struct {
   int32_t in_features;  /* 1..2^20 */
   int32_t out_features; /* 1..2^20 */

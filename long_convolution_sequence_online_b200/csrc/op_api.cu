@@ -146,6 +146,11 @@ fi_status fi_linattn_prefill(const fi_linattn_config* cfg, int32_t n, const void
       !aligned(lengths, 4) || !aligned(state_in, 4) || !aligned(state_out, 4))
     return invalid("a pointer is not aligned to its element size");
   if (n > 0 && (o == q || o == k || o == v)) return invalid("o must not be an input");
+  if (state_in && state_out && state_in != state_out) {
+    // one (sequence, head)'s state would be written before another's is read
+    const uint64_t bytes = (uint64_t)s.B * s.H * s.dk * s.dv * 4, a = (uintptr_t)state_in, b = (uintptr_t)state_out;
+    if ((a < b ? b - a : a - b) < bytes) return invalid("state_in and state_out overlap without being the same");
+  }
   s.n = n;
   int sms = 0;
   cudaError_t e = device_sms(&sms);

@@ -470,3 +470,48 @@ def test_linear_bf16_long_contractions(fi, n, nin, nout, positive):  # noqa: F81
         want += x[:, c:c + (1 << 16)].double() @ w[:, c:c + (1 << 16)].double().T
     cut = nin / 16 * (0.5 if positive else 2 / 3) * U32
     assert _off(y, want) <= math.hypot(U16 / math.sqrt(3.0), cut)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,d", [(100, 64), (2065, 64), (2065, 128), (300, 200)])
+def test_prefill_that_starts_from_a_state_and_keeps_none(fi, n, d, dtype):  # noqa: F811
+    q, k, v, ld, s0 = _la_inputs(n, 1, 2, d, d, dtype, n)
+    o, before = torch.empty_like(v), s0.clone()
+    fi.linattn_prefill(q, k, v, ld, o, state_in=s0, scale=d ** -0.5)
+    fi.op_sync()
+    assert torch.equal(s0, before)
+    _check_la(o, None, q, k, v, ld, d ** -0.5, s0, None, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefill_of_300001_positions(fi, dtype):  # noqa: F811
+    # without decay, outputs are products with running sums. Besides what a shorter prompt has
+    # (9.7 x 2^-24), 37 chunks of a segment and 64 segments are added up with rounding, of sums
+    # that grow like a walk: sqrt(37 / 6) + sqrt(64 / 6).
+    n, H, d = 300001, 2, 8
+    q, k, v, _, _ = _la_inputs(n, 1, H, d, d, dtype, 1)
+    ld = torch.zeros(H, device="cuda")
+    o, S = torch.empty_like(v), torch.empty(1, H, d, d, device="cuda")
+    fi.linattn_prefill(q, k, v, ld, o, state_out=S)
+    fi.op_sync()
+    sums = torch.cumsum(k.double()[..., :, None] * v.double()[..., None, :], dim=0)
+    want = (q.double()[..., None, :] @ sums)[..., 0, :]
+    extra = (math.sqrt(37 / 6) + math.sqrt(64 / 6)) * U32
+    assert _off(o, want) <= (9.7 * U32 + extra if dtype == "f32" else U16 / math.sqrt(3.0) + 2.0 ** -16)
+    assert _off(S, sums[-1]) <= (6.6 if dtype == "f32" else 14.6) * U32 + extra
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nin,nout", [((1 << 21) + 3, 16, 9), (1, 16, 1 << 20), (3, 8, (1 << 20) - 1), (20, 16, 1 << 20), (200, 8, (1 << 20) - 3)])
+def test_linear_of_very_many_rows_or_columns(fi, n, nin, nout, dtype):  # noqa: F811
+    g = torch.Generator(device="cuda").manual_seed(nin)
+    x, w, b = (_rand(g, *s, dtype=DT[dtype]) for s in ((n, nin), (nout, nin), (nout,)))
+    y = torch.empty(n, nout, dtype=DT[dtype], device="cuda")
+    fi.linear(x, w, y, bias=b, act="relu")
+    fi.op_sync()
+    for r in range(0, n, 1 << 20):
+        part = slice(r, min(r + (1 << 20), n))
+        want = (x[part].double() @ w.double().T + b.double()).clamp(min=0)
+        A = x[part].double().abs() @ w.double().abs().T + b.double().abs()
+        tol = (nin + 16) * U32 * A + (U16 if dtype == "bf16" else U32) * want
+        assert ((y[part].double() - want).abs() <= tol).all()

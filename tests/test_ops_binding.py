@@ -118,3 +118,15 @@ def test_more_than_2_to_the_29_rows_or_positions_are_refused(fi):
     assert "2^29" in fi.lib.fi_last_error().decode()
     assert fi.lib.fi_linear_workspace(al, most, P, P, ctypes.byref(need)) == fi.FI_OK
     assert need.value == 3 * 8 * 2 * most + 512        # x's parts, and w's in units of 256
+
+
+def test_states_that_overlap_in_part_are_refused(fi):
+    la = fi.LinattnConfig(2, 8, 4, 3, fi.FI_F32, 1.0)
+    for name, d in (("q_stride", 8), ("k_stride", 8), ("v_stride", 4), ("o_stride", 4)):
+        getattr(la, name)[:] = (6 * d, 2 * d, d)
+    p = [ctypes.c_void_p(1 << (12 + i)) for i in range(5)]
+    at, bytes_ = ctypes.addressof(la), 2 * 3 * 8 * 4 * 4
+    for shift in (4, 128, bytes_ - 4, -4, 4 - bytes_):
+        s_in, s_out = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + shift)
+        assert fi.lib.fi_linattn_prefill(at, 5, p[0], p[1], p[2], p[3], None, s_in, s_out, p[4], None, 0, None) == fi.FI_E_INVALID
+        assert "overlap" in fi.lib.fi_last_error().decode()
