@@ -375,12 +375,14 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
     for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
       const LaTask k = la_task<OUT, PARTS>(s, p, a, i);
       float* ws = a.ws ? a.ws + (size_t)k.slot * p.G * slot : nullptr;
-      const float* s_in = a.state_in ? a.state_in + k.bh * s.state_slot + k.v0 : nullptr;
+      const float ld2 = la_log2_decay(__ldg(a.log_decay + k.h));
+      // an empty sequence passes its state on whatever the decay
+      const bool from_state = a.state_in && (k.len == 0 || !la_drops(ld2));
+      const float* s_in = from_state ? a.state_in + k.bh * s.state_slot + k.v0 : nullptr;
       if (!OUT && k.seg == 0 && s_in)
         for (int r = warp; r < s.dk; r += kWorkers)
           for (int c = lane; c < k.dv; c += 32) ws[r * ws_ld + c] = s_in[(size_t)r * s.state_ld + c];
       if (k.nch == 0 && !(OUT && k.seg == 0 && k.len == 0)) continue;
-      const float ld2 = la_log2_decay(__ldg(a.log_decay + k.h));
       sync();                                      // the task before is done with the tables and the stage
       if (tid <= kCh) G[tid] = la_pow(ld2, tid);
       if (tid >= 160 && tid < 192) GR[tid - 160] = la_pow(ld2, 191 - tid);
@@ -389,7 +391,7 @@ k_linattn_tc(LaShape s, LaPlan p, LaPtrs a, const __grid_constant__ CUtensorMap 
       for (int e = 0; e < CW; ++e) st[e] = 0.f;
       const float* src = !OUT ? nullptr : p.G > 1 ? ws : s_in;
       const int src_ld = p.G > 1 ? ws_ld : s.state_ld;
-      const int g0 = s_in && !(la_drops(ld2) && k.len > 0) ? 0 : 1;   // an empty sequence passes its state on
+      const int g0 = s_in ? 0 : 1;
       constexpr int PER = DV / 8;                  // float4s of half a row of the state
       if (src && g0 <= k.seg) {
         // slot 0: the state before the prompt; slot g: segment g - 1's contribution
