@@ -227,9 +227,10 @@ __global__ void __launch_bounds__(kLaThreads) k_linattn(LaShape s, LaPlan p, LaP
 // its eight warps take the rows in turn (a lane: V consecutive columns) and
 // add up their parts of q^T S at the end.
 // Bound by the state, read and written once: 64 sequences x 16 heads of 128, 134 MB in
-// 23 us (5.9 TB/s, 0.90 of a copy); one sequence is a launch, 2.1 us.
+// 23 us (5.9 TB/s, 0.90 of a copy); one sequence is a launch, 2.2 us. Three CTAs per SM, which
+// 80 registers allow, are needed for it (37 x 9 heads of 56 x 104: 3.6 us, with two 4.5).
 template <typename T, int V>
-__global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __restrict__ q, const T* __restrict__ k,
+__global__ void __launch_bounds__(256, 3) k_linattn_step(LaShape s, const T* __restrict__ q, const T* __restrict__ k,
                                                      const T* __restrict__ v, const float* __restrict__ log_decay,
                                                      float* __restrict__ state, T* __restrict__ o) {
   using vec = typename std::conditional<V == 4, float4, typename std::conditional<V == 2, float2, float>::type>::type;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
   const int c = (blockIdx.y * 32 + lane) * V;
   const bool in = c < s.dv;
   const float ld2 = la_log2_decay(__ldg(log_decay + h)), g = la_pow(ld2, 1);
-  const bool drops = la_drops(ld2);
+  const uint32_t keep = la_drops(ld2) ? 0u : ~0u;    // of the state before
   if (tid < s.dk) {
     qs[tid] = op_load(q + b * s.qs[1] + h * s.qs[2] + tid);
     ks[tid] = op_load(k + b * s.ks[1] + h * s.ks[2] + tid);
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(256) k_linattn_step(LaShape s, const T* __rest
         *reinterpret_cast<vec*>(f) = x[u];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          f[e] = fmaf(ks[d], vv[e], drops ? 0.f : g * f[e]);
+          f[e] = fmaf(ks[d], vv[e], g * __uint_as_float(__float_as_uint(f[e]) & keep));
           acc[e] = fmaf(qs[d], f[e], acc[e]);
         }
         __stcs(reinterpret_cast<vec*>(sp + (size_t)d * s.dv), *reinterpret_cast<const vec*>(f));
