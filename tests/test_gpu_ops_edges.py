@@ -515,3 +515,22 @@ def test_linear_of_very_many_rows_or_columns(fi, n, nin, nout, dtype):  # noqa: 
         A = x[part].double().abs() @ w.double().abs().T + b.double().abs()
         tol = (nin + 16) * U32 * A + (U16 if dtype == "bf16" else U32) * want
         assert ((y[part].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_gelu_fp32_is_accurate_everywhere(fi, n):  # noqa: F811
+    # relative to the result: the fit 1.9e-8, its 9 steps and the reciprocal (times 3.8 at
+    # most, the fit's slope) 8 roundings, the exponential 3, products and the difference 4, and
+    # 1.25 u^2 of them for the exponent: (16 + 1.5 u^2) 2^-24, one more for x w
+    u = torch.cat([torch.linspace(-9, 9, 4001), torch.logspace(-30, 0, 301), -torch.logspace(-30, 0, 301), torch.tensor([0.0, -0.0, 20.0, 3e38])]).cuda()
+    w = torch.zeros(u.numel(), 16, device="cuda")
+    w[:, 2] = u
+    x = torch.zeros(n, 16, device="cuda")
+    x[:, 2] = 1.0
+    y = torch.empty(n, u.numel(), device="cuda")
+    fi.linear(x, w, y, act="gelu")
+    fi.op_sync()
+    u64 = _f64(u)
+    want = u64 * np.array([0.5 * math.erfc(-t / math.sqrt(2.0)) for t in u64])
+    err = np.abs(_f64(y) - want)
+    assert np.all(err <= (17 + 1.5 * np.minimum(u64 * u64, 81)) * U32 * np.abs(want))
