@@ -9,7 +9,7 @@
 //
 // The chunked form here takes the shapes whose tiles do not fit the tensor cores' kernel
 // (k_linattn_tc.cu): bf16 above 128 dimensions. Bound by shared-memory reads of its 4 x 4
-// outer products with one CTA per SM: 4 x 2048 positions, 8 heads of 256 1.6 ms (12 TFLOP/s).
+// outer products with one CTA per SM: 4 x 2048 positions, 8 heads of 256 1.5 ms (12 TFLOP/s).
 #include "op_internal.cuh"
 
 namespace fi {

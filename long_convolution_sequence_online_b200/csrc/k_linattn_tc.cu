@@ -12,8 +12,8 @@
 //     o      = scale g^{i+1} inter + intra
 // Roundings below fp32: the result, and P and S where they enter their products, to two
 // bf16 parts, 16 bits each: 2^-16 of every term at most, where the result's own rounding
-// is 2^-8 of itself. (With one part each, 32 x 2K positions of 16 heads of 128 took 301
-// us instead of 367 and 16K of one sequence 118 instead of 129, with an error of the size
+// is 2^-8 of itself. (With one part each, 32 x 2K positions of 16 heads of 128 took 300
+// us instead of 357 and 16K of one sequence 113 instead of 125, with an error of the size
 // of the result's own rounding, 0.00235 in the 2-norm instead of 0.00166, and a multiple
 // of it where the two terms cancel.) S's parts take the same place one after the other;
 // shared memory has none for both. The state itself must stay an fp32 sum, so w V
@@ -34,17 +34,17 @@
 // warps do not hide their own latency, and more code at a time misses the
 // instruction cache.)
 //
-// Bound: the workers' instruction latency, at 48 % of the issue slots and 37 % of the
-// tensor pipe: 4.3 us a chunk at 128 x 128 with all SMs at work. 16 heads of 128, bf16: one
-// sequence of 16K 112 us (states 40, outputs 72; 2.4 TB/s), 32 of 2K 288 us (3.9 TB/s, 1000 W).
-// fp32, 12 heads of 64, 8K: 106 us (layout 27, states 26, outputs 55), waiting on
-// products and single-buffered tiles.
+// Bound: the workers' instruction latency, at 51 % of the issue slots and 42 % of the
+// tensor pipe: 5.8 us a chunk at 128 x 128 with all SMs at work (16 chunks with the CTA's
+// start). 16 heads of 128, bf16: one sequence of 16K 125 us (states 40, outputs 85; 2.2
+// TB/s), 32 of 2K 353 to 362 us (3.1 TB/s). fp32, 12 heads of 64, 8K: 108 us (layout 27,
+// states 26, outputs 56), waiting on products and single-buffered tiles.
 //
 // fp32 inputs come as three bf16 parts each and every product as six products of parts;
 // their tiles fit up to 64 dimensions. Above, blocks of 64 value dimensions are tasks of
 // their own, and blocks of key dimensions launches of their own, of which the later
 // ones add to the outputs (q . k is the sum over them). Scores are formed once per
-// block: 4 x 2048 positions, 16 heads of 128, 0.49 ms; in fp32 arithmetic (k_linattn.cu) 0.97.
+// block: 4 x 2048 positions, 16 heads of 128, 0.51 ms; in fp32 arithmetic (k_linattn.cu) 0.97.
 #include <type_traits>
 
 #include "op_internal.cuh"

@@ -14,8 +14,8 @@
 //
 // Bound: the tensor pipe. 16384 x 2048 -> 8192 bf16 + GELU 439 to 460 us (1.2 PFLOP/s
 // under the power cap, where the library's product alone takes 400 to 415), 8192 x 2048 ->
-// 2048 49 us (46); fp32 8192 x 768 -> 768 + GELU 59 us, 10 of them laying out (192 tiles
-// are 2.6 rounds of the pairs), 4096 x 2048 -> 2048 170 us. Small products are bound by
+// 2048 49 us (46); fp32 8192 x 768 -> 768 + GELU 57 us, 10 of them laying out (192 tiles
+// are 2.6 rounds of the pairs), 4096 x 2048 -> 2048 170 to 175 us. Small products are bound by
 // latency, 6 to 7 us up to a contraction of 1000.
 //
 // Operands come by TMA, which wants bf16 rows that start at 16-byte boundaries.
