@@ -263,7 +263,8 @@ def generate_noalloc(h, batch: int, n: int, x0, eps, y_out, dtype: str = "f32", 
                                    _stream(stream)), "fi_generate_noalloc")
 
 
-# -- operators (no context): linear attention and the linear layer
+# -- operators (no context): linear attention and the linear layer; inference only, autograd does
+# not see what they write
 #
 # What a call's tensors look like (shapes, strides, types, devices) is checked once
 # per combination and kept with the configuration it gives; of the tensors' addresses
